@@ -315,6 +315,63 @@ kq_status kq_w4a4_linear_t(int32_t fmt,
                            const void* mu, const void* wbar,
                            void* Y, hipStream_t stream);
 
+/* ---- The 8-bit path: for the layers that 4 bits are too few for, and for the norm and the
+ * gated feed-forward block around them.  Values are E4M3 (OCP; 1 sign, 4 exponent, 3 mantissa
+ * bits, largest 448) with one E8M0 scale for every 128 consecutive values of a row:
+ *   codes  u8 [rows][K]                    E4M3
+ *   scales u8 [rows][kq_fp8_scale_cols(K)] byte e + 127 of each group, zero bytes behind the
+ *                                          last group (a row is 4 ceil(K / 512) bytes)
+ * K is a multiple of 16; the last group of a row may be short.  A group's e is the smallest
+ * with max|y| <= 448 2^e (at least -127), its codes are y 2^-e rounded to nearest even; a
+ * group of zeros has byte 0.  A group that holds an infinity or a NaN has byte 255 and code
+ * 0x7F throughout (both NaN), and makes NaN every product that uses it.
+ * Weights are [N][K] ([out][in]) and are quantized by the same call as activations; scales
+ * given for blocks of 128 x 128 are the special case in which 128 rows repeat the same bytes.
+ * 16-bit inputs and outputs are fp16 or bf16 (KQ_DT_*), sums are float32.  M <= 2^30; N and
+ * K <= 2^20, F <= 2^19, all multiples of 16.  Pointers 16-byte aligned, scales 4, workspaces
+ * 256.  Outputs must not overlap inputs or each other, except where a call says so.  The
+ * current device must be the one that the stream and the pointers belong to. */
+enum { KQ_DT_F16 = 0, KQ_DT_BF16 = 1 };
+enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1, KQ_ACT_GELU_TANH = 2 };
+
+/* Bytes of a row of scales, 4 ceil(K / 512); 0 for a K outside 1 .. 2^20. */
+int64_t kq_fp8_scale_cols(int64_t K);
+
+/* codes, scales of X [M][K] (activations with no norm before them, and weights offline). */
+kq_status kq_quantize_fp8(int32_t dtype, const void* X, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales,
+                          hipStream_t stream);
+
+/* Residual addition, root-mean-square norm and quantization in one pass:
+ *   h = X + residual (float32; h = X if residual is NULL),
+ *   residual_out = h rounded to the dtype (written only if residual is given),
+ *   codes, scales of y = h / sqrt(mean_k h^2 + eps) * gamma.
+ * y is formed from the float32 h, not from its rounded copy.  All 16-bit arrays have the one
+ * dtype: X, residual, residual_out [M][K], gamma [K].  residual_out may be residual itself.
+ * K <= 16384 (a row stays in registers); eps finite and >= 0 (else KQ_ERR_VALUE).  Squares are
+ * summed in float32: a bf16 row with values beyond about 1e18 overflows the sum and gives zeros. */
+kq_status kq_rmsnorm_quantize_fp8(int32_t dtype, const void* X, const void* residual, const void* gamma, float eps,
+                                  int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, void* residual_out,
+                                  hipStream_t stream);
+
+/* Y = Xq Wq^T (+ bias): Y [M][N] and bias [N] (or NULL) in the dtype, float32 accumulation.
+ * workspace: at least kq_fp8_linear_workspace_bytes(M, N, K) bytes (0: none needed), which
+ * holds partial sums when few rows are split over K; they are added in a fixed order.  Calls
+ * that share a workspace must not overlap (captured graphs that hold it included). */
+size_t kq_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+kq_status kq_fp8_linear(int32_t dtype, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+                        const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const void* bias, void* Y,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The first half of a gated feed-forward block: codes, scales ([M][F]) of
+ *   act(Xq Wg^T) * (Xq Wu^T),   wcodes [2 F][K]: the F rows of Wg, then the F rows of Wu.
+ * act: SiLU g / (1 + exp -g); GELU g Phi(g); its tanh form.  Both projections, the activation
+ * and the product stay in float32; the result is rounded once, to E4M3.  kq_fp8_linear with
+ * the down-projection's weights takes codes and scales as they are.  workspace as above. */
+size_t kq_fp8_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K);
+kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+                              const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,
+                              uint8_t* scales, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,6 +13,12 @@ library is missing: there is no fallback.
     T = kq.lowrank_down(X, L1)
     Y = kq.w4a4_linear_t(codes, scales, wcodes, wscales, T=T, L2=L2, mu=mu, wbar=wbar)
 
+    # the 8-bit path: a gated feed-forward block behind its norm
+    wc, ws = kq.quantize_fp8(W)                                 # offline, W [N][K]
+    codes, scales, h = kq.rmsnorm_quantize_fp8(X, gamma, residual=h)
+    codes, scales = kq.fp8_gated_linear(codes, scales, gate_up_codes, gate_up_scales, act="silu")
+    X = kq.fp8_linear(codes, scales, down_codes, down_scales, dtype=X.dtype)
+
 Outputs and workspaces that the binding allocates itself are marked as used on the stream
 the call runs on (``record_stream``), so torch's allocator does not hand their memory to
 another stream's work before the call has finished there.
@@ -25,7 +31,9 @@ __all__ = ["mfma_fp4_probe", "load", "lib_path", "abi_version", "status_str", "l
            "transform_quantize", "fold_inverse_into_weights", "fold_inverse_into_weights_nk",
            "w4a4_linear", "w4a4_linear_t", "w4a4_linear_workspace_bytes",
            "lowrank_down", "lowrank_down_workspace_bytes", "transform_quantize_lowrank",
-           "svd_lowrank", "svd_lowrank_workspace_bytes", "KQError"]
+           "svd_lowrank", "svd_lowrank_workspace_bytes", "fp8_scale_cols", "quantize_fp8", "rmsnorm_quantize_fp8",
+           "fp8_linear", "fp8_linear_workspace_bytes", "fp8_gated_linear", "fp8_gated_linear_workspace_bytes",
+           "KQError"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -33,6 +41,8 @@ _LIB = None
 KQ_OK = 0
 XFORM_NONE, XFORM_KRON, XFORM_RPBH, XFORM_DENSE, XFORM_KRON_BLOCKS = 0, 1, 2, 3, 4
 FMT_MXFP4, FMT_LM4, FMT_LM2 = 0, 1, 2
+DT_F16, DT_BF16 = 0, 1
+_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _FMT = {"mxfp4": FMT_MXFP4, "lm4": FMT_LM4, "lm2": FMT_LM2}
 
 
@@ -99,6 +109,20 @@ def load():
     lib.kq_w4a4_linear_noalloc.argtypes = [i32, vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, i32, vp, vp, vp, vp]
     lib.kq_w4a4_linear_t.restype = i32
     lib.kq_w4a4_linear_t.argtypes = [i32, vp, vp, i64, i64, vp, vp, i64, vp, vp, i32, vp, vp, vp, vp]
+    lib.kq_fp8_scale_cols.restype = i64
+    lib.kq_fp8_scale_cols.argtypes = [i64]
+    lib.kq_quantize_fp8.restype = i32
+    lib.kq_quantize_fp8.argtypes = [i32, vp, i64, i64, vp, vp, vp]
+    lib.kq_rmsnorm_quantize_fp8.restype = i32
+    lib.kq_rmsnorm_quantize_fp8.argtypes = [i32, vp, vp, vp, ctypes.c_float, i64, i64, vp, vp, vp, vp]
+    lib.kq_fp8_linear_workspace_bytes.restype = sz
+    lib.kq_fp8_linear_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.kq_fp8_linear.restype = i32
+    lib.kq_fp8_linear.argtypes = [i32, vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, sz, vp]
+    lib.kq_fp8_gated_linear_workspace_bytes.restype = sz
+    lib.kq_fp8_gated_linear_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.kq_fp8_gated_linear.restype = i32
+    lib.kq_fp8_gated_linear.argtypes = [i32, vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, sz, vp]
     _LIB = lib
     return lib
 
@@ -573,3 +597,191 @@ def w4a4_linear_t(xcodes, xscales, wcodes, wscales, T=None, L2=None, mu=None, wb
     if s != KQ_OK:
         raise KQError(s, "kq_w4a4_linear_t")
     return Y
+
+
+# ------------------------------------------------------------------------- the 8-bit path
+
+def _matrix(t, name):
+    if not isinstance(t, _torch().Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D torch.Tensor")
+    return t.shape
+
+
+def _dtype16(dtype, name):
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return DT_BF16
+    if dtype == torch.float16:
+        return DT_F16
+    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16 (got {dtype})")
+
+
+def _call(name, device, stream, tensors, made, args):
+    """One library call on `stream` (default: the current stream of the tensors' device, which
+    is made the current device for the call if it is not)."""
+    torch = _torch()
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: tensors on {device} and {t.device}")
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    else:
+        if stream.device != device:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
+        raw = stream.cuda_stream
+        if stream != torch.cuda.current_stream(device):
+            for t in made:
+                if t is not None:
+                    t.record_stream(stream)
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == device.index:
+        s = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            s = fn(*args, raw)
+    if s != KQ_OK:
+        raise KQError(s, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def fp8_scale_cols(K):
+    """Scale bytes of a row of K values: one per 128, padded to a multiple of four."""
+    return (K + 511) // 512 * 4
+
+
+def _fp8_out(rows, K, codes, scales, device, made):
+    torch = _torch()
+    if codes is None:
+        codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device)
+        made.append(codes)
+    else:
+        _check(codes, "codes", torch.float8_e4m3fn, (rows, K))
+    if scales is None:
+        scales = torch.empty((rows, fp8_scale_cols(K)), dtype=torch.uint8, device=device)
+        made.append(scales)
+    else:
+        _check(scales, "scales", torch.uint8, (rows, fp8_scale_cols(K)))
+    return codes, scales
+
+
+def quantize_fp8(X, codes=None, scales=None, stream=None):
+    """E4M3 codes (float8_e4m3fn [M][K]) and E8M0 scale bytes (uint8 [M][fp8_scale_cols(K)],
+    one per 128 values) of X (fp16 or bf16 [M][K], K a multiple of 16).  Also for weights
+    [N][K], offline."""
+    M, K = _matrix(X, "X")
+    dt = _dtype16(X.dtype, "X")
+    _check(X, "X", X.dtype)
+    made = []
+    codes, scales = _fp8_out(M, K, codes, scales, X.device, made)
+    _call("kq_quantize_fp8", X.device, stream, (codes, scales), made,
+          (dt, _addr(X), M, K, _addr(codes), _addr(scales)))
+    return codes, scales
+
+
+def rmsnorm_quantize_fp8(X, gamma, eps=1e-6, residual=None, codes=None, scales=None, residual_out=None, stream=None):
+    """h = X + residual; codes and scales (as quantize_fp8) of h / sqrt(mean h^2 + eps) * gamma.
+    X, residual fp16 or bf16 [M][K], gamma [K] of the same dtype, K <= 16384.  Returns (codes,
+    scales, h rounded to the dtype); the last is None without a residual.  residual_out may be
+    residual itself (updated in place)."""
+    M, K = _matrix(X, "X")
+    dt = _dtype16(X.dtype, "X")
+    _check(X, "X", X.dtype)
+    _check(gamma, "gamma", X.dtype, (K,))
+    torch = _torch()
+    made = []
+    if residual is not None:
+        _check(residual, "residual", X.dtype, (M, K))
+        if residual_out is None:
+            residual_out = torch.empty_like(X)
+            made.append(residual_out)
+        else:
+            _check(residual_out, "residual_out", X.dtype, (M, K))
+    else:
+        residual_out = None
+    codes, scales = _fp8_out(M, K, codes, scales, X.device, made)
+    _call("kq_rmsnorm_quantize_fp8", X.device, stream, (gamma, residual, residual_out, codes, scales), made,
+          (dt, _addr(X), _addr(residual), _addr(gamma), float(eps), M, K, _addr(codes), _addr(scales),
+           _addr(residual_out)))
+    return codes, scales, residual_out
+
+
+def _fp8_operands(xcodes, xscales, wcodes, wscales):
+    f8, u8 = _torch().float8_e4m3fn, _torch().uint8
+    M, K = _matrix(xcodes, "xcodes")
+    N = _matrix(wcodes, "wcodes")[0]
+    _check(xcodes, "xcodes", f8)
+    _check(wcodes, "wcodes", f8, (N, K))
+    _check(xscales, "xscales", u8, (M, fp8_scale_cols(K)))
+    _check(wscales, "wscales", u8, (N, fp8_scale_cols(K)))
+    return M, N, K
+
+
+def _fp8_workspace(workspace, need, device, made):
+    torch = _torch()
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+    elif need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+        made.append(workspace)
+    return workspace, (0 if workspace is None else workspace.numel())
+
+
+def fp8_linear_workspace_bytes(M, N, K):
+    """Workspace bytes kq_fp8_linear needs (0: none)."""
+    return load().kq_fp8_linear_workspace_bytes(M, N, K)
+
+
+def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, workspace=None, stream=None):
+    """Y = Xq Wq^T (+ bias), fp16 or bf16 [M][N], float32 accumulation.  xcodes [M][K] and
+    wcodes [N][K] float8_e4m3fn with their scale bytes (quantize_fp8); N a multiple of 16; bias
+    [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16).  workspace: a
+    uint8 device tensor of fp8_linear_workspace_bytes(M, N, K) bytes (256-byte aligned); by
+    default one is taken from torch's allocator."""
+    torch = _torch()
+    M, N, K = _fp8_operands(xcodes, xscales, wcodes, wscales)
+    if dtype is None:
+        dtype = Y.dtype if Y is not None else bias.dtype if bias is not None else torch.float16
+    dt = _dtype16(dtype, "dtype")
+    device = xcodes.device
+    if bias is not None:
+        _check(bias, "bias", dtype, (N,))
+    made = []
+    if Y is None:
+        Y = torch.empty((M, N), dtype=dtype, device=device)
+        made.append(Y)
+    else:
+        _check(Y, "Y", dtype, (M, N))
+    workspace, nb = _fp8_workspace(workspace, fp8_linear_workspace_bytes(M, N, K), device, made)
+    _call("kq_fp8_linear", device, stream, (xscales, wcodes, wscales, bias, Y, workspace), made,
+          (dt, _addr(xcodes), _addr(xscales), M, K, _addr(wcodes), _addr(wscales), N, _addr(bias), _addr(Y),
+           _addr(workspace), nb))
+    return Y
+
+
+def fp8_gated_linear_workspace_bytes(M, F, K):
+    """Workspace bytes kq_fp8_gated_linear needs (0: none)."""
+    return load().kq_fp8_gated_linear_workspace_bytes(M, F, K)
+
+
+def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, scales=None, workspace=None,
+                     stream=None):
+    """codes and scales (as quantize_fp8, [M][F]) of act(Xq Wg^T) * (Xq Wu^T).  wcodes [2 F][K]
+    holds the F rows of Wg, then the F rows of Wu; F a multiple of 16.  act: 'silu', 'gelu' or
+    'gelu_tanh'.  The result feeds fp8_linear with the down-projection's weights."""
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
+    M, N, K = _fp8_operands(xcodes, xscales, wcodes, wscales)
+    if N % 2:
+        raise ValueError("wcodes must hold as many gate rows as up rows")
+    F = N // 2
+    device = xcodes.device
+    made = []
+    codes, scales = _fp8_out(M, F, codes, scales, device, made)
+    workspace, nb = _fp8_workspace(workspace, fp8_gated_linear_workspace_bytes(M, F, K), device, made)
+    _call("kq_fp8_gated_linear", device, stream, (xscales, wcodes, wscales, codes, scales, workspace), made,
+          (_ACT[act], _addr(xcodes), _addr(xscales), M, K, _addr(wcodes), _addr(wscales), F, _addr(codes),
+           _addr(scales), _addr(workspace), nb))
+    return codes, scales
