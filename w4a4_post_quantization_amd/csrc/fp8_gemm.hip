@@ -23,60 +23,156 @@ __device__ __forceinline__ float f8_act(float g) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
 }
 
-// 64 x 64 output tile, 2 x 2 wavefronts of 32 x 32, operands straight from global memory.
-template <int ACT, bool BF16>   // ACT -1: the linear
-__global__ __launch_bounds__(256) void f8_simple_kernel(const uint8_t* __restrict__ wcodes,
-                                                        const uint8_t* __restrict__ wscales,
-                                                        const uint8_t* __restrict__ xcodes,
-                                                        const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
-                                                        const uint16_t* __restrict__ bias, void* __restrict__ out) {
-  constexpr bool GATED = ACT >= 0;
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  const int l32 = lane & 31, h = lane >> 5;
-  const int SC = (int)f8_scale_cols(K);
-  const int n0 = blockIdx.x * 64 + (wid & 1) * 32;
-  const int64_t m0 = (int64_t)blockIdx.y * 64 + (wid >> 1) * 32;
-  const int n = n0 + l32;
-  const int64_t m = m0 + l32;
-  v16f acc[GATED ? 2 : 1];
+// ---------------------------------------------------------------------------------
+// Few tokens (up to 16 MT): the weights' bytes bound it.  A workgroup takes 16 weight rows
+// (gated: 16 gate rows and the 16 up rows of the same columns) and all tokens; its NW
+// wavefronts take the 128-wide groups of k in turn, U groups of loads in flight each, and
+// their sums are added through LDS in wavefront order.  The codes are widened to bf16 with
+// their scale applied (exact: four significant bits) and multiplied by the bf16 matrix
+// instruction, which sums in float32: there is time for it under the loads, and it does not
+// drop bits as the 8-bit instruction does.  Lane l holds row l % 16 and, of each group, bytes
+// 16 (l / 16) .. + 15 of both 64-byte halves, the same for both operands.
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+
+// Eight of the sixteen codes in a piece (p = 0, 1), widened and scaled.
+template <int P>
+__device__ __forceinline__ v8b f8_widen8(const v4i& w, float scale) {
+  const uint32_t lo = (uint32_t)w[2 * P], hi = (uint32_t)w[2 * P + 1];
+  const v2b a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const v2b b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const v2b c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const v2b d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return v8b{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <int ACT, bool BF16, int MT, int NW, int U>   // ACT -1: the linear
+__global__ __launch_bounds__(64 * NW) void f8_rows_kernel(const uint8_t* __restrict__ wcodes,
+                                                          const uint8_t* __restrict__ wscales,
+                                                          const uint8_t* __restrict__ xcodes,
+                                                          const uint8_t* __restrict__ xscales, int M, int N, int K,
+                                                          const uint16_t* __restrict__ bias, void* __restrict__ out) {
+  constexpr int RT = ACT >= 0 ? 2 : 1;
+  __shared__ v4f part[NW][RT * MT][64];
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int SC = (int)f8_scale_cols(K), T = (K + 127) / 128;
+  const int n0 = 16 * blockIdx.x;
+  __amdgpu_buffer_rsrc_t rw[RT], rws[RT];
 #pragma unroll
-  for (int t = 0; t < (GATED ? 2 : 1); ++t)
+  for (int i = 0; i < RT; ++i) {
+    rw[i] = make_rsrc(wcodes + (int64_t)(n0 + i * N) * K, 16LL * K);
+    rws[i] = make_rsrc(wscales + (int64_t)(n0 + i * N) * SC, 16LL * SC);
+  }
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xcodes, (int64_t)M * K), rxs = make_rsrc(xscales, (int64_t)M * SC);
+  v4f acc[RT][MT];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
-  auto load = [&](const uint8_t* row, bool live, int k) {
-    v4i lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-    if (live && k < K) lo = *reinterpret_cast<const v4i*>(row + k);
-    if (live && k + 16 < K) hi = *reinterpret_cast<const v4i*>(row + k + 16);
-    return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  };
-  for (int k0 = 0; k0 < K; k0 += 64) {
-    const int k = k0 + 32 * h, g = k0 >> 7;
-    const v8i b = load(xcodes + m * K, m < M, k);
-    const int sb = m < M ? xscales[m * SC + g] : 0;
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int t = 0; t < (GATED ? 2 : 1); ++t) {
-      const int64_t r = n + (int64_t)t * N;
-      const v8i a = load(wcodes + r * K, n < N, k);
-      const int sa = n < N ? wscales[r * SC + g] : 0;
-      acc[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[t], 0, 0, 0, sa, 0, sb);
+    for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  for (int t0 = wid; t0 < T; t0 += NW * U) {
+    v4i w[U][RT][2], x[U][MT][2];
+    uint32_t ws[U][RT], xs[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * NW;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int k = 128 * t + 64 * p + 16 * q;
+        const bool live = k < K;                               // K is a multiple of 16
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          w[u][i][p] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rw[i], live ? r * K + k : KQ_OOB, 0, 0));
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          x[u][j][p] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, live ? (16 * j + r) * K + k : KQ_OOB, 0, 0));
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) ws[u][i] = __builtin_amdgcn_raw_buffer_load_b8(rws[i], t < T ? r * SC + t : KQ_OOB, 0, 0);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) xs[u][j] = __builtin_amdgcn_raw_buffer_load_b8(rxs, t < T ? (16 * j + r) * SC + t : KQ_OOB, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);                         // all loads out before the first product
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v8b wb[RT][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const float s = __uint_as_float(ws[u][i] << 23);
+        wb[i][0] = f8_widen8<0>(w[u][i][0], s);
+        wb[i][1] = f8_widen8<1>(w[u][i][0], s);
+        wb[i][2] = f8_widen8<0>(w[u][i][1], s);
+        wb[i][3] = f8_widen8<1>(w[u][i][1], s);
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const float s = __uint_as_float(xs[u][j] << 23);
+        const v8b xb[4] = {f8_widen8<0>(x[u][j][0], s), f8_widen8<1>(x[u][j][0], s), f8_widen8<0>(x[u][j][1], s),
+                           f8_widen8<1>(x[u][j][1], s)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[i][c], xb[c], acc[i][j], 0, 0, 0);
+      }
     }
   }
-  if (m >= M) return;
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const int col = n0 + 8 * (q >> 2) + 4 * h + (q & 3);
-    if (col >= N) continue;
-    float v = acc[0][q];
-    if (GATED) {
-      static_cast<float*>(out)[m * N + col] = f8_act<ACT>(v) * acc[GATED ? 1 : 0][q];
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[wid][i * MT + j][lane] = acc[i][j];
+  __syncthreads();
+  // wavefront j sums and stores tokens 16 j .. + 15: lane l holds columns 4 (l / 16) .. + 3 of token l % 16
+  for (int j = wid; j < MT; j += NW) {
+    v4f s[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      s[i] = part[0][i * MT + j][lane];
+#pragma unroll
+      for (int v = 1; v < NW; ++v) s[i] += part[v][i * MT + j][lane];
+    }
+    const int m = 16 * j + r, col = n0 + 4 * q;
+    if (m >= M) continue;
+    if constexpr (ACT >= 0) {
+      v4f y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = f8_act<ACT>(s[0][e]) * s[RT - 1][e];
+      *reinterpret_cast<v4f*>(static_cast<float*>(out) + (int64_t)m * N + col) = y;
     } else {
-      if (bias) v += unpack1_16<BF16>(bias[col]);
-      static_cast<uint16_t*>(out)[m * N + col] = (uint16_t)pack2_16<BF16>(v, 0.0f);
+      if (bias) {
+        const uint2 b = *reinterpret_cast<const uint2*>(bias + col);
+        s[0][0] += unpack1_16<BF16>((uint16_t)(b.x & 0xFFFFu));
+        s[0][1] += unpack1_16<BF16>((uint16_t)(b.x >> 16));
+        s[0][2] += unpack1_16<BF16>((uint16_t)(b.y & 0xFFFFu));
+        s[0][3] += unpack1_16<BF16>((uint16_t)(b.y >> 16));
+      }
+      uint2 o;
+      o.x = pack2_16<BF16>(s[0][0], s[0][1]);
+      o.y = pack2_16<BF16>(s[0][2], s[0][3]);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + (int64_t)m * N + col) = o;
     }
   }
 }
 
-static dim3 simple_grid(int64_t M, int64_t N) { return dim3((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64)); }
+template <int ACT, bool BF16>
+static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+                              const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
+                              void* out, hipStream_t s) {
+  const dim3 g((unsigned)(N / 16));
+#define KQ_ROWS(MT, NW, U)                                                                                          \
+  hipLaunchKernelGGL((f8_rows_kernel<ACT, BF16, MT, NW, U>), g, dim3(64 * NW), 0, s, wcodes, wscales, xcodes, xscales, \
+                     (int)M, (int)N, (int)K, bias, out)
+  if (M <= 16) {
+    if (K <= 4096) KQ_ROWS(1, 8, 4);
+    else KQ_ROWS(1, 16, 4);
+  } else if (M <= 32) {
+    KQ_ROWS(2, 8, 2);
+  } else {
+    KQ_ROWS(4, 8, 2);
+  }
+#undef KQ_ROWS
+  return hipGetLastError();
+}
 
 // ---------------------------------------------------------------------------------
 // Many tokens: tiles of 256 weight rows by 64 TM token rows on four wavefronts (2 x 2), each
@@ -393,9 +489,7 @@ static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, i
                                 const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
                                 uint8_t* Y, hipStream_t s) {
   if (M > 64) return gemm_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
-  hipLaunchKernelGGL((f8_simple_kernel<-1, BF16>), simple_grid(M, N), dim3(256), 0, s, wcodes, wscales, xcodes,
-                     xscales, M, (int)N, (int)K, bias, Y);
-  return hipGetLastError();
+  return rows_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
 }
 
 hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
@@ -414,9 +508,7 @@ static hipError_t gated_launch(const uint8_t* xcodes, const uint8_t* xscales, in
                                const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,
                                uint8_t* scales, void* workspace, hipStream_t s) {
   if (M > 64) return gemm_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
-  hipLaunchKernelGGL((f8_simple_kernel<ACT, false>), simple_grid(M, F), dim3(256), 0, s, wcodes, wscales, xcodes,
-                     xscales, M, (int)F, (int)K, nullptr, workspace);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = rows_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, workspace, s);
   if (e != hipSuccess) return e;
   return launch_f8_quantize_f32(static_cast<const float*>(workspace), M, F, codes, scales, s);
 }
