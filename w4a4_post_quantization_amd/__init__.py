@@ -600,6 +600,8 @@ def w4a4_linear_t(xcodes, xscales, wcodes, wscales, T=None, L2=None, mu=None, wb
 
 
 # ------------------------------------------------------------------------- the 8-bit path
+# One-token calls take 2 to 14 us on the GPU, so the host side is kept short: one combined test
+# per tensor (the named refusal is worked out only when it fails) and one library call.
 
 def _matrix(t, name):
     if not isinstance(t, _torch().Tensor) or t.dim() != 2:
@@ -607,44 +609,46 @@ def _matrix(t, name):
     return t.shape
 
 
-def _dtype16(dtype, name):
-    torch = _torch()
-    if dtype == torch.bfloat16:
+def _dtype16(torch, dtype, name):
+    if dtype is torch.bfloat16:
         return DT_BF16
-    if dtype == torch.float16:
+    if dtype is torch.float16:
         return DT_F16
     raise ValueError(f"{name} must be torch.float16 or torch.bfloat16 (got {dtype})")
 
 
-def _call(name, device, stream, tensors, made, args):
-    """One library call on `stream` (default: the current stream of the tensors' device, which
-    is made the current device for the call if it is not)."""
+def _same(t, name, dtype, shape, index):
+    """t: a contiguous tensor of the dtype and shape on GPU `index`; its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the first tensor on GPU {index}")
+
+
+def _call(name, index, stream, made, args):
+    """One library call on `stream` (default: the current stream of the tensors' GPU, which is
+    made the current device for the call if it is not)."""
     torch = _torch()
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: tensors on {device} and {t.device}")
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(index)
     else:
-        if stream.device != device:
-            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on GPU {index}")
         raw = stream.cuda_stream
-        if stream != torch.cuda.current_stream(device):
+        if stream != torch.cuda.current_stream(index):
             for t in made:
-                if t is not None:
-                    t.record_stream(stream)
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == device.index:
+                t.record_stream(stream)
+    fn = getattr(_LIB or load(), name)
+    if torch.cuda.current_device() == index:
         s = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             s = fn(*args, raw)
     if s != KQ_OK:
         raise KQError(s, name)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def fp8_scale_cols(K):
@@ -652,32 +656,29 @@ def fp8_scale_cols(K):
     return (K + 511) // 512 * 4
 
 
-def _fp8_out(rows, K, codes, scales, device, made):
-    torch = _torch()
+def _fp8_out(torch, rows, K, codes, scales, device, made):
+    index, cols = device.index, (K + 511) // 512 * 4
     if codes is None:
         codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device)
         made.append(codes)
-    else:
-        _check(codes, "codes", torch.float8_e4m3fn, (rows, K))
     if scales is None:
-        scales = torch.empty((rows, fp8_scale_cols(K)), dtype=torch.uint8, device=device)
+        scales = torch.empty((rows, cols), dtype=torch.uint8, device=device)
         made.append(scales)
-    else:
-        _check(scales, "scales", torch.uint8, (rows, fp8_scale_cols(K)))
-    return codes, scales
+    return (codes, scales, _same(codes, "codes", torch.float8_e4m3fn, (rows, K), index),
+            _same(scales, "scales", torch.uint8, (rows, cols), index))
 
 
 def quantize_fp8(X, codes=None, scales=None, stream=None):
     """E4M3 codes (float8_e4m3fn [M][K]) and E8M0 scale bytes (uint8 [M][fp8_scale_cols(K)],
     one per 128 values) of X (fp16 or bf16 [M][K], K a multiple of 16).  Also for weights
     [N][K], offline."""
+    torch = _torch()
     M, K = _matrix(X, "X")
-    dt = _dtype16(X.dtype, "X")
-    _check(X, "X", X.dtype)
-    made = []
-    codes, scales = _fp8_out(M, K, codes, scales, X.device, made)
-    _call("kq_quantize_fp8", X.device, stream, (codes, scales), made,
-          (dt, _addr(X), M, K, _addr(codes), _addr(scales)))
+    dt = _dtype16(torch, X.dtype, "X")
+    device, made = X.device, []
+    x = _same(X, "X", X.dtype, X.shape, device.index if X.is_cuda else -1)
+    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, device, made)
+    _call("kq_quantize_fp8", device.index, stream, made, (dt, x, M, K, c, s))
     return codes, scales
 
 
@@ -686,47 +687,43 @@ def rmsnorm_quantize_fp8(X, gamma, eps=1e-6, residual=None, codes=None, scales=N
     X, residual fp16 or bf16 [M][K], gamma [K] of the same dtype, K <= 16384.  Returns (codes,
     scales, h rounded to the dtype); the last is None without a residual.  residual_out may be
     residual itself (updated in place)."""
-    M, K = _matrix(X, "X")
-    dt = _dtype16(X.dtype, "X")
-    _check(X, "X", X.dtype)
-    _check(gamma, "gamma", X.dtype, (K,))
     torch = _torch()
-    made = []
+    M, K = _matrix(X, "X")
+    dtype, device, made = X.dtype, X.device, []
+    dt = _dtype16(torch, dtype, "X")
+    index = device.index if X.is_cuda else -1
+    x = _same(X, "X", dtype, X.shape, index)
+    g = _same(gamma, "gamma", dtype, (K,), index)
+    r = o = None
     if residual is not None:
-        _check(residual, "residual", X.dtype, (M, K))
+        r = _same(residual, "residual", dtype, (M, K), index)
         if residual_out is None:
             residual_out = torch.empty_like(X)
             made.append(residual_out)
-        else:
-            _check(residual_out, "residual_out", X.dtype, (M, K))
+        o = _same(residual_out, "residual_out", dtype, (M, K), index)
     else:
         residual_out = None
-    codes, scales = _fp8_out(M, K, codes, scales, X.device, made)
-    _call("kq_rmsnorm_quantize_fp8", X.device, stream, (gamma, residual, residual_out, codes, scales), made,
-          (dt, _addr(X), _addr(residual), _addr(gamma), float(eps), M, K, _addr(codes), _addr(scales),
-           _addr(residual_out)))
+    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, device, made)
+    _call("kq_rmsnorm_quantize_fp8", index, stream, made, (dt, x, r, g, eps, M, K, c, s, o))
     return codes, scales, residual_out
 
 
-def _fp8_operands(xcodes, xscales, wcodes, wscales):
-    f8, u8 = _torch().float8_e4m3fn, _torch().uint8
+def _fp8_operands(torch, xcodes, xscales, wcodes, wscales):
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
     M, K = _matrix(xcodes, "xcodes")
     N = _matrix(wcodes, "wcodes")[0]
-    _check(xcodes, "xcodes", f8)
-    _check(wcodes, "wcodes", f8, (N, K))
-    _check(xscales, "xscales", u8, (M, fp8_scale_cols(K)))
-    _check(wscales, "wscales", u8, (N, fp8_scale_cols(K)))
-    return M, N, K
+    index, cols = xcodes.device.index if xcodes.is_cuda else -1, (K + 511) // 512 * 4
+    return M, N, K, (_same(xcodes, "xcodes", f8, (M, K), index), _same(xscales, "xscales", u8, (M, cols), index)), \
+        (_same(wcodes, "wcodes", f8, (N, K), index), _same(wscales, "wscales", u8, (N, cols), index))
 
 
-def _fp8_workspace(workspace, need, device, made):
-    torch = _torch()
-    if workspace is not None:
-        _check(workspace, "workspace", torch.uint8)
-    elif need:
+def _fp8_workspace(torch, workspace, need, device, made):
+    if workspace is None:
+        if not need:
+            return None, 0
         workspace = torch.empty((need,), dtype=torch.uint8, device=device)
         made.append(workspace)
-    return workspace, (0 if workspace is None else workspace.numel())
+    return _same(workspace, "workspace", torch.uint8, workspace.shape, device.index), workspace.numel()
 
 
 def fp8_linear_workspace_bytes(M, N, K):
@@ -741,23 +738,18 @@ def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, 
     uint8 device tensor of fp8_linear_workspace_bytes(M, N, K) bytes (256-byte aligned); by
     default one is taken from torch's allocator."""
     torch = _torch()
-    M, N, K = _fp8_operands(xcodes, xscales, wcodes, wscales)
+    M, N, K, x, w = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if dtype is None:
         dtype = Y.dtype if Y is not None else bias.dtype if bias is not None else torch.float16
-    dt = _dtype16(dtype, "dtype")
-    device = xcodes.device
-    if bias is not None:
-        _check(bias, "bias", dtype, (N,))
-    made = []
+    dt = _dtype16(torch, dtype, "dtype")
+    device, made = xcodes.device, []
+    b = None if bias is None else _same(bias, "bias", dtype, (N,), device.index)
     if Y is None:
         Y = torch.empty((M, N), dtype=dtype, device=device)
         made.append(Y)
-    else:
-        _check(Y, "Y", dtype, (M, N))
-    workspace, nb = _fp8_workspace(workspace, fp8_linear_workspace_bytes(M, N, K), device, made)
-    _call("kq_fp8_linear", device, stream, (xscales, wcodes, wscales, bias, Y, workspace), made,
-          (dt, _addr(xcodes), _addr(xscales), M, K, _addr(wcodes), _addr(wscales), N, _addr(bias), _addr(Y),
-           _addr(workspace), nb))
+    y = _same(Y, "Y", dtype, (M, N), device.index)
+    wk, nb = _fp8_workspace(torch, workspace, fp8_linear_workspace_bytes(M, N, K), device, made)
+    _call("kq_fp8_linear", device.index, stream, made, (dt, *x, M, K, *w, N, b, y, wk, nb))
     return Y
 
 
@@ -771,17 +763,15 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
     """codes and scales (as quantize_fp8, [M][F]) of act(Xq Wg^T) * (Xq Wu^T).  wcodes [2 F][K]
     holds the F rows of Wg, then the F rows of Wu; F a multiple of 16.  act: 'silu', 'gelu' or
     'gelu_tanh'.  The result feeds fp8_linear with the down-projection's weights."""
+    torch = _torch()
     if act not in _ACT:
         raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
-    M, N, K = _fp8_operands(xcodes, xscales, wcodes, wscales)
+    M, N, K, x, w = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if N % 2:
         raise ValueError("wcodes must hold as many gate rows as up rows")
     F = N // 2
-    device = xcodes.device
-    made = []
-    codes, scales = _fp8_out(M, F, codes, scales, device, made)
-    workspace, nb = _fp8_workspace(workspace, fp8_gated_linear_workspace_bytes(M, F, K), device, made)
-    _call("kq_fp8_gated_linear", device, stream, (xscales, wcodes, wscales, codes, scales, workspace), made,
-          (_ACT[act], _addr(xcodes), _addr(xscales), M, K, _addr(wcodes), _addr(wscales), F, _addr(codes),
-           _addr(scales), _addr(workspace), nb))
+    device, made = xcodes.device, []
+    codes, scales, c, s = _fp8_out(torch, M, F, codes, scales, device, made)
+    wk, nb = _fp8_workspace(torch, workspace, fp8_gated_linear_workspace_bytes(M, F, K), device, made)
+    _call("kq_fp8_gated_linear", device.index, stream, made, (_ACT[act], *x, M, K, *w, F, c, s, wk, nb))
     return codes, scales

@@ -24,18 +24,25 @@ __device__ __forceinline__ float f8_act(float g) {
 }
 
 // ---------------------------------------------------------------------------------
-// Few tokens (up to 16 MT): the weights' bytes bound it.  A workgroup takes 16 weight rows
+// Few tokens (up to 16 MT): the weights' bytes bound it.  A workgroup takes 16 RT weight rows
 // (gated: 16 gate rows and the 16 up rows of the same columns) and all tokens; its NW
-// wavefronts take the 128-wide groups of k in turn, U groups of loads in flight each, and
-// their sums are added through LDS in wavefront order.  The codes are widened to bf16 with
-// their scale applied (exact: four significant bits) and multiplied by the bf16 matrix
-// instruction, which sums in float32: there is time for it under the loads, and it does not
-// drop bits as the 8-bit instruction does.  Lane l holds row l % 16 and, of each group, bytes
-// 16 (l / 16) .. + 15 of both 64-byte halves, the same for both operands.
+// wavefronts take the 128-wide groups of k in turn and their sums are added through LDS in
+// wavefront order.  Each wavefront streams its groups through a ring of S slots of its own in
+// LDS, so the loop has no barrier: 8 rows x 128 bytes a load, whole cache lines.  (Loading the
+// fragments straight into registers puts a different row in every lane; the address unit then
+// takes one lane a cycle, 64 cycles instead of 16 a load, which bound it: 4096 x 11008 by one
+// token 10.3 us, 6144 x 4096 by 64 tokens 28.8 us.)  A row's eight 16-byte chunks are
+// XOR-swizzled by the row; lane l holds row l % 16 and chunks l / 16 and 4 + l / 16 of it, the
+// same k for both operands.  Scale bytes of 128 groups (16384 k) at a time are staged for all.
+// WIDE: the codes are widened to bf16 with their scale applied (exact: four significant bits)
+// and multiplied by the bf16 matrix instruction, which sums in float32.  The 8-bit instruction
+// keeps about 14 bits below the largest of each four products (relative error of a sum 2e-5 to
+// 5e-5 measured, a hundredth of bf16's rounding); for up to 16 tokens there is time under the
+// loads to do without that.
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
-// Eight of the sixteen codes in a piece (p = 0, 1), widened and scaled.
+// Eight of the sixteen codes in a piece (P = 0, 1), widened and scaled.
 template <int P>
 __device__ __forceinline__ v8b f8_widen8(const v4i& w, float scale) {
   const uint32_t lo = (uint32_t)w[2 * P], hi = (uint32_t)w[2 * P + 1];
@@ -46,97 +53,135 @@ __device__ __forceinline__ v8b f8_widen8(const v4i& w, float scale) {
   return v8b{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-template <int ACT, bool BF16, int MT, int NW, int U>   // ACT -1: the linear
+template <int ACT, bool BF16, int RT, int MT, int NW, int S>   // ACT -1: the linear
 __global__ __launch_bounds__(64 * NW) void f8_rows_kernel(const uint8_t* __restrict__ wcodes,
                                                           const uint8_t* __restrict__ wscales,
                                                           const uint8_t* __restrict__ xcodes,
                                                           const uint8_t* __restrict__ xscales, int M, int N, int K,
                                                           const uint16_t* __restrict__ bias, void* __restrict__ out) {
-  constexpr int RT = ACT >= 0 ? 2 : 1;
-  __shared__ v4f part[NW][RT * MT][64];
+  constexpr bool GATED = ACT >= 0, WIDE = MT == 1;
+  constexpr int NF = RT + MT;                                  // 16-row fragments of a group: RT weight, MT token
+  constexpr int SLOT = 2048 * NF, RING = NW * S * SLOT, SCALES = 2048 * NF, PART = NW * RT * MT * 1024;
+  static_assert(!GATED || RT == 2, "gate and up");
+  __shared__ __align__(16) uint8_t lds[(RING > PART ? RING : PART) + SCALES];
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int SC = (int)f8_scale_cols(K), T = (K + 127) / 128;
-  const int n0 = 16 * blockIdx.x;
-  __amdgpu_buffer_rsrc_t rw[RT], rws[RT];
+  const int n0 = 16 * (GATED ? 1 : RT) * blockIdx.x;
+  v4i rc[NF], rs[NF];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    rw[i] = make_rsrc(wcodes + (int64_t)(n0 + i * N) * K, 16LL * K);
-    rws[i] = make_rsrc(wscales + (int64_t)(n0 + i * N) * SC, 16LL * SC);
+  for (int f = 0; f < NF; ++f) {
+    const int64_t row = f < RT ? n0 + (int64_t)f * (GATED ? N : 16) : 16 * (f - RT);
+    const int64_t rows = f < RT ? (GATED ? 16 : min(16, N - n0 - 16 * f)) : min(16, M - 16 * (f - RT));
+    rc[f] = rsrc_words((f < RT ? wcodes : xcodes) + row * K, rows * K);
+    rs[f] = rsrc_words((f < RT ? wscales : xscales) + row * SC, rows * SC);
   }
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xcodes, (int64_t)M * K), rxs = make_rsrc(xscales, (int64_t)M * SC);
+  const uint32_t lds0 = lds_addr(lds), ring0 = lds0 + wid * S * SLOT;
+  const int lr = lane >> 3, lc = 16 * ((lane & 7) ^ lr);       // a load's row (+ 8) and chunk of this lane
+  auto load = [&](int slot, int t) {                           // group t (past the last: zeros)
+    const int k = 128 * t + lc;
+    const uint32_t off = t < T && k < K ? lr * K + k : KQ_OOB;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) lds_load16(rc[f], ring0 + slot * SLOT + 2048 * f + 1024 * p, (int)(off + 8 * p * K));
+  };
+  const int sw = r & 7, c0 = 128 * r + 16 * (q ^ sw), c1 = 128 * r + 16 * ((4 + q) ^ sw);
   v4f acc[RT][MT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  for (int t0 = wid; t0 < T; t0 += NW * U) {
-    v4i w[U][RT][2], x[U][MT][2];
-    uint32_t ws[U][RT], xs[U][MT];
+  constexpr int SC_OFF = RING > PART ? RING : PART;
+  int slot = 0, t = wid;
+  for (int t1 = 0; t1 < T; t1 += 128) {                        // 16384 k: one round for all but the longest
+    __syncthreads();
+    for (int f = wid; f < 2 * NF; f += NW) {                   // 8 rows of scale bytes a load
+      const uint32_t at = lr * SC + t1 + lc;
+      v4i src = rs[0];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = t0 + u * NW;
+      for (int e = 1; e < NF; ++e) src = f / 2 == e ? rs[e] : src;
+      lds_load16(src, lds0 + SC_OFF + 1024 * f, (int)(at + 8 * (f & 1) * SC));
+    }
+    if (t1 == 0) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int k = 128 * t + 64 * p + 16 * q;
-        const bool live = k < K;                               // K is a multiple of 16
+      for (int u = 0; u < S; ++u) load(u, t + u * NW);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(S * 2 * NF));      // the scales
+    } else {
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    }
+    lds_barrier();
+    const int t2 = min(T, t1 + 128);
+    for (; t < t2; t += NW) {
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm((S - 1) * 2 * NF));
+      asm volatile("" ::: "memory");
+      const uint8_t* const st = lds + wid * S * SLOT + slot * SLOT;
+      const int ts = t - t1;
+      const uint8_t* const sc = lds + SC_OFF + 128 * r + 16 * ((ts >> 4) ^ sw) + (ts & 15);
+      v4i lo[NF], hi[NF];
+      int s[NF];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          w[u][i][p] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rw[i], live ? r * K + k : KQ_OOB, 0, 0));
+      for (int f = 0; f < NF; ++f) {
+        lo[f] = *reinterpret_cast<const v4i*>(st + 2048 * f + c0);
+        hi[f] = *reinterpret_cast<const v4i*>(st + 2048 * f + c1);
+        s[f] = sc[2048 * f];
+      }
+      // the slot is free once its fragments are in registers
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      load(slot, t + S * NW);
+      __builtin_amdgcn_sched_barrier(0);
+      slot = slot + 1 == S ? 0 : slot + 1;
+      if constexpr (WIDE) {
+        v8b xb[4];
+        const float sx = __uint_as_float((uint32_t)s[RT] << 23);
+        xb[0] = f8_widen8<0>(lo[RT], sx);
+        xb[1] = f8_widen8<1>(lo[RT], sx);
+        xb[2] = f8_widen8<0>(hi[RT], sx);
+        xb[3] = f8_widen8<1>(hi[RT], sx);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float w = __uint_as_float((uint32_t)s[i] << 23);
+          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<0>(lo[i], w), xb[0], acc[i][0], 0, 0, 0);
+          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<1>(lo[i], w), xb[1], acc[i][0], 0, 0, 0);
+          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<0>(hi[i], w), xb[2], acc[i][0], 0, 0, 0);
+          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<1>(hi[i], w), xb[3], acc[i][0], 0, 0, 0);
+        }
+      } else {
+        auto join = [&](int f) { return v8i{lo[f].x, lo[f].y, lo[f].z, lo[f].w, hi[f].x, hi[f].y, hi[f].z, hi[f].w}; };
 #pragma unroll
         for (int j = 0; j < MT; ++j)
-          x[u][j][p] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, live ? (16 * j + r) * K + k : KQ_OOB, 0, 0));
-      }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) ws[u][i] = __builtin_amdgcn_raw_buffer_load_b8(rws[i], t < T ? r * SC + t : KQ_OOB, 0, 0);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) xs[u][j] = __builtin_amdgcn_raw_buffer_load_b8(rxs, t < T ? (16 * j + r) * SC + t : KQ_OOB, 0, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);                         // all loads out before the first product
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      v8b wb[RT][4];
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const float s = __uint_as_float(ws[u][i] << 23);
-        wb[i][0] = f8_widen8<0>(w[u][i][0], s);
-        wb[i][1] = f8_widen8<1>(w[u][i][0], s);
-        wb[i][2] = f8_widen8<0>(w[u][i][1], s);
-        wb[i][3] = f8_widen8<1>(w[u][i][1], s);
-      }
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const float s = __uint_as_float(xs[u][j] << 23);
-        const v8b xb[4] = {f8_widen8<0>(x[u][j][0], s), f8_widen8<1>(x[u][j][0], s), f8_widen8<0>(x[u][j][1], s),
-                           f8_widen8<1>(x[u][j][1], s)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < RT; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[i][c], xb[c], acc[i][j], 0, 0, 0);
+          for (int i = 0; i < RT; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(i), join(RT + j), acc[i][j], 0, 0, 0, s[i], 0, s[RT + j]);
       }
     }
   }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));                   // the last refills, before the ring is reused
+  __syncthreads();
+  v4f* const part = reinterpret_cast<v4f*>(lds);               // [NW][RT MT][64]
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) part[wid][i * MT + j][lane] = acc[i][j];
+    for (int j = 0; j < MT; ++j) part[(wid * RT * MT + i * MT + j) * 64 + lane] = acc[i][j];
   __syncthreads();
-  // wavefront j sums and stores tokens 16 j .. + 15: lane l holds columns 4 (l / 16) .. + 3 of token l % 16
-  for (int j = wid; j < MT; j += NW) {
-    v4f s[RT];
+  // 16 tokens (gated) or 16 x 16 outputs a wavefront at a time: lane l holds columns
+  // 4 (l / 16) .. + 3 of token l % 16
+  for (int f = wid; f < (GATED ? MT : RT * MT); f += NW) {
+    v4f s[2];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      s[i] = part[0][i * MT + j][lane];
+    for (int i = 0; i < (GATED ? 2 : 1); ++i) {
+      s[i] = part[(i * MT + f) * 64 + lane];
 #pragma unroll
-      for (int v = 1; v < NW; ++v) s[i] += part[v][i * MT + j][lane];
+      for (int v = 1; v < NW; ++v) s[i] += part[(v * RT * MT + i * MT + f) * 64 + lane];
     }
-    const int m = 16 * j + r, col = n0 + 4 * q;
-    if (m >= M) continue;
-    if constexpr (ACT >= 0) {
+    const int m = 16 * (f % MT) + r, col = n0 + 16 * (GATED ? 0 : f / MT) + 4 * q;
+    if (m >= M || col >= N) continue;
+    if constexpr (GATED) {
       v4f y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = f8_act<ACT>(s[0][e]) * s[RT - 1][e];
+      for (int e = 0; e < 4; ++e) y[e] = f8_act<ACT>(s[0][e]) * s[1][e];
       *reinterpret_cast<v4f*>(static_cast<float*>(out) + (int64_t)m * N + col) = y;
     } else {
       if (bias) {
@@ -154,132 +199,164 @@ __global__ __launch_bounds__(64 * NW) void f8_rows_kernel(const uint8_t* __restr
   }
 }
 
+template <int ACT, bool BF16, int RT, int MT, int NW, int S>
+static hipError_t rows_go(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K, const uint8_t* wcodes,
+                          const uint8_t* wscales, int64_t N, const uint16_t* bias, void* out, hipStream_t s) {
+  const int64_t per = ACT >= 0 ? 16 : 16 * RT;
+  hipLaunchKernelGGL((f8_rows_kernel<ACT, BF16, RT, MT, NW, S>), dim3((unsigned)((N + per - 1) / per)), dim3(64 * NW), 0,
+                     s, wcodes, wscales, xcodes, xscales, (int)M, (int)N, (int)K, bias, out);
+  return hipGetLastError();
+}
+
+// Tokens the rows kernel takes; above, tiles.  Measured (us): linear 6144 x 4096, 64 tokens 9.8
+// against 11.7 in tiles, 128 tokens 13.1 against 12.3; gated 11008 x 4096, 32 tokens 27.6 against
+// 33.3, 64 tokens 30.5 against 31.2 (a second launch and 2.8 MB of float32 between them).
+constexpr int64_t ROWS_LINEAR = 64, ROWS_GATED = 32;
+
 template <int ACT, bool BF16>
 static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                               const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
                               void* out, hipStream_t s) {
-  const dim3 g((unsigned)(N / 16));
-#define KQ_ROWS(MT, NW, U)                                                                                          \
-  hipLaunchKernelGGL((f8_rows_kernel<ACT, BF16, MT, NW, U>), g, dim3(64 * NW), 0, s, wcodes, wscales, xcodes, xscales, \
-                     (int)M, (int)N, (int)K, bias, out)
-  if (M <= 16) {
-    if (K <= 4096) KQ_ROWS(1, 8, 4);
-    else KQ_ROWS(1, 16, 4);
-  } else if (M <= 32) {
-    KQ_ROWS(2, 8, 2);
+#define KQ_ROWS(RT, MT, NW, S) \
+  rows_go<ACT, BF16, RT, MT, NW, S>(xcodes, xscales, M, K, wcodes, wscales, N, bias, out, s)
+  if constexpr (ACT >= 0) {
+    return M <= 16 ? KQ_ROWS(2, 1, 8, 2) : KQ_ROWS(2, 2, 4, 4);
   } else {
-    KQ_ROWS(4, 8, 2);
+    // 16 weight rows a workgroup while that is at most one workgroup per compute unit, with twice
+    // the wavefronts if it leaves some idle (one token, 1024 x 4096: 3.9 against 4.3 us; 11008 x
+    // 4096: 13.0 against 12.2); else, from 17 tokens, 32, which halves what the tokens' codes
+    // cost (24 tokens, 6144 x 4096: 8.3 against 11.2 us; 1152 x 1152: 4.0 against 3.3)
+    const int64_t wgs = (N + 15) / 16, cus = device_cu_count();
+    if (M <= 16) return wgs < cus ? KQ_ROWS(1, 1, 8, 2) : KQ_ROWS(1, 1, 4, 4);
+    if (M <= 32) return wgs <= cus ? KQ_ROWS(1, 2, 4, 4) : KQ_ROWS(2, 2, 4, 4);
+    return wgs <= cus ? KQ_ROWS(1, 4, 4, 2) : KQ_ROWS(2, 4, 4, 2);
   }
 #undef KQ_ROWS
-  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------------
-// Many tokens: tiles of 256 weight rows by 64 TM token rows on four wavefronts (2 x 2), each
-// 128 x 32 TM as 4 x TM blocks of 32 x 32 (TM = 4: 256 float32 accumulators a lane).  The
-// operands go from global memory straight into LDS, 64 k (one matrix instruction) a stage,
-// four stages deep; a stage's row is four 16-byte chunks, XOR-swizzled so that the fragment
-// reads (16 rows x one chunk) and the staging writes hit distinct banks.  Lane l of half
-// h = l / 32 takes chunks h and 2 + h of its row as its 32 values of k.
-// Per stage: wait for the next stage's loads, one barrier, then 4 TM products of 64 cycles
-// with the next stage's fragment reads and the loads of the stage after the ring spread
-// between them (the barrier has freed this stage's own slot: its fragments are in registers).
+// More tokens: tiles of BN weight rows by BM token rows on four wavefronts, WN along the
+// weights and 4 / WN along the tokens, each TN x TM blocks of 32 x 32.  The operands go from
+// global memory straight into LDS, 64 k (one matrix instruction) a stage, NS stages deep; a
+// stage's row is four 16-byte chunks, XOR-swizzled so that the fragment reads (16 rows x one
+// chunk) and the staging writes hit distinct banks.  Lane l of half h = l / 32 takes chunks h
+// and 2 + h of its row as its 32 values of k.
+// A step is G stages: wait for the next step's loads, one barrier, which makes them visible and
+// frees this step's slots (its fragments are in registers), then this step's products, with the
+// reads of the next step's fragments and the loads that refill the freed slots spread between
+// them.  Large tiles have enough products in one stage; for small ones a step of one stage would
+// be the latency of its fragment reads.
 // Scale bytes come 16 at a time for each row (2048 k, so seldom) into a double-buffered area.
-struct F8Tile {
-  static constexpr int NS = 4;                                 // stages
-  static constexpr int A_BYTES = 256 * 64;
-  static constexpr int STAGE = 2 * A_BYTES;
-  static constexpr int SC_OFF = NS * STAGE;                    // two scale groups: 256 + 256 rows x 16 bytes
-  static constexpr int SC_BYTES = 512 * 16;
-  static constexpr int BIAS_OFF = SC_OFF + 2 * SC_BYTES;       // 64 lanes x 16 bytes (256 biases used)
-  static constexpr int TOP_OFF = BIAS_OFF + 1024;              // gated: 2 x 256 maxima
-  static constexpr int LDS = TOP_OFF + 2048;                   // 150528 bytes
+template <int WN_, int TN_, int TM_, int NS_, int G_>
+struct F8Cfg {
+  static constexpr int WN = WN_, WM = 4 / WN_, TN = TN_, TM = TM_, NS = NS_, G = G_;
+  static constexpr int BN = 32 * TN * WN, BM = 32 * TM * WM;
+  static constexpr int BROWS = BM < 64 ? 64 : BM;              // staged token rows (zeros past BM)
+  static constexpr int A_BYTES = BN * 64;
+  static constexpr int STAGE = A_BYTES + BROWS * 64;
+  static constexpr int SC_OFF = NS * STAGE;                    // two scale groups: BN + BROWS rows x 16 bytes
+  static constexpr int SC_BYTES = (BN + BROWS) * 16;
+  static constexpr int BIAS_OFF = SC_OFF + 2 * SC_BYTES;       // 64 lanes x 16 bytes (BN biases used)
+  static constexpr int TOP_OFF = BIAS_OFF + 1024;              // gated: WN x BM maxima
+  static constexpr int LDS = TOP_OFF + WN * BM * 4;
 };
 
 __device__ __forceinline__ int f8_swz(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
 
-// ACT -1: the linear, weight rows n0 .. n0 + 255.  Gated: rows f0 .. f0 + 127 of both halves,
-// f0 = n0 / 2; wavefront column wn holds gate and up of columns f0 + 64 wn .. + 63, so that a
-// lane has both factors of an output, and the tile's 128 columns are one scale group.
-template <int ACT, bool BF16, int TM>
+// ACT -1: the linear, weight rows n0 .. n0 + BN - 1.  Gated (BN = 256): rows f0 .. f0 + 127 of
+// both halves, f0 = n0 / 2, staged gate rows first; wavefront column wn takes gate and up of the
+// same 16 TN columns, so that a lane has both factors of an output, and the tile's 128 columns
+// are one scale group.
+template <int ACT, bool BF16, class C>
 __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
                                         const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
                                         const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
                                         const uint16_t* __restrict__ bias, uint8_t* __restrict__ out,
                                         uint8_t* __restrict__ oscales, int64_t m0, int n0) {
-  using C = F8Tile;
   constexpr bool GATED = ACT >= 0;
-  constexpr int NS = C::NS, NL = 4 + TM, NM = 4 * TM, NR = 2 * (4 + TM);
+  constexpr int NS = C::NS, TN = C::TN, TM = C::TM, NA = C::BN / 64, NB = C::BROWS / 64, NL = NA + NB;
+  constexpr int G = C::G, NM = G * TN * TM, NR = 2 * (TN + TM), SG = G > 1 ? G / 2 : 1;
+  static_assert(!GATED || C::BN == 256, "a gated tile is one scale group wide");
+  static_assert(G == 1 || G == 2 || G == 4, "a loop body of two steps is whole groups and divides 32 stages");
+  static_assert(NS % (2 * G) == 0, "the two steps of a loop body never wrap inside the ring");
   // the thread index, hidden from the compiler, so that it does not keep every lane-dependent
   // offset live across a tile loop
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wid & 1, wm = wid >> 1;
+  const int wn = wid % C::WN, wm = wid / C::WN;
   const int l32 = lane & 31, h = lane >> 5;
   const int SC = (int)f8_scale_cols(K);
   const int nk = 2 * ((K + 127) / 128);                        // stages: whole groups, zeros past K
 
-  // wave w stages weight rows 64 w .. 64 w + 63 of the tile and token rows 16 TM w .. + 16 TM - 1
-  const int64_t arow = GATED ? (int64_t)(wid & 1) * N + (n0 >> 1) + 64 * (wid >> 1) : (int64_t)n0 + 64 * wid;
-  const int64_t aleft = GATED ? N - (n0 >> 1) - 64 * (wid >> 1) : N - n0 - 64 * wid;
+  // wave w stages weight rows 16 NA w .. of the tile (gated: waves 0, 1 gate, 2, 3 up) and token
+  // rows 16 NB w ..; the first waves also the scales of 64 rows each, in the same order
+  const int64_t arow = GATED ? (int64_t)(wid >> 1) * N + (n0 >> 1) + 64 * (wid & 1) : (int64_t)n0 + 16 * NA * wid;
+  const int64_t aleft = GATED ? N - (n0 >> 1) - 64 * (wid & 1) : N - n0 - 16 * NA * wid;
+  const int64_t srow = GATED ? arow : (int64_t)n0 + 64 * wid, sleft = GATED ? aleft : N - n0 - 64 * wid;
   const v4i rA = rsrc_words(wcodes + arow * K, aleft * K);
-  const v4i rAS = rsrc_words(wscales + arow * SC, aleft * SC);
-  const v4i rB = rsrc_words(xcodes + m0 * K, (M - m0) * K);
-  const v4i rBS = rsrc_words(xscales + m0 * SC, (M - m0) * SC);
+  const v4i rAS = rsrc_words(wscales + srow * SC, sleft * SC);
+  const int64_t mleft = min(M - m0, (int64_t)C::BM);
+  const v4i rB = rsrc_words(xcodes + m0 * K, mleft * K);
+  const v4i rBS = rsrc_words(xscales + m0 * SC, mleft * SC);
 
   const uint32_t lds0 = lds_addr(lds);
   const int csw = 16 * ((lane & 3) ^ f8_swz(lane >> 2));
   // unsigned: an offset past the end is KQ_OOB plus at most 2^28 and stays past every range
-  const uint32_t ogA = (lane >> 2) * K + csw, ogB = (16 * TM * wid + (lane >> 2)) * K + csw;
+  const uint32_t ogA = (lane >> 2) * K + csw, ogB = (16 * NB * wid + (lane >> 2)) * K + csw;
   auto k_off = [&](int ks) -> uint32_t { return 64 * ks + csw < K ? 64 * ks : KQ_OOB; };
-  auto code_load = [&](int ks, uint32_t ko, int g) {                // load g (0 .. NL - 1) of stage ks
-    const uint32_t st = lds0 + (uint32_t)((ks % NS) * C::STAGE);
-    if (g < 4) lds_load16(rA, st + (64 * wid + 16 * g) * 64, (int)(ogA + 16 * g * K + ko));
-    else lds_load16(rB, st + C::A_BYTES + (16 * TM * wid + 16 * (g - 4)) * 64, (int)(ogB + 16 * (g - 4) * K + ko));
+  auto code_load = [&](int slot, uint32_t ko, int g) {         // load g (0 .. NL - 1) of a stage
+    const uint32_t st = lds0 + (uint32_t)(slot * C::STAGE);
+    if (g < NA) lds_load16(rA, st + (16 * NA * wid + 16 * g) * 64, (int)(ogA + 16 * g * K + ko));
+    else lds_load16(rB, st + C::A_BYTES + (16 * NB * wid + 16 * (g - NA)) * 64, (int)(ogB + 16 * (g - NA) * K + ko));
   };
-  // scale bytes of stages 32 grp .. 32 grp + 31, issued only when skip is zero: the branch is
-  // inside the assembly so that the loop body stays one block for the scheduler.  A row's last
-  // piece may run into the next row; those bytes are never read.
-  const uint32_t osc = lane * SC, oscb = wid < TM ? (64 * wid + lane) * SC : KQ_OOB;
+  // scale bytes of stages 32 grp .. 32 grp + 31, issued only when skip is zero, by the waves that
+  // have rows: the branches are inside the assembly so that the loop body stays one block for
+  // the scheduler.  A row's last piece may run into the next row; those bytes are never read.
+  const uint32_t osc = lane * SC, oscb = (64 * wid + lane) * SC;
   auto scale_loads = [&](int grp, int skip) {
     const uint32_t sc = lds0 + (uint32_t)(C::SC_OFF + (grp & 1) * C::SC_BYTES + 16 * 64 * wid);
     const uint32_t ko = 32 * grp < nk ? 16 * grp : KQ_OOB;
     asm volatile(
         "s_cmp_lg_u32 %0, 0\n\t"
         "s_cbranch_scc1 1f\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "buffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
         "s_mov_b32 m0, %2\n\t"
         "buffer_load_dwordx4 %4, %6, 0 offen lds\n"
-        "1:"
-        :: "s"(__builtin_amdgcn_readfirstlane(skip)), "s"(__builtin_amdgcn_readfirstlane(sc)),
-           "s"(__builtin_amdgcn_readfirstlane(sc + 256 * 16)), "v"(osc + ko), "v"(oscb + (wid < TM ? ko : 0)),
-           "s"(rAS), "s"(rBS)
+        "1:\n\t"
+        "s_cmp_lg_u32 %1, 0\n\t"
+        "s_cbranch_scc1 2f\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "buffer_load_dwordx4 %5, %7, 0 offen lds\n"
+        "2:"
+        :: "s"(__builtin_amdgcn_readfirstlane(wid < C::BN / 64 ? skip : 1)),
+           "s"(__builtin_amdgcn_readfirstlane(wid < C::BROWS / 64 ? skip : 1)), "s"(__builtin_amdgcn_readfirstlane(sc)),
+           "s"(__builtin_amdgcn_readfirstlane(sc + C::BN * 16)), "v"(osc + ko), "v"(oscb + ko), "s"(rAS), "s"(rBS)
         : "memory", "m0", "scc");
   };
 
-  const int wrow_a = 128 * wn, wrow_b = 32 * TM * wm;
+  // weight block i of a wavefront is LDS rows wrow_a + 32 blk(i) ..
+  auto blk = [](int i) { return GATED ? 4 * (i / (TN / 2 > 0 ? TN / 2 : 1)) + i % (TN / 2 > 0 ? TN / 2 : 1) : i; };
+  const int wrow_a = (GATED ? 16 : 32) * TN * wn, wrow_b = 32 * TM * wm;
   const int sw = f8_swz(l32);                                  // the same for every block of 32 rows
   const int fa = (wrow_a + l32) * 64, fb = C::A_BYTES + (wrow_b + l32) * 64;
   const int c0 = 16 * (h ^ sw), c1 = 16 * ((2 + h) ^ sw);
   auto read_half = [&](const uint8_t* st, int q, v8i* a, v8i* b) {   // half fragment q (0 .. NR - 1)
     const int f = q >> 1;
-    const int at = (f < 4 ? fa + 2048 * f : fb + 2048 * (f - 4)) + ((q & 1) ? c1 : c0);
+    const int at = (f < TN ? fa + 2048 * blk(f) : fb + 2048 * (f - TN)) + ((q & 1) ? c1 : c0);
     const v4i v = *reinterpret_cast<const v4i*>(st + at);
-    v8i& d = f < 4 ? a[f] : b[f - 4];
+    v8i& d = f < TN ? a[f] : b[f - TN];
 #pragma unroll
     for (int e = 0; e < 4; ++e) d[4 * (q & 1) + e] = v[e];
   };
-  const int sa_at = 16 * (wrow_a + l32), sb_at = 256 * 16 + 16 * (wrow_b + l32);
-  auto read_scale = [&](int ks, int q) -> int {                // scale of fragment q for the pair of stages from ks
+  const int sa_at = 16 * (wrow_a + l32), sb_at = C::BN * 16 + 16 * (wrow_b + l32);
+  auto read_scale = [&](int ks, int q) -> int {                // scale of fragment q for the group at stage ks
     const uint8_t* sc = lds + C::SC_OFF + ((ks >> 5) & 1) * C::SC_BYTES + ((ks >> 1) & 15);
-    return sc[q < 4 ? sa_at + 512 * q : sb_at + 512 * (q - 4)];
+    return sc[q < TN ? sa_at + 512 * blk(q) : sb_at + 512 * (q - TN)];
   };
 
-  v16f acc[4][TM];
+  v16f acc[TN][TM];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < TN; ++i)
 #pragma unroll
     for (int j = 0; j < TM; ++j)
 #pragma unroll
@@ -287,62 +364,89 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
 
   if (!GATED && wid == 0) {                                    // without a bias, or past N: zeros
     const v4i rW = rsrc_words(bias + n0, bias ? (int64_t)(N - n0) * 2 : 0);
-    lds_load16(rW, lds0 + C::BIAS_OFF, lane < 32 ? 16 * lane : KQ_OOB);
+    lds_load16(rW, lds0 + C::BIAS_OFF, lane < C::BN / 8 ? 16 * lane : KQ_OOB);
   }
   scale_loads(0, 0);
 #pragma unroll
   for (int p = 0; p < NS; ++p)
 #pragma unroll
     for (int g = 0; g < NL; ++g) code_load(p, k_off(p), g);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 1) * NL));       // biases, scales and stage 0
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - G) * NL));       // biases, scales and the first step's stages
   lds_barrier();
-  v8i a[2][4], b[2][TM];
-  int s[4 + TM];
+  v8i a[2][G][TN], b[2][G][TM];
+  int s[2][SG][TN + TM];                                       // G = 1: one set for both steps
 #pragma unroll
-  for (int q = 0; q < 4 + TM; ++q) s[q] = read_scale(0, q);
+  for (int c = 0; c < SG; ++c)
 #pragma unroll
-  for (int q = 0; q < NR; ++q) read_half(lds, q, a[0], b[0]);
+    for (int q = 0; q < TN + TM; ++q) s[0][c][q] = read_scale(2 * c, q);
+#pragma unroll
+  for (int c = 0; c < G; ++c)
+#pragma unroll
+    for (int q = 0; q < NR; ++q) read_half(lds + c * C::STAGE, q, a[0][c], b[0][c]);
 
-  for (int ks = 0; ks < nk; ks += 2) {
-    int ns[4 + TM];
+  int slot = 0, after = 2 * G % NS;                            // of stages ks and ks + 2 G
+  for (int ks = 0; ks < nk; ks += 2 * G) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      // stage ks + u + 1 has landed once at most those of the two stages behind it are outstanding
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 2) * NL));
+      // the next step's stages have landed once at most those of the NS - 2 G behind them are
+      // outstanding
+      const int k0 = ks + u * G;
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 2 * G) * NL));
       lds_barrier();
       if (u == 0) scale_loads((ks >> 5) + 1, ks & 31);
-      const uint8_t* const nxt = lds + ((ks + u + 1) % NS) * C::STAGE;
-      const uint32_t ko = k_off(ks + u + NS);
+      auto reads = [&](int q0, int q1) {                       // of the next step: G NR half fragments
+#pragma unroll
+        for (int q = q0; q < q1; ++q)
+          read_half(lds + ((u == 0 ? slot + G : after) + q / NR) * C::STAGE, q % NR, a[1 - u][q / NR], b[1 - u][q / NR]);
+      };
+      auto scales = [&](int q0, int q1) {                      // of the next step: SG (TN + TM)
+#pragma unroll
+        for (int q = q0; q < q1; ++q)
+          s[G == 1 ? 1 : 1 - u][q / (TN + TM)][q % (TN + TM)] = read_scale(k0 + G + 2 * (q / (TN + TM)), q % (TN + TM));
+      };
       __builtin_amdgcn_sched_barrier(0);
+      if (G > 1) {
+        reads(0, G * NR);
+        scales(0, SG * (TN + TM));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      uint32_t ko[G];
+#pragma unroll
+      for (int c = 0; c < G; ++c) ko[c] = k_off(k0 + NS + c);
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
-        const int i = m / TM, j = m % TM;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[u][i], b[u][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
+        const int c = m / (TN * TM), i = m / TM % TN, j = m % TM;
+        const int* const sc = s[G == 1 ? 0 : u][c / 2];
+        // behind the last group the codes are zeros, and no scale byte found there may be NaN
+        const int on = G == 1 || k0 + c < nk ? -1 : 0;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[u][c][i], b[u][c][j], acc[i][j], 0, 0, 0, sc[i] & on, 0, sc[TN + j] & on);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int q = NR * m / NM; q < NR * (m + 1) / NM; ++q) read_half(nxt, q, a[1 - u], b[1 - u]);
-        if (u == 1) {
-#pragma unroll
-          for (int q = (4 + TM) * m / NM; q < (4 + TM) * (m + 1) / NM; ++q) ns[q] = read_scale(ks + 2, q);
+        if (G == 1) {
+          reads(NR * m / NM, NR * (m + 1) / NM);
+          if (u == 1) scales((TN + TM) * m / NM, (TN + TM) * (m + 1) / NM);
         }
 #pragma unroll
-        for (int g = NL * m / NM; g < NL * (m + 1) / NM; ++g) code_load(ks + u + NS, ko, g);
+        for (int g = G * NL * m / NM; g < G * NL * (m + 1) / NM; ++g) code_load(slot + u * G + g / NL, ko[g / NL], g % NL);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    if (G == 1) {
 #pragma unroll
-    for (int q = 0; q < 4 + TM; ++q) s[q] = ns[q];
+      for (int q = 0; q < TN + TM; ++q) s[0][0][q] = s[1][0][q];
+    }
+    slot = after;
+    after = after + 2 * G == NS ? 0 : after + 2 * G;
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));                   // no load may land in LDS after this tile
 
   if constexpr (!GATED) {
-    const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, (M - m0) * N * 2);
+    const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, mleft * N * 2);
     const uint32_t* const bias_t = reinterpret_cast<const uint32_t*>(lds + C::BIAS_OFF);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       const int ml = wrow_b + 32 * j + l32;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < TN; ++i) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           uint32_t pk[2][2];
@@ -372,40 +476,44 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
       }
     }
   } else {
-    // outputs in place of the gates, the maximum of each token's 64 columns to LDS, and after
-    // the barrier the scale of its 128 (rows past F are zeros on both sides and stay zeros)
+    // outputs in place of the gates, the maximum of each token's columns in this wave to LDS, and
+    // after the barrier the scale of all 128 (rows past F are zeros on both sides and stay zeros)
+    constexpr int TH = TN / 2;
     uint32_t* const tops = reinterpret_cast<uint32_t*>(lds + C::TOP_OFF);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < TH; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float v = f8_act<ACT>(acc[i][j][e]) * acc[i + 2][j][e];
+          const float v = f8_act<ACT>(acc[i][j][e]) * acc[i + TH][j][e];
           acc[i][j][e] = v;
           top = umax32(top, abs_bits(v));
         }
       top = umax32(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      if (h == 0) tops[256 * wn + wrow_b + 32 * j + l32] = top;
+      if (h == 0) tops[C::BM * wn + wrow_b + 32 * j + l32] = top;
     }
     lds_barrier();
     const int f0 = n0 >> 1, OS = (int)f8_scale_cols(N), grp = f0 >> 7;
-    const __amdgpu_buffer_rsrc_t rQ = make_rsrc(out + m0 * N, (M - m0) * N);
+    const __amdgpu_buffer_rsrc_t rQ = make_rsrc(out + m0 * N, mleft * N);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       const int ml = wrow_b + 32 * j + l32;
-      const uint32_t byte = f8_scale_byte(umax32(tops[ml], tops[256 + ml]));
+      uint32_t top = tops[ml];
+#pragma unroll
+      for (int v = 1; v < C::WN; ++v) top = umax32(top, tops[C::BM * v + ml]);
+      const uint32_t byte = f8_scale_byte(top);
       const bool bad = byte == 255u;
       const float inv = bad ? 1.0f : f8_inv_scale(byte);
-      if (wn == 0 && h == 0 && m0 + ml < M) {
+      if (wn == 0 && h == 0 && ml < mleft) {
         uint8_t* const row = oscales + (m0 + ml) * OS;
         row[grp] = (uint8_t)byte;
         if (f0 + 128 >= N)
           for (int q = grp + 1; q < OS; ++q) row[q] = 0;       // padding
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < TH; ++i) {
         uint32_t w[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -416,44 +524,74 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
         const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
         const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
         const v4i outv = {(int)s0[0], (int)s0[1], (int)s1[0], (int)s1[1]};
-        const int col = f0 + 64 * wn + 32 * i + 16 * h;
+        const int col = f0 + wrow_a + 32 * i + 16 * h;
         __builtin_amdgcn_raw_buffer_store_b128(outv, rQ, col < N ? ml * N + col : KQ_OOB, 0, 0);
       }
     }
   }
 }
 
+// Consecutive tile numbers, which the dispatcher deals out to the compute dies in turn, are
+// remapped so that each die holds a contiguous run of tiles.
+__device__ __forceinline__ int f8_remap(int pid, int n) {
+  const int per = n / 8;
+  return pid < 8 * per ? (pid % 8) * per + pid / 8 : pid;
+}
+
+using F8Large = F8Cfg<2, 4, 4, 4, 1>;     // 256 x 256
+using F8Half = F8Cfg<2, 4, 2, 4, 1>;      // 256 x 128 tokens
+
 // The first full_rows rows of 256-token tiles are whole tiles, grouped eight along M for reuse
 // in the level-2 caches; the rows below them are tiles of 128 tokens.  Each workgroup loops over
-// every grid-th tile.  Consecutive tile numbers, which the dispatcher deals out to the compute
-// dies in turn, are remapped so that each die holds a contiguous run of tiles.
+// every grid-th tile.
 template <int ACT, bool BF16>
 __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
     uint8_t* __restrict__ out, uint8_t* __restrict__ oscales, int full_rows) {
-  __shared__ __align__(16) uint8_t lds[F8Tile::LDS];
+  __shared__ __align__(16) uint8_t lds[F8Large::LDS];
+  static_assert(F8Half::LDS <= F8Large::LDS, "");
   const int tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256;
   const int nfull = tiles_n * full_rows;
   const int hrows = max(0, (int)((M + 127) / 128) - 2 * full_rows), nhalf = tiles_n * hrows;
-  auto remap = [](int pid, int n) {
-    const int per = n / 8;
-    return pid < 8 * per ? (pid % 8) * per + pid / 8 : pid;
-  };
   for (int t = blockIdx.x; t < nfull + nhalf; t += gridDim.x) {
     if (t < nfull) {
       constexpr int GM = 8;
-      const int pid = remap(t, nfull);
+      const int pid = f8_remap(t, nfull);
       const int first = pid / (GM * tiles_n) * GM, rows = min(full_rows - first, GM), in = pid % (GM * tiles_n);
-      f8_tile<ACT, BF16, 4>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                            256LL * (first + in % rows), 256 * (in / rows));
+      f8_tile<ACT, BF16, F8Large>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
+                                  256LL * (first + in % rows), 256 * (in / rows));
     } else {
-      const int q = remap(t - nfull, nhalf);
-      f8_tile<ACT, BF16, 2>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                            256LL * full_rows + 128LL * (q % hrows), 256 * (q / hrows));
+      const int q = f8_remap(t - nfull, nhalf);
+      f8_tile<ACT, BF16, F8Half>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
+                                 256LL * full_rows + 128LL * (q % hrows), 256 * (q / hrows));
     }
     __syncthreads();                         // the next tile's loads stay off what this one's epilogue reads
   }
+}
+
+// One tile of configuration C per workgroup.
+template <int ACT, bool BF16, class C>
+__global__ __launch_bounds__(256, 1) void f8_small_kernel(
+    const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
+    const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
+    uint8_t* __restrict__ out, uint8_t* __restrict__ oscales) {
+  __shared__ __align__(16) uint8_t lds[C::LDS];
+  const int rows = (int)((M + C::BM - 1) / C::BM);
+  const int pid = f8_remap(blockIdx.x, gridDim.x);
+  f8_tile<ACT, BF16, C>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, (int64_t)C::BM * (pid % rows),
+                        C::BN * (pid / rows));
+}
+
+template <int ACT, bool BF16, class C>
+static hipError_t small_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+                               const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
+                               uint8_t* out, uint8_t* oscales, hipStream_t s) {
+  const int64_t cols = ACT >= 0 ? C::BN / 2 : C::BN;
+  const int64_t grid = (N + cols - 1) / cols * ((M + C::BM - 1) / C::BM);
+  hipLaunchKernelGGL((f8_small_kernel<ACT, BF16, C>), dim3((unsigned)grid), dim3(256), 0, s, wcodes, wscales, xcodes,
+                     xscales, M, (int)N, (int)K, bias, out, oscales);
+  return hipGetLastError();
 }
 
 template <int ACT, bool BF16>
@@ -484,12 +622,25 @@ static hipError_t gemm_launch(const uint8_t* xcodes, const uint8_t* xscales, int
 
 size_t f8_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
+// The smallest tiles that give at most one workgroup per compute unit: fewer, larger tiles read
+// less, but a chain of k over few compute units is bound by what one of them can take in.
 template <bool BF16>
 static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                                 const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
                                 uint8_t* Y, hipStream_t s) {
-  if (M > 64) return gemm_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
-  return rows_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
+  if (M <= ROWS_LINEAR) return rows_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
+  const int64_t cus = device_cu_count();
+  auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
+#define KQ_TILE(...) \
+  small_launch<-1, BF16, F8Cfg<__VA_ARGS__>>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s)
+  // measured (us) at 4096 x 4096 with 64 x 64 / 128 x 64 / 128 x 128 / 256 x 256: 200 tokens 12.0 /
+  // 15.1 / 18.0 / 27.6, 512 tokens 18.4 / 16.4 / 18.9 / 29.0, 1024 tokens 33.6 / 30.6 / 22.5 / 30.5,
+  // 2048 tokens 79 / 60 / 43 / 39
+  if (tiles(64, 64) <= cus) return KQ_TILE(2, 1, 1, 8, 2);
+  if (tiles(128, 64) <= cus) return KQ_TILE(2, 2, 1, 8, 2);
+  if (tiles(128, 128) <= cus) return KQ_TILE(2, 2, 2, 4, 1);
+#undef KQ_TILE
+  return gemm_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
 }
 
 hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
@@ -501,16 +652,28 @@ hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xsc
               : linear_launch<false>(xcodes, xscales, M, K, wcodes, wscales, N, b, y, s);
 }
 
-size_t f8_gated_workspace_bytes(int64_t M, int64_t F, int64_t) { return M > 64 ? 0 : (size_t)M * F * 4; }
+size_t f8_gated_workspace_bytes(int64_t M, int64_t F, int64_t) { return M > ROWS_GATED ? 0 : (size_t)M * F * 4; }
 
 template <int ACT>
 static hipError_t gated_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                                const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,
                                uint8_t* scales, void* workspace, hipStream_t s) {
-  if (M > 64) return gemm_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
-  const hipError_t e = rows_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, workspace, s);
-  if (e != hipSuccess) return e;
-  return launch_f8_quantize_f32(static_cast<const float*>(workspace), M, F, codes, scales, s);
+  if (M <= ROWS_GATED) {
+    // a workgroup's 16 columns are an eighth of a scale group: the outputs go through the
+    // workspace in float32 and the quantizer
+    const hipError_t e = rows_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, workspace, s);
+    if (e != hipSuccess) return e;
+    return launch_f8_quantize_f32(static_cast<const float*>(workspace), M, F, codes, scales, s);
+  }
+  const int64_t cols = (F + 127) / 128, cus = device_cu_count();
+#define KQ_TILE(...) \
+  small_launch<ACT, false, F8Cfg<__VA_ARGS__>>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s)
+  // as the linear's rule; measured (us) with 32 / 64 / 128 tokens a tile: 64 tokens, 11008 x 4096 31 /
+  // 36 / 35; 128 tokens 52 / 34 / 37; 203 tokens 73 / 56 / 37; 203 tokens, 5600 x 2240 29 / 18 / 21
+  if (cols * ((M + 31) / 32) <= cus) return KQ_TILE(4, 2, 1, 6, 1);
+  if (cols * ((M + 63) / 64) <= cus) return KQ_TILE(2, 4, 1, 6, 1);
+#undef KQ_TILE
+  return gemm_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
 }
 
 hipError_t launch_f8_gated(int act, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
