@@ -353,20 +353,23 @@ kq_status kq_rmsnorm_quantize_fp8(int32_t dtype, const void* X, const void* resi
                                   int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, void* residual_out,
                                   hipStream_t stream);
 
-/* Y = Xq Wq^T (+ bias): Y [M][N] and bias [N] (or NULL) in the dtype, float32 accumulation.
- * workspace: at least kq_fp8_linear_workspace_bytes(M, N, K) bytes (0: none needed), which
- * holds partial sums when few rows are split over K; they are added in a fixed order.  Calls
- * that share a workspace must not overlap (captured graphs that hold it included). */
-size_t kq_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+/* Y = Xq Wq^T (+ bias): Y [M][N] and bias [N] (or NULL) in the dtype, float32 accumulation (to
+ * 16 tokens of exact products; above, by the 8-bit matrix instructions, which keep about 14 bits
+ * below the largest of each four products: a relative error of 2e-5 to 5e-5 of a sum, where the
+ * output's own rounding is 5e-4 (fp16) or 4e-3 (bf16)).  The order of additions is fixed: equal
+ * inputs of equal shape give equal bits. */
 kq_status kq_fp8_linear(int32_t dtype, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                         const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const void* bias, void* Y,
-                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+                        hipStream_t stream);
 
 /* The first half of a gated feed-forward block: codes, scales ([M][F]) of
  *   act(Xq Wg^T) * (Xq Wu^T),   wcodes [2 F][K]: the F rows of Wg, then the F rows of Wu.
  * act: SiLU g / (1 + exp -g); GELU g Phi(g); its tanh form.  Both projections, the activation
  * and the product stay in float32; the result is rounded once, to E4M3.  kq_fp8_linear with
- * the down-projection's weights takes codes and scales as they are.  workspace as above. */
+ * the down-projection's weights takes codes and scales as they are.  workspace: at least
+ * kq_fp8_gated_linear_workspace_bytes(M, F, K) bytes (0: none needed), which holds the float32
+ * outputs of a few tokens.  Calls that share a workspace must not overlap, replays of captured
+ * graphs that hold it included. */
 size_t kq_fp8_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K);
 kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                               const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,

@@ -121,11 +121,11 @@ def test_norm_refusals(lib):
 
 def test_linear_refusals(lib):
     f = lib.kq_fp8_linear
-    ok = dict(dt=1, x=P, xs=P, M=4, K=64, w=P, ws=P, N=32, b=P, Y=P, wk=P, nb=1 << 40)
+    ok = dict(dt=1, x=P, xs=P, M=4, K=64, w=P, ws=P, N=32, b=P, Y=P)
 
     def call(**kw):
         a = {**ok, **kw}
-        return f(a["dt"], a["x"], a["xs"], a["M"], a["K"], a["w"], a["ws"], a["N"], a["b"], a["Y"], a["wk"], a["nb"], None)
+        return f(a["dt"], a["x"], a["xs"], a["M"], a["K"], a["w"], a["ws"], a["N"], a["b"], a["Y"], None)
     for name in ("x", "xs", "w", "ws", "Y"):
         assert call(**{name: None}) == NULL
     assert call(dt=2) == UNSUPPORTED
@@ -135,8 +135,6 @@ def test_linear_refusals(lib):
         assert call(**{name: ODD16}) == ALIGN
     for name in ("xs", "ws"):
         assert call(**{name: ODD4}) == ALIGN
-    assert lib.kq_fp8_linear_workspace_bytes(0, 32, 64) == 0
-    assert lib.kq_fp8_linear_workspace_bytes(4, 33, 64) == 0
 
 
 def test_gated_refusals(lib):

@@ -184,6 +184,8 @@ LINEAR_SHAPES = [
     (37, 6144, 512), (48, 272, 912), (63, 400, 2240), (64, 640, 128), (65, 272, 256), (96, 1152, 4096), (100, 2240, 5600),
     (128, 256, 1024), (129, 272, 128), (200, 144, 2240), (255, 256, 64), (256, 512, 512), (257, 784, 400),
     (300, 1152, 1152), (513, 528, 272), (1000, 2240, 1152), (1024, 1024, 1024), (1025, 4112, 16), (2060, 1552, 640),
+    (5, 272, 16400), (40, 48, 33040),                                  # more than one set of scale bytes
+    (1031, 4112, 4304), (4100, 4112, 272), (2500, 8208, 656), (1290, 6160, 144),   # large tiles, whole and halved
 ]
 
 
@@ -264,7 +266,9 @@ def test_linear_extreme_scales(kq):
 GATED_SHAPES = [(1, 16, 16), (1, 128, 4096), (1, 1152, 512), (2, 144, 528), (3, 272, 272), (7, 2240, 1152), (16, 400, 1040),
                 (17, 528, 640), (32, 1024, 256), (33, 144, 144), (64, 256, 2240), (65, 272, 528), (100, 640, 1152),
                 (128, 128, 512), (130, 144, 400), (203, 1104, 2240), (256, 256, 1024), (300, 528, 272), (513, 1152, 640),
-                (1030, 784, 528), (2050, 272, 128)]
+                (1030, 784, 528), (2050, 272, 128),
+                (3, 48, 16400), (40, 144, 16656), (1030, 2064, 528), (2050, 4112, 400), (600, 11024, 272),
+                (1100, 2192, 4240)]
 
 
 @pytest.mark.parametrize("M,F,K", GATED_SHAPES)

@@ -32,7 +32,7 @@ __all__ = ["mfma_fp4_probe", "load", "lib_path", "abi_version", "status_str", "l
            "w4a4_linear", "w4a4_linear_t", "w4a4_linear_workspace_bytes",
            "lowrank_down", "lowrank_down_workspace_bytes", "transform_quantize_lowrank",
            "svd_lowrank", "svd_lowrank_workspace_bytes", "fp8_scale_cols", "quantize_fp8", "rmsnorm_quantize_fp8",
-           "fp8_linear", "fp8_linear_workspace_bytes", "fp8_gated_linear", "fp8_gated_linear_workspace_bytes",
+           "fp8_linear", "fp8_gated_linear", "fp8_gated_linear_workspace_bytes",
            "KQError"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -115,10 +115,8 @@ def load():
     lib.kq_quantize_fp8.argtypes = [i32, vp, i64, i64, vp, vp, vp]
     lib.kq_rmsnorm_quantize_fp8.restype = i32
     lib.kq_rmsnorm_quantize_fp8.argtypes = [i32, vp, vp, vp, ctypes.c_float, i64, i64, vp, vp, vp, vp]
-    lib.kq_fp8_linear_workspace_bytes.restype = sz
-    lib.kq_fp8_linear_workspace_bytes.argtypes = [i64, i64, i64]
     lib.kq_fp8_linear.restype = i32
-    lib.kq_fp8_linear.argtypes = [i32, vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, sz, vp]
+    lib.kq_fp8_linear.argtypes = [i32, vp, vp, i64, i64, vp, vp, i64, vp, vp, vp]
     lib.kq_fp8_gated_linear_workspace_bytes.restype = sz
     lib.kq_fp8_gated_linear_workspace_bytes.argtypes = [i64, i64, i64]
     lib.kq_fp8_gated_linear.restype = i32
@@ -726,17 +724,10 @@ def _fp8_workspace(torch, workspace, need, device, made):
     return _same(workspace, "workspace", torch.uint8, workspace.shape, device.index), workspace.numel()
 
 
-def fp8_linear_workspace_bytes(M, N, K):
-    """Workspace bytes kq_fp8_linear needs (0: none)."""
-    return load().kq_fp8_linear_workspace_bytes(M, N, K)
-
-
-def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, workspace=None, stream=None):
+def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, stream=None):
     """Y = Xq Wq^T (+ bias), fp16 or bf16 [M][N], float32 accumulation.  xcodes [M][K] and
     wcodes [N][K] float8_e4m3fn with their scale bytes (quantize_fp8); N a multiple of 16; bias
-    [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16).  workspace: a
-    uint8 device tensor of fp8_linear_workspace_bytes(M, N, K) bytes (256-byte aligned); by
-    default one is taken from torch's allocator."""
+    [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16)."""
     torch = _torch()
     M, N, K, x, w = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if dtype is None:
@@ -748,8 +739,7 @@ def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, 
         Y = torch.empty((M, N), dtype=dtype, device=device)
         made.append(Y)
     y = _same(Y, "Y", dtype, (M, N), device.index)
-    wk, nb = _fp8_workspace(torch, workspace, fp8_linear_workspace_bytes(M, N, K), device, made)
-    _call("kq_fp8_linear", device.index, stream, made, (dt, *x, M, K, *w, N, b, y, wk, nb))
+    _call("kq_fp8_linear", device.index, stream, made, (dt, *x, M, K, *w, N, b, y))
     return Y
 
 
@@ -762,7 +752,9 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
                      stream=None):
     """codes and scales (as quantize_fp8, [M][F]) of act(Xq Wg^T) * (Xq Wu^T).  wcodes [2 F][K]
     holds the F rows of Wg, then the F rows of Wu; F a multiple of 16.  act: 'silu', 'gelu' or
-    'gelu_tanh'.  The result feeds fp8_linear with the down-projection's weights."""
+    'gelu_tanh'.  The result feeds fp8_linear with the down-projection's weights.  workspace: a
+    uint8 device tensor of fp8_gated_linear_workspace_bytes(M, F, K) bytes (256-byte aligned); by
+    default one is taken from torch's allocator."""
     torch = _torch()
     if act not in _ACT:
         raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")

@@ -263,6 +263,65 @@ struct F8Cfg {
 
 __device__ __forceinline__ int f8_swz(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
 
+// The gated tiles' epilogue.  acc[0 .. TH - 1] are gates, acc[TH .. 2 TH - 1] the up values of the
+// same columns f0 + col0 + 32 i .., lane l's token of block j row0 + 32 j + l % 32.  Outputs in place
+// of the gates, the maximum of each token's columns in this wave to LDS, and after the barrier the
+// scale of all 128 (columns past F are zeros on both sides and stay zeros).
+template <int ACT, int TH, int TM, int WN, int BM>
+__device__ __forceinline__ void f8_gated_store(v16f (&acc)[2 * TH][TM], uint8_t* __restrict__ lds_tops, int wn, int col0,
+                                               int row0, int l32, int h, int64_t m0, int64_t mleft, int f0, int F,
+                                               uint8_t* __restrict__ out, uint8_t* __restrict__ oscales) {
+  uint32_t* const tops = reinterpret_cast<uint32_t*>(lds_tops);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < TH; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float v = f8_act<ACT>(acc[i][j][e]) * acc[i + TH][j][e];
+        acc[i][j][e] = v;
+        top = umax32(top, abs_bits(v));
+      }
+    top = umax32(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    if (h == 0) tops[BM * wn + row0 + 32 * j + l32] = top;
+  }
+  lds_barrier();
+  const int OS = (int)f8_scale_cols(F), grp = f0 >> 7;
+  const __amdgpu_buffer_rsrc_t rQ = make_rsrc(out + m0 * F, mleft * F);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int ml = row0 + 32 * j + l32;
+    uint32_t top = tops[ml];
+#pragma unroll
+    for (int v = 1; v < WN; ++v) top = umax32(top, tops[BM * v + ml]);
+    const uint32_t byte = f8_scale_byte(top);
+    const bool bad = byte == 255u;
+    const float inv = bad ? 1.0f : f8_inv_scale(byte);
+    if (wn == 0 && h == 0 && ml < mleft) {
+      uint8_t* const row = oscales + (m0 + ml) * OS;
+      row[grp] = (uint8_t)byte;
+      if (f0 + 128 >= F)
+        for (int q = grp + 1; q < OS; ++q) row[q] = 0;         // padding
+    }
+#pragma unroll
+    for (int i = 0; i < TH; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t c = f8_pack4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3], inv);
+        w[g] = bad ? 0x7F7F7F7Fu : c;
+      }
+      // dword g of half h is columns 8 g + 4 h .. + 3: swaps leave half h with 16 h .. + 15
+      const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+      const v4i outv = {(int)s0[0], (int)s0[1], (int)s1[0], (int)s1[1]};
+      const int col = f0 + col0 + 32 * i + 16 * h;
+      __builtin_amdgcn_raw_buffer_store_b128(outv, rQ, col < F ? ml * F + col : KQ_OOB, 0, 0);
+    }
+  }
+}
+
 // ACT -1: the linear, weight rows n0 .. n0 + BN - 1.  Gated (BN = 256): rows f0 .. f0 + 127 of
 // both halves, f0 = n0 / 2, staged gate rows first; wavefront column wn takes gate and up of the
 // same 16 TN columns, so that a lane has both factors of an output, and the tile's 128 columns
@@ -274,11 +333,10 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
                                         const uint16_t* __restrict__ bias, uint8_t* __restrict__ out,
                                         uint8_t* __restrict__ oscales, int64_t m0, int n0) {
   constexpr bool GATED = ACT >= 0;
-  constexpr int NS = C::NS, TN = C::TN, TM = C::TM, NA = C::BN / 64, NB = C::BROWS / 64, NL = NA + NB;
-  constexpr int G = C::G, NM = G * TN * TM, NR = 2 * (TN + TM), SG = G > 1 ? G / 2 : 1;
+  constexpr int NS = C::NS, TN = C::TN, TM = C::TM, G = C::G;
+  constexpr int NA = C::BN / 64, NB = C::BROWS / 64, NL = NA + NB;   // loads (16 rows) of a wave and stage
+  constexpr int NR = 2 * (TN + TM);                            // reads of 64 k
   static_assert(!GATED || C::BN == 256, "a gated tile is one scale group wide");
-  static_assert(G == 1 || G == 2 || G == 4, "a loop body of two steps is whole groups and divides 32 stages");
-  static_assert(NS % (2 * G) == 0, "the two steps of a loop body never wrap inside the ring");
   // the thread index, hidden from the compiler, so that it does not keep every lane-dependent
   // offset live across a tile loop
   int tid = threadIdx.x;
@@ -287,7 +345,7 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
   const int wn = wid % C::WN, wm = wid / C::WN;
   const int l32 = lane & 31, h = lane >> 5;
   const int SC = (int)f8_scale_cols(K);
-  const int nk = 2 * ((K + 127) / 128);                        // stages: whole groups, zeros past K
+  const int T = (K + 127) / 128;                               // groups (zeros past K)
 
   // wave w stages weight rows 16 NA w .. of the tile (gated: waves 0, 1 gate, 2, 3 up) and token
   // rows 16 NB w ..; the first waves also the scales of 64 rows each, in the same order
@@ -301,22 +359,22 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
   const v4i rBS = rsrc_words(xscales + m0 * SC, mleft * SC);
 
   const uint32_t lds0 = lds_addr(lds);
-  const int csw = 16 * ((lane & 3) ^ f8_swz(lane >> 2));
+  const int lrow = lane >> 2, lcol = 16 * ((lane & 3) ^ f8_swz(lrow));   // a load's row and first byte of this lane
   // unsigned: an offset past the end is KQ_OOB plus at most 2^28 and stays past every range
-  const uint32_t ogA = (lane >> 2) * K + csw, ogB = (16 * NB * wid + (lane >> 2)) * K + csw;
-  auto k_off = [&](int ks) -> uint32_t { return 64 * ks + csw < K ? 64 * ks : KQ_OOB; };
+  const uint32_t ogA = lrow * K, ogB = (16 * NB * wid + lrow) * K;
+  auto k_off = [&](int ks) -> uint32_t { return 64 * ks + lcol < K ? 64 * ks + lcol : KQ_OOB; };
   auto code_load = [&](int slot, uint32_t ko, int g) {         // load g (0 .. NL - 1) of a stage
     const uint32_t st = lds0 + (uint32_t)(slot * C::STAGE);
     if (g < NA) lds_load16(rA, st + (16 * NA * wid + 16 * g) * 64, (int)(ogA + 16 * g * K + ko));
     else lds_load16(rB, st + C::A_BYTES + (16 * NB * wid + 16 * (g - NA)) * 64, (int)(ogB + 16 * (g - NA) * K + ko));
   };
-  // scale bytes of stages 32 grp .. 32 grp + 31, issued only when skip is zero, by the waves that
+  // scale bytes of groups 16 grp .. 16 grp + 15, issued only when skip is zero, by the waves that
   // have rows: the branches are inside the assembly so that the loop body stays one block for
   // the scheduler.  A row's last piece may run into the next row; those bytes are never read.
   const uint32_t osc = lane * SC, oscb = (64 * wid + lane) * SC;
   auto scale_loads = [&](int grp, int skip) {
     const uint32_t sc = lds0 + (uint32_t)(C::SC_OFF + (grp & 1) * C::SC_BYTES + 16 * 64 * wid);
-    const uint32_t ko = 32 * grp < nk ? 16 * grp : KQ_OOB;
+    const uint32_t ko = 16 * grp < T ? 16 * grp : KQ_OOB;
     asm volatile(
         "s_cmp_lg_u32 %0, 0\n\t"
         "s_cbranch_scc1 1f\n\t"
@@ -342,15 +400,14 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
   const int c0 = 16 * (h ^ sw), c1 = 16 * ((2 + h) ^ sw);
   auto read_half = [&](const uint8_t* st, int q, v8i* a, v8i* b) {   // half fragment q (0 .. NR - 1)
     const int f = q >> 1;
-    const int at = (f < TN ? fa + 2048 * blk(f) : fb + 2048 * (f - TN)) + ((q & 1) ? c1 : c0);
-    const v4i v = *reinterpret_cast<const v4i*>(st + at);
+    const v4i v = *reinterpret_cast<const v4i*>(st + (f < TN ? fa + 2048 * blk(f) : fb + 2048 * (f - TN)) + ((q & 1) ? c1 : c0));
     v8i& d = f < TN ? a[f] : b[f - TN];
 #pragma unroll
     for (int e = 0; e < 4; ++e) d[4 * (q & 1) + e] = v[e];
   };
   const int sa_at = 16 * (wrow_a + l32), sb_at = C::BN * 16 + 16 * (wrow_b + l32);
-  auto read_scale = [&](int ks, int q) -> int {                // scale of fragment q for the group at stage ks
-    const uint8_t* sc = lds + C::SC_OFF + ((ks >> 5) & 1) * C::SC_BYTES + ((ks >> 1) & 15);
+  auto read_scale = [&](int grp, int q) -> int {               // scale of fragment q for a group of k
+    const uint8_t* sc = lds + C::SC_OFF + ((grp >> 4) & 1) * C::SC_BYTES + (grp & 15);
     return sc[q < TN ? sa_at + 512 * blk(q) : sb_at + 512 * (q - TN)];
   };
 
@@ -371,20 +428,20 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
   for (int p = 0; p < NS; ++p)
 #pragma unroll
     for (int g = 0; g < NL; ++g) code_load(p, k_off(p), g);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - G) * NL));       // biases, scales and the first step's stages
+  static_assert(G == 1 || G == 2, "a loop body of two steps is whole groups");
+  static_assert(NS % (2 * G) == 0, "the two steps of a loop body never wrap inside the ring");
+  constexpr int NM = G * TN * TM;
+  const int nk = 2 * T;                                      // stages
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - G) * NL));     // biases, scales and the first step's stages
   lds_barrier();
   v8i a[2][G][TN], b[2][G][TM];
-  int s[2][SG][TN + TM];                                       // G = 1: one set for both steps
+  int s[2][TN + TM];                                         // G = 1: the first set for both steps
 #pragma unroll
-  for (int c = 0; c < SG; ++c)
+  for (int q = 0; q < TN + TM; ++q) s[0][q] = read_scale(0, q);
 #pragma unroll
-    for (int q = 0; q < TN + TM; ++q) s[0][c][q] = read_scale(2 * c, q);
-#pragma unroll
-  for (int c = 0; c < G; ++c)
-#pragma unroll
-    for (int q = 0; q < NR; ++q) read_half(lds + c * C::STAGE, q, a[0][c], b[0][c]);
+  for (int q = 0; q < G * NR; ++q) read_half(lds + q / NR * C::STAGE, q % NR, a[0][q / NR], b[0][q / NR]);
 
-  int slot = 0, after = 2 * G % NS;                            // of stages ks and ks + 2 G
+  int slot = 0, after = 2 * G % NS;                          // of stages ks and ks + 2 G
   for (int ks = 0; ks < nk; ks += 2 * G) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -393,34 +450,36 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
       const int k0 = ks + u * G;
       __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 2 * G) * NL));
       lds_barrier();
-      if (u == 0) scale_loads((ks >> 5) + 1, ks & 31);
-      auto reads = [&](int q0, int q1) {                       // of the next step: G NR half fragments
+      __builtin_amdgcn_sched_barrier(0);
+      // the next step's fragments, and its scales if it starts a group
+      auto reads = [&](int q0, int q1) {
 #pragma unroll
         for (int q = q0; q < q1; ++q)
           read_half(lds + ((u == 0 ? slot + G : after) + q / NR) * C::STAGE, q % NR, a[1 - u][q / NR], b[1 - u][q / NR]);
       };
-      auto scales = [&](int q0, int q1) {                      // of the next step: SG (TN + TM)
+      auto scales = [&](int q0, int q1) {
 #pragma unroll
-        for (int q = q0; q < q1; ++q)
-          s[G == 1 ? 1 : 1 - u][q / (TN + TM)][q % (TN + TM)] = read_scale(k0 + G + 2 * (q / (TN + TM)), q % (TN + TM));
+        for (int q = q0; q < q1; ++q) s[G == 1 ? 1 : 1 - u][q] = read_scale((k0 + G) / 2, q);
       };
-      __builtin_amdgcn_sched_barrier(0);
       if (G > 1) {
         reads(0, G * NR);
-        scales(0, SG * (TN + TM));
+        scales(0, TN + TM);
         __builtin_amdgcn_sched_barrier(0);
       }
       uint32_t ko[G];
 #pragma unroll
-      for (int c = 0; c < G; ++c) ko[c] = k_off(k0 + NS + c);
-#pragma unroll
       for (int m = 0; m < NM; ++m) {
         const int c = m / (TN * TM), i = m / TM % TN, j = m % TM;
-        const int* const sc = s[G == 1 ? 0 : u][c / 2];
+        const int* const sc = s[G == 1 ? 0 : u];
         // behind the last group the codes are zeros, and no scale byte found there may be NaN
         const int on = G == 1 || k0 + c < nk ? -1 : 0;
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[u][c][i], b[u][c][j], acc[i][j], 0, 0, 0, sc[i] & on, 0, sc[TN + j] & on);
         __builtin_amdgcn_sched_barrier(0);
+        if (m == 0) {
+          if (u == 0) scale_loads((ks >> 5) + 1, ks & 31);
+#pragma unroll
+          for (int d = 0; d < G; ++d) ko[d] = k_off(k0 + NS + d);
+        }
         if (G == 1) {
           reads(NR * m / NM, NR * (m + 1) / NM);
           if (u == 1) scales((TN + TM) * m / NM, (TN + TM) * (m + 1) / NM);
@@ -432,7 +491,7 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
     }
     if (G == 1) {
 #pragma unroll
-      for (int q = 0; q < TN + TM; ++q) s[0][0][q] = s[1][0][q];
+      for (int q = 0; q < TN + TM; ++q) s[0][q] = s[1][q];
     }
     slot = after;
     after = after + 2 * G == NS ? 0 : after + 2 * G;
@@ -476,58 +535,8 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
       }
     }
   } else {
-    // outputs in place of the gates, the maximum of each token's columns in this wave to LDS, and
-    // after the barrier the scale of all 128 (rows past F are zeros on both sides and stay zeros)
-    constexpr int TH = TN / 2;
-    uint32_t* const tops = reinterpret_cast<uint32_t*>(lds + C::TOP_OFF);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < TH; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float v = f8_act<ACT>(acc[i][j][e]) * acc[i + TH][j][e];
-          acc[i][j][e] = v;
-          top = umax32(top, abs_bits(v));
-        }
-      top = umax32(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      if (h == 0) tops[C::BM * wn + wrow_b + 32 * j + l32] = top;
-    }
-    lds_barrier();
-    const int f0 = n0 >> 1, OS = (int)f8_scale_cols(N), grp = f0 >> 7;
-    const __amdgpu_buffer_rsrc_t rQ = make_rsrc(out + m0 * N, mleft * N);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int ml = wrow_b + 32 * j + l32;
-      uint32_t top = tops[ml];
-#pragma unroll
-      for (int v = 1; v < C::WN; ++v) top = umax32(top, tops[C::BM * v + ml]);
-      const uint32_t byte = f8_scale_byte(top);
-      const bool bad = byte == 255u;
-      const float inv = bad ? 1.0f : f8_inv_scale(byte);
-      if (wn == 0 && h == 0 && ml < mleft) {
-        uint8_t* const row = oscales + (m0 + ml) * OS;
-        row[grp] = (uint8_t)byte;
-        if (f0 + 128 >= N)
-          for (int q = grp + 1; q < OS; ++q) row[q] = 0;       // padding
-      }
-#pragma unroll
-      for (int i = 0; i < TH; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t c = f8_pack4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3], inv);
-          w[g] = bad ? 0x7F7F7F7Fu : c;
-        }
-        // dword g of half h is columns 8 g + 4 h .. + 3: swaps leave half h with 16 h .. + 15
-        const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-        const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-        const v4i outv = {(int)s0[0], (int)s0[1], (int)s1[0], (int)s1[1]};
-        const int col = f0 + wrow_a + 32 * i + 16 * h;
-        __builtin_amdgcn_raw_buffer_store_b128(outv, rQ, col < N ? ml * N + col : KQ_OOB, 0, 0);
-      }
-    }
+    f8_gated_store<ACT, TN / 2, TM, C::WN, C::BM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1,
+                                                  N, out, oscales);
   }
 }
 
@@ -538,8 +547,236 @@ __device__ __forceinline__ int f8_remap(int pid, int n) {
   return pid < 8 * per ? (pid % 8) * per + pid / 8 : pid;
 }
 
-using F8Large = F8Cfg<2, 4, 4, 4, 1>;     // 256 x 256
-using F8Half = F8Cfg<2, 4, 2, 4, 1>;      // 256 x 128 tokens
+// ---------------------------------------------------------------------------------
+// Many tokens: tiles of 256 weight rows by 64 TM token rows on four wavefronts (2 x 2), each
+// 128 x 32 TM as 4 x TM blocks of 32 x 32 (TM = 4: 256 float32 accumulators a lane).  A stage is
+// 128 k, two matrix instructions deep, its rows eight 16-byte chunks, so that a load takes whole
+// cache lines: 8 rows x 128 bytes.  With stages of 64 k each line is asked for twice, and with
+// every compute unit at work the level-2 caches' request rate bound the loop (4096 x 4096 x 11008:
+// 161 against 137 us).  Rows are XOR-swizzled so that the fragment reads hit distinct banks.
+// A stage goes in two halves of 64 k, 4 TM products each.  First half: the second half's fragments
+// are read under the first products; a barrier then frees the stage's slot, and half of the loads
+// of the stage after next go into it.  Second half: the other loads, and the next stage's first
+// fragments, for which the wait and barrier between the halves made that stage visible (its loads
+// are older than the half just issued).
+// What bounds it: the chip's power.  In the loop the products take 2050 of 2300 (K = 4096) to
+// 2550 (K = 11008) cycles of a whole tile's stage, at a clock of 1.67 to 1.78 GHz; alone on eight
+// compute units the same loop runs at 2.4 GHz.
+template <int TM_>
+struct F8Big {
+  static constexpr int TM = TM_, BM = 64 * TM;
+  static constexpr int A_BYTES = 256 * 128, STAGE = A_BYTES + BM * 128;
+  static constexpr int SC_OFF = 2 * STAGE;                     // two sets of 16 groups' bytes, 256 + BM rows
+  static constexpr int SC_BYTES = (256 + BM) * 16;
+  static constexpr int BIAS_OFF = SC_OFF + 2 * SC_BYTES;       // 64 lanes x 16 bytes (256 biases used)
+  static constexpr int TOP_OFF = BIAS_OFF + 1024;              // gated: 2 x BM maxima
+  static constexpr int LDS = TOP_OFF + 2 * BM * 4;             // TM = 4: 150528 bytes
+};
+
+template <int ACT, bool BF16, class C>
+__device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
+                                            const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
+                                            const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
+                                            const uint16_t* __restrict__ bias, uint8_t* __restrict__ out,
+                                            uint8_t* __restrict__ oscales, int64_t m0, int n0) {
+  constexpr bool GATED = ACT >= 0;
+  constexpr int TM = C::TM, NB = 2 * TM, NL = 8 + NB;          // loads (8 rows) of a wave and stage
+  constexpr int NM = 4 * TM, NR = 2 * (4 + TM);                // products and reads of a half
+  // the thread index, hidden from the compiler, so that it does not keep every lane-dependent
+  // offset live across the tile loop
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wid & 1, wm = wid >> 1;
+  const int l32 = lane & 31, h = lane >> 5;
+  const int SC = (int)f8_scale_cols(K), T = (K + 127) / 128;
+
+  // wave w stages weight rows 64 w .. of the tile (gated: waves 0, 1 gate, 2, 3 up) and token rows
+  // 8 NB w ..; the first waves also the scales of 64 token rows each
+  const int64_t arow = GATED ? (int64_t)(wid >> 1) * N + (n0 >> 1) + 64 * (wid & 1) : (int64_t)n0 + 64 * wid;
+  const int64_t aleft = GATED ? N - (n0 >> 1) - 64 * (wid & 1) : N - n0 - 64 * wid;
+  const v4i rA = rsrc_words(wcodes + arow * K, aleft * K);
+  const v4i rAS = rsrc_words(wscales + arow * SC, aleft * SC);
+  const int64_t mleft = min(M - m0, (int64_t)C::BM);
+  const v4i rB = rsrc_words(xcodes + m0 * K, mleft * K);
+  const v4i rBS = rsrc_words(xscales + m0 * SC, mleft * SC);
+
+  const uint32_t lds0 = lds_addr(lds);
+  // a load's row and first byte of this lane; rows 8 .. 15 of each 16 have another swizzle
+  const int lrow = lane >> 3, lcol = 16 * ((lane ^ lrow) & 7);
+  // unsigned: an offset past the end is KQ_OOB plus at most 2^28 and stays past every range
+  const uint32_t ogA = lrow * K, ogB = (8 * NB * wid + lrow) * K;
+  auto k_off = [&](int p, int odd) -> uint32_t {
+    const int k = 128 * p + (lcol ^ (16 * odd));
+    return k < K ? k : KQ_OOB;
+  };
+  auto code_load = [&](int slot, uint32_t ko, int g) {         // load g (0 .. NL - 1) of a stage
+    const uint32_t st = lds0 + (uint32_t)(slot * C::STAGE);
+    if (g < 8) lds_load16(rA, st + (64 * wid + 8 * g) * 128, (int)(ogA + 8 * g * K + ko));
+    else lds_load16(rB, st + C::A_BYTES + (8 * NB * wid + 8 * (g - 8)) * 128, (int)(ogB + 8 * (g - 8) * K + ko));
+  };
+  // scale bytes of stages 16 grp .. 16 grp + 15, issued only when skip is zero, by the waves that
+  // have rows: the branches are inside the assembly so that the loop body stays one block for
+  // the scheduler.  A row's last piece may run into the next row; those bytes are never used.
+  const uint32_t osc = lane * SC, oscb = (64 * wid + lane) * SC;
+  auto scale_loads = [&](int grp, int skip) {
+    const uint32_t sc = lds0 + (uint32_t)(C::SC_OFF + (grp & 1) * C::SC_BYTES + 16 * 64 * wid);
+    const uint32_t ko = 16 * grp < T ? 16 * grp : KQ_OOB;
+    asm volatile(
+        "s_cmp_lg_u32 %0, 0\n\t"
+        "s_cbranch_scc1 1f\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "buffer_load_dwordx4 %4, %6, 0 offen lds\n"
+        "1:\n\t"
+        "s_cmp_lg_u32 %1, 0\n\t"
+        "s_cbranch_scc1 2f\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "buffer_load_dwordx4 %5, %7, 0 offen lds\n"
+        "2:"
+        :: "s"(__builtin_amdgcn_readfirstlane(skip)), "s"(__builtin_amdgcn_readfirstlane(wid < C::BM / 64 ? skip : 1)),
+           "s"(__builtin_amdgcn_readfirstlane(sc)), "s"(__builtin_amdgcn_readfirstlane(sc + 256 * 16)), "v"(osc + ko),
+           "v"(oscb + ko), "s"(rAS), "s"(rBS)
+        : "memory", "m0", "scc");
+  };
+
+  // weight block i of a wavefront is staged row wrow_a + 32 blk(i) ..: gated blocks 0, 1 are its
+  // gate rows, 2, 3 the up rows of the same columns, 128 rows on
+  auto blk = [](int i) { return GATED ? 4 * (i >> 1) + (i & 1) : i; };
+  const int wrow_a = (GATED ? 64 : 128) * wn, wrow_b = 32 * TM * wm;
+  const int sw = (l32 ^ (l32 >> 3 & 1)) & 7;                   // the same for every block of 32 rows
+  const int fa = (wrow_a + l32) * 128, fb = C::A_BYTES + (wrow_b + l32) * 128;
+  // half fragment q (0 .. NR - 1) of half c of a stage: a lane's 32 values of the half's 64 k are
+  // chunks h and 2 + h of its four
+  auto read_half = [&](const uint8_t* st, int c, int q, v8i* a, v8i* b) {
+    const int f = q >> 1, chunk = 16 * ((4 * c + 2 * (q & 1) + h) ^ sw);
+    const v4i v = *reinterpret_cast<const v4i*>(st + (f < 4 ? fa + 4096 * blk(f) : fb + 4096 * (f - 4)) + chunk);
+    v8i& d = f < 4 ? a[f] : b[f - 4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[4 * (q & 1) + e] = v[e];
+  };
+  const int sa_at = 16 * (wrow_a + l32), sb_at = 256 * 16 + 16 * (wrow_b + l32);
+  auto read_scale = [&](int p, int q) -> int {                 // scale of fragment q for a stage
+    const uint8_t* sc = lds + C::SC_OFF + ((p >> 4) & 1) * C::SC_BYTES + (p & 15);
+    return sc[q < 4 ? sa_at + 512 * blk(q) : sb_at + 512 * (q - 4)];
+  };
+
+  v16f acc[4][TM];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  if (!GATED && wid == 0) {                                    // without a bias, or past N: zeros
+    const v4i rW = rsrc_words(bias + n0, bias ? (int64_t)(N - n0) * 2 : 0);
+    lds_load16(rW, lds0 + C::BIAS_OFF, lane < 32 ? 16 * lane : KQ_OOB);
+  }
+  scale_loads(0, 0);
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int g = 0; g < NL; ++g) code_load(p, k_off(p, g & 1), g);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(NL));                  // biases, scales and stage 0
+  lds_barrier();
+  constexpr int ND = NM * 3 / 8, NE = NM * 3 / 4;              // products that the reads are spread under
+  v8i a[2][4], b[2][TM];
+  int s[4 + TM], ns[4 + TM];
+#pragma unroll
+  for (int q = 0; q < 4 + TM; ++q) s[q] = read_scale(0, q);
+#pragma unroll
+  for (int q = 0; q < NR; ++q) read_half(lds, 0, q, a[0], b[0]);
+  for (int p = 0; p < T; ++p) {
+    const int slot = p & 1;
+    const uint8_t* const cur = lds + slot * C::STAGE;
+    const uint8_t* const nxt = lds + (slot ^ 1) * C::STAGE;
+    uint32_t ko[2];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const int i = m / TM, j = m % TM;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[0][i], b[0][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (m < ND) {
+#pragma unroll
+        for (int q = NR * m / ND; q < NR * (m + 1) / ND; ++q) read_half(cur, 1, q, a[1], b[1]);
+      }
+      if (m == NM / 2 - 1) {
+        lds_barrier();
+        scale_loads((p >> 4) + 1, p & 15);
+        ko[0] = k_off(p + 2, 0);
+        ko[1] = k_off(p + 2, 1);
+      }
+      if (m >= NM / 2) {
+#pragma unroll
+        for (int g = NL * (m - NM / 2) / NM; g < NL * (m + 1 - NM / 2) / NM; ++g) code_load(slot, ko[g & 1], g);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(NL / 2));
+    lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const int i = m / TM, j = m % TM;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[1][i], b[1][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (m < NE) {
+#pragma unroll
+        for (int q = NR * m / NE; q < NR * (m + 1) / NE; ++q) read_half(nxt, 0, q, a[0], b[0]);
+#pragma unroll
+        for (int q = (4 + TM) * m / NE; q < (4 + TM) * (m + 1) / NE; ++q) ns[q] = read_scale(p + 1, q);
+      }
+      if (m < NM / 2) {
+#pragma unroll
+        for (int g = NL / 2 + NL * m / NM; g < NL / 2 + NL * (m + 1) / NM; ++g) code_load(slot, ko[g & 1], g);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int q = 0; q < 4 + TM; ++q) s[q] = ns[q];
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));                   // no load may land in LDS after this tile
+
+  if constexpr (!GATED) {
+    // Outputs go through the slots, which a token's columns leave in whole cache lines: a lane
+    // holds four columns of one token, and stored as they are the 64 lanes of a store touch 32
+    // rows.  A wave's 32 TM tokens x 128 columns, rows of 16 chunks swizzled by the row, the halves
+    // of a chunk swapped in rows 16 .. 31 of each 32 (a write's 32 lanes hit every bank).  (4096 x
+    // 4096 x 1024: 23.4 against 29.4 us.)
+    lds_barrier();                                             // every wave's loads have landed
+    uint8_t* const own = lds + wid * (32 * TM * 256);
+    const uint2* const bias_t = reinterpret_cast<const uint2*>(lds + C::BIAS_OFF);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint2 w = bias_t[(wrow_a + 32 * i + 8 * g + 4 * h) / 4];
+        const float b0 = unpack1_16<BF16>((uint16_t)(w.x & 0xFFFFu)), b1 = unpack1_16<BF16>((uint16_t)(w.x >> 16));
+        const float b2 = unpack1_16<BF16>((uint16_t)(w.y & 0xFFFFu)), b3 = unpack1_16<BF16>((uint16_t)(w.y >> 16));
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          const int row = 32 * j + l32;
+          uint2 o;
+          o.x = pack2_16<BF16>(acc[i][j][4 * g] + b0, acc[i][j][4 * g + 1] + b1);
+          o.y = pack2_16<BF16>(acc[i][j][4 * g + 2] + b2, acc[i][j][4 * g + 3] + b3);
+          *reinterpret_cast<uint2*>(own + row * 256 + 16 * ((4 * i + g) ^ (row & 15)) + 8 * (h ^ (l32 >> 4))) = o;
+        }
+      }
+    const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, mleft * N * 2);
+    const int c = lane & 15, col = n0 + wrow_a + 8 * c;
+#pragma unroll
+    for (int x = 0; x < 8 * TM; ++x) {
+      const int row = 4 * x + (lane >> 4);
+      v4i v = *reinterpret_cast<const v4i*>(own + row * 256 + 16 * (c ^ (row & 15)));
+      if (x >> 2 & 1) v = v4i{v.z, v.w, v.x, v.y};
+      __builtin_amdgcn_raw_buffer_store_b128(v, rY, col < N ? ((wrow_b + row) * N + col) * 2 : KQ_OOB, 0, 0);
+    }
+  } else {
+    f8_gated_store<ACT, 2, TM, 2, C::BM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out,
+                                         oscales);
+  }
+}
 
 // The first full_rows rows of 256-token tiles are whole tiles, grouped eight along M for reuse
 // in the level-2 caches; the rows below them are tiles of 128 tokens.  Each workgroup loops over
@@ -549,8 +786,7 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
     uint8_t* __restrict__ out, uint8_t* __restrict__ oscales, int full_rows) {
-  __shared__ __align__(16) uint8_t lds[F8Large::LDS];
-  static_assert(F8Half::LDS <= F8Large::LDS, "");
+  __shared__ __align__(16) uint8_t lds[F8Big<4>::LDS];
   const int tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256;
   const int nfull = tiles_n * full_rows;
   const int hrows = max(0, (int)((M + 127) / 128) - 2 * full_rows), nhalf = tiles_n * hrows;
@@ -559,12 +795,12 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
       constexpr int GM = 8;
       const int pid = f8_remap(t, nfull);
       const int first = pid / (GM * tiles_n) * GM, rows = min(full_rows - first, GM), in = pid % (GM * tiles_n);
-      f8_tile<ACT, BF16, F8Large>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                                  256LL * (first + in % rows), 256 * (in / rows));
+      f8_big_tile<ACT, BF16, F8Big<4>>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
+                                       256LL * (first + in % rows), 256 * (in / rows));
     } else {
       const int q = f8_remap(t - nfull, nhalf);
-      f8_tile<ACT, BF16, F8Half>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                                 256LL * full_rows + 128LL * (q % hrows), 256 * (q / hrows));
+      f8_big_tile<ACT, BF16, F8Big<2>>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
+                                       256LL * full_rows + 128LL * (q % hrows), 256 * (q / hrows));
     }
     __syncthreads();                         // the next tile's loads stay off what this one's epilogue reads
   }
@@ -620,8 +856,6 @@ static hipError_t gemm_launch(const uint8_t* xcodes, const uint8_t* xscales, int
   return hipGetLastError();
 }
 
-size_t f8_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-
 // The smallest tiles that give at most one workgroup per compute unit: fewer, larger tiles read
 // less, but a chain of k over few compute units is bound by what one of them can take in.
 template <bool BF16>
@@ -645,7 +879,7 @@ static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, i
 
 hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                             const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const void* bias, void* Y,
-                            void* workspace, hipStream_t s) {
+                            hipStream_t s) {
   const uint16_t* b = static_cast<const uint16_t*>(bias);
   uint8_t* y = static_cast<uint8_t*>(Y);
   return bf16 ? linear_launch<true>(xcodes, xscales, M, K, wcodes, wscales, N, b, y, s)

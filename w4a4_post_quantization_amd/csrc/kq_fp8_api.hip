@@ -54,14 +54,9 @@ kq_status kq_rmsnorm_quantize_fp8(int32_t dtype, const void* X, const void* resi
                                       stream));
 }
 
-size_t kq_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (check_rows(M, K) != KQ_OK || check_rows(1, N) != KQ_OK) return 0;
-  return f8_linear_workspace_bytes(M, N, K);
-}
-
 kq_status kq_fp8_linear(int32_t dtype, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                         const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const void* bias, void* Y,
-                        void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                        hipStream_t stream) {
   if (!xcodes || !xscales || !wcodes || !wscales || !Y) return KQ_ERR_NULL;
   if (!dtype_ok(dtype)) return KQ_ERR_UNSUPPORTED;
   kq_status st = check_rows(M, K);
@@ -69,11 +64,7 @@ kq_status kq_fp8_linear(int32_t dtype, const uint8_t* xcodes, const uint8_t* xsc
   if (st != KQ_OK) return st;
   if (!aligned(xcodes, 16) || !aligned(wcodes, 16) || !aligned(Y, 16) || !aligned(bias, 16)) return KQ_ERR_ALIGN;
   if (!aligned(xscales, 4) || !aligned(wscales, 4)) return KQ_ERR_ALIGN;
-  const size_t need = f8_linear_workspace_bytes(M, N, K);
-  if (need && (!workspace || workspace_bytes < need)) return KQ_ERR_WORKSPACE;
-  if (need && !aligned(workspace, 256)) return KQ_ERR_ALIGN;
-  return hip_status(launch_f8_linear(dtype == KQ_DT_BF16, xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, workspace,
-                                     stream));
+  return hip_status(launch_f8_linear(dtype == KQ_DT_BF16, xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, stream));
 }
 
 size_t kq_fp8_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) {
