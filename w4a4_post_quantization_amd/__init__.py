@@ -176,9 +176,15 @@ def lloyd_max_levels(n):
 
 # ------------------------------------------------------------------ marshalling helpers
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t):
@@ -599,7 +605,8 @@ def w4a4_linear_t(xcodes, xscales, wcodes, wscales, T=None, L2=None, mu=None, wb
 
 # ------------------------------------------------------------------------- the 8-bit path
 # One-token calls take 2 to 14 us on the GPU, so the host side is kept short: one combined test
-# per tensor (the named refusal is worked out only when it fails) and one library call.
+# per given tensor (the named refusal is worked out only when it fails), none for those made
+# here, and one library call.
 
 def _matrix(t, name):
     if not isinstance(t, _torch().Tensor) or t.dim() != 2:
@@ -626,10 +633,9 @@ def _same(t, name, dtype, shape, index):
     raise ValueError(f"{name} is on {t.device}, the first tensor on GPU {index}")
 
 
-def _call(name, index, stream, made, args):
+def _call(torch, name, index, stream, made, args):
     """One library call on `stream` (default: the current stream of the tensors' GPU, which is
     made the current device for the call if it is not)."""
-    torch = _torch()
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
     else:
@@ -654,16 +660,20 @@ def fp8_scale_cols(K):
     return (K + 511) // 512 * 4
 
 
-def _fp8_out(torch, rows, K, codes, scales, device, made):
-    index, cols = device.index, (K + 511) // 512 * 4
+def _fp8_out(torch, rows, K, codes, scales, index, made):
+    """codes and scales (made here where not given) and their addresses."""
     if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device)
+        codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=index)
         made.append(codes)
+        c = codes.data_ptr()
+    else:
+        c = _same(codes, "codes", torch.float8_e4m3fn, (rows, K), index)
+    cols = (K + 511) // 512 * 4
     if scales is None:
-        scales = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+        scales = torch.empty((rows, cols), dtype=torch.uint8, device=index)
         made.append(scales)
-    return (codes, scales, _same(codes, "codes", torch.float8_e4m3fn, (rows, K), index),
-            _same(scales, "scales", torch.uint8, (rows, cols), index))
+        return codes, scales, c, scales.data_ptr()
+    return codes, scales, c, _same(scales, "scales", torch.uint8, (rows, cols), index)
 
 
 def quantize_fp8(X, codes=None, scales=None, stream=None):
@@ -671,12 +681,12 @@ def quantize_fp8(X, codes=None, scales=None, stream=None):
     one per 128 values) of X (fp16 or bf16 [M][K], K a multiple of 16).  Also for weights
     [N][K], offline."""
     torch = _torch()
-    M, K = _matrix(X, "X")
-    dt = _dtype16(torch, X.dtype, "X")
-    device, made = X.device, []
-    x = _same(X, "X", X.dtype, X.shape, device.index if X.is_cuda else -1)
-    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, device, made)
-    _call("kq_quantize_fp8", device.index, stream, made, (dt, x, M, K, c, s))
+    shape = M, K = _matrix(X, "X")
+    dtype, index, made = X.dtype, X.get_device(), []
+    dt = _dtype16(torch, dtype, "X")
+    x = _same(X, "X", dtype, shape, index)
+    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, index, made)
+    _call(torch, "kq_quantize_fp8", index, stream, made, (dt, x, M, K, c, s))
     return codes, scales
 
 
@@ -686,42 +696,35 @@ def rmsnorm_quantize_fp8(X, gamma, eps=1e-6, residual=None, codes=None, scales=N
     scales, h rounded to the dtype); the last is None without a residual.  residual_out may be
     residual itself (updated in place)."""
     torch = _torch()
-    M, K = _matrix(X, "X")
-    dtype, device, made = X.dtype, X.device, []
+    shape = M, K = _matrix(X, "X")
+    dtype, index, made = X.dtype, X.get_device(), []
     dt = _dtype16(torch, dtype, "X")
-    index = device.index if X.is_cuda else -1
-    x = _same(X, "X", dtype, X.shape, index)
+    x = _same(X, "X", dtype, shape, index)
     g = _same(gamma, "gamma", dtype, (K,), index)
     r = o = None
-    if residual is not None:
-        r = _same(residual, "residual", dtype, (M, K), index)
+    if residual is None:
+        residual_out = None
+    else:
+        r = _same(residual, "residual", dtype, shape, index)
         if residual_out is None:
             residual_out = torch.empty_like(X)
             made.append(residual_out)
-        o = _same(residual_out, "residual_out", dtype, (M, K), index)
-    else:
-        residual_out = None
-    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, device, made)
-    _call("kq_rmsnorm_quantize_fp8", index, stream, made, (dt, x, r, g, eps, M, K, c, s, o))
+            o = residual_out.data_ptr()
+        else:
+            o = _same(residual_out, "residual_out", dtype, shape, index)
+    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, index, made)
+    _call(torch, "kq_rmsnorm_quantize_fp8", index, stream, made, (dt, x, r, g, eps, M, K, c, s, o))
     return codes, scales, residual_out
 
 
 def _fp8_operands(torch, xcodes, xscales, wcodes, wscales):
+    """M, N, K, the GPU and the addresses of both operands."""
     f8, u8 = torch.float8_e4m3fn, torch.uint8
-    M, K = _matrix(xcodes, "xcodes")
+    shape = M, K = _matrix(xcodes, "xcodes")
     N = _matrix(wcodes, "wcodes")[0]
-    index, cols = xcodes.device.index if xcodes.is_cuda else -1, (K + 511) // 512 * 4
-    return M, N, K, (_same(xcodes, "xcodes", f8, (M, K), index), _same(xscales, "xscales", u8, (M, cols), index)), \
-        (_same(wcodes, "wcodes", f8, (N, K), index), _same(wscales, "wscales", u8, (N, cols), index))
-
-
-def _fp8_workspace(torch, workspace, need, device, made):
-    if workspace is None:
-        if not need:
-            return None, 0
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-        made.append(workspace)
-    return _same(workspace, "workspace", torch.uint8, workspace.shape, device.index), workspace.numel()
+    index, cols = xcodes.get_device(), (K + 511) // 512 * 4
+    return (M, N, K, index, _same(xcodes, "xcodes", f8, shape, index), _same(xscales, "xscales", u8, (M, cols), index),
+            _same(wcodes, "wcodes", f8, (N, K), index), _same(wscales, "wscales", u8, (N, cols), index))
 
 
 def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, stream=None):
@@ -729,17 +732,19 @@ def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, 
     wcodes [N][K] float8_e4m3fn with their scale bytes (quantize_fp8); N a multiple of 16; bias
     [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16)."""
     torch = _torch()
-    M, N, K, x, w = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
+    M, N, K, index, x, xs, w, ws = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if dtype is None:
         dtype = Y.dtype if Y is not None else bias.dtype if bias is not None else torch.float16
     dt = _dtype16(torch, dtype, "dtype")
-    device, made = xcodes.device, []
-    b = None if bias is None else _same(bias, "bias", dtype, (N,), device.index)
+    made = []
+    b = None if bias is None else _same(bias, "bias", dtype, (N,), index)
     if Y is None:
-        Y = torch.empty((M, N), dtype=dtype, device=device)
+        Y = torch.empty((M, N), dtype=dtype, device=index)
         made.append(Y)
-    y = _same(Y, "Y", dtype, (M, N), device.index)
-    _call("kq_fp8_linear", device.index, stream, made, (dt, *x, M, K, *w, N, b, y))
+        y = Y.data_ptr()
+    else:
+        y = _same(Y, "Y", dtype, (M, N), index)
+    _call(torch, "kq_fp8_linear", index, stream, made, (dt, x, xs, M, K, w, ws, N, b, y))
     return Y
 
 
@@ -758,12 +763,20 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
     torch = _torch()
     if act not in _ACT:
         raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
-    M, N, K, x, w = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
+    M, N, K, index, x, xs, w, ws = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if N % 2:
         raise ValueError("wcodes must hold as many gate rows as up rows")
     F = N // 2
-    device, made = xcodes.device, []
-    codes, scales, c, s = _fp8_out(torch, M, F, codes, scales, device, made)
-    wk, nb = _fp8_workspace(torch, workspace, fp8_gated_linear_workspace_bytes(M, F, K), device, made)
-    _call("kq_fp8_gated_linear", device.index, stream, made, (_ACT[act], *x, M, K, *w, F, c, s, wk, nb))
+    made = []
+    codes, scales, c, s = _fp8_out(torch, M, F, codes, scales, index, made)
+    wk = nb = 0
+    if workspace is not None:
+        wk, nb = _same(workspace, "workspace", torch.uint8, workspace.shape, index), workspace.numel()
+    else:
+        nb = fp8_gated_linear_workspace_bytes(M, F, K)
+        if nb:
+            workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
+            made.append(workspace)
+            wk = workspace.data_ptr()
+    _call(torch, "kq_fp8_gated_linear", index, stream, made, (_ACT[act], x, xs, M, K, w, ws, F, c, s, wk or None, nb))
     return codes, scales
