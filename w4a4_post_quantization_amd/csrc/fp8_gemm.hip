@@ -235,8 +235,8 @@ static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int
 }
 
 // ---------------------------------------------------------------------------------
-// More tokens: tiles of BN weight rows by BM token rows on four wavefronts, WN along the
-// weights and 4 / WN along the tokens, each TN x TM blocks of 32 x 32.  The operands go from
+// Middling token counts, linear: tiles of 64 TN weight rows by 64 TM token rows on four wavefronts
+// (2 x 2), each TN x TM blocks of 32 x 32.  The operands go from
 // global memory straight into LDS, 64 k (one matrix instruction) a stage, NS stages deep; a
 // stage's row is four 16-byte chunks, XOR-swizzled so that the fragment reads (16 rows x one
 // chunk) and the staging writes hit distinct banks.  Lane l of half h = l / 32 takes chunks h
@@ -247,113 +247,40 @@ static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int
 // them.  Large tiles have enough products in one stage; for small ones a step of one stage would
 // be the latency of its fragment reads.
 // Scale bytes come 16 at a time for each row (2048 k, so seldom) into a double-buffered area.
-template <int WN_, int TN_, int TM_, int NS_, int G_>
-struct F8Cfg {
-  static constexpr int WN = WN_, WM = 4 / WN_, TN = TN_, TM = TM_, NS = NS_, G = G_;
-  static constexpr int BN = 32 * TN * WN, BM = 32 * TM * WM;
-  static constexpr int BROWS = BM < 64 ? 64 : BM;              // staged token rows (zeros past BM)
-  static constexpr int A_BYTES = BN * 64;
-  static constexpr int STAGE = A_BYTES + BROWS * 64;
-  static constexpr int SC_OFF = NS * STAGE;                    // two scale groups: BN + BROWS rows x 16 bytes
-  static constexpr int SC_BYTES = (BN + BROWS) * 16;
+template <int TN_, int TM_, int NS_, int G_>
+struct F8Small {
+  static constexpr int TN = TN_, TM = TM_, NS = NS_, G = G_;
+  static constexpr int BN = 64 * TN, BM = 64 * TM;
+  static constexpr int A_BYTES = BN * 64, STAGE = A_BYTES + BM * 64;
+  static constexpr int SC_OFF = NS * STAGE;                    // two sets of 16 groups' bytes, BN + BM rows
+  static constexpr int SC_BYTES = (BN + BM) * 16;
   static constexpr int BIAS_OFF = SC_OFF + 2 * SC_BYTES;       // 64 lanes x 16 bytes (BN biases used)
-  static constexpr int TOP_OFF = BIAS_OFF + 1024;              // gated: WN x BM maxima
-  static constexpr int LDS = TOP_OFF + WN * BM * 4;
+  static constexpr int LDS = BIAS_OFF + 1024;
 };
 
 __device__ __forceinline__ int f8_swz(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
 
-// The gated tiles' epilogue.  acc[0 .. TH - 1] are gates, acc[TH .. 2 TH - 1] the up values of the
-// same columns f0 + col0 + 32 i .., lane l's token of block j row0 + 32 j + l % 32.  Outputs in place
-// of the gates, the maximum of each token's columns in this wave to LDS, and after the barrier the
-// scale of all 128 (columns past F are zeros on both sides and stay zeros).
-template <int ACT, int TH, int TM, int WN, int BM>
-__device__ __forceinline__ void f8_gated_store(v16f (&acc)[2 * TH][TM], uint8_t* __restrict__ lds_tops, int wn, int col0,
-                                               int row0, int l32, int h, int64_t m0, int64_t mleft, int f0, int F,
-                                               uint8_t* __restrict__ out, uint8_t* __restrict__ oscales) {
-  uint32_t* const tops = reinterpret_cast<uint32_t*>(lds_tops);
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < TH; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float v = f8_act<ACT>(acc[i][j][e]) * acc[i + TH][j][e];
-        acc[i][j][e] = v;
-        top = umax32(top, abs_bits(v));
-      }
-    top = umax32(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    if (h == 0) tops[BM * wn + row0 + 32 * j + l32] = top;
-  }
-  lds_barrier();
-  const int OS = (int)f8_scale_cols(F), grp = f0 >> 7;
-  const __amdgpu_buffer_rsrc_t rQ = make_rsrc(out + m0 * F, mleft * F);
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int ml = row0 + 32 * j + l32;
-    uint32_t top = tops[ml];
-#pragma unroll
-    for (int v = 1; v < WN; ++v) top = umax32(top, tops[BM * v + ml]);
-    const uint32_t byte = f8_scale_byte(top);
-    const bool bad = byte == 255u;
-    const float inv = bad ? 1.0f : f8_inv_scale(byte);
-    if (wn == 0 && h == 0 && ml < mleft) {
-      uint8_t* const row = oscales + (m0 + ml) * OS;
-      row[grp] = (uint8_t)byte;
-      if (f0 + 128 >= F)
-        for (int q = grp + 1; q < OS; ++q) row[q] = 0;         // padding
-    }
-#pragma unroll
-    for (int i = 0; i < TH; ++i) {
-      uint32_t w[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint32_t c = f8_pack4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3], inv);
-        w[g] = bad ? 0x7F7F7F7Fu : c;
-      }
-      // dword g of half h is columns 8 g + 4 h .. + 3: swaps leave half h with 16 h .. + 15
-      const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-      const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-      const v4i outv = {(int)s0[0], (int)s0[1], (int)s1[0], (int)s1[1]};
-      const int col = f0 + col0 + 32 * i + 16 * h;
-      __builtin_amdgcn_raw_buffer_store_b128(outv, rQ, col < F ? ml * F + col : KQ_OOB, 0, 0);
-    }
-  }
-}
-
-// ACT -1: the linear, weight rows n0 .. n0 + BN - 1.  Gated (BN = 256): rows f0 .. f0 + 127 of
-// both halves, f0 = n0 / 2, staged gate rows first; wavefront column wn takes gate and up of the
-// same 16 TN columns, so that a lane has both factors of an output, and the tile's 128 columns
-// are one scale group.
-template <int ACT, bool BF16, class C>
-__device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
-                                        const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
-                                        const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
-                                        const uint16_t* __restrict__ bias, uint8_t* __restrict__ out,
-                                        uint8_t* __restrict__ oscales, int64_t m0, int n0) {
-  constexpr bool GATED = ACT >= 0;
+// Weight rows n0 .. n0 + BN - 1, token rows m0 .. m0 + BM - 1.
+template <bool BF16, class C>
+__device__ __forceinline__ void f8_small_tile(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
+                                              const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
+                                              const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
+                                              const uint16_t* __restrict__ bias, uint8_t* __restrict__ out, int64_t m0,
+                                              int n0) {
   constexpr int NS = C::NS, TN = C::TN, TM = C::TM, G = C::G;
-  constexpr int NA = C::BN / 64, NB = C::BROWS / 64, NL = NA + NB;   // loads (16 rows) of a wave and stage
+  constexpr int NA = TN, NB = TM, NL = NA + NB;                // loads (16 rows) of a wave and stage
   constexpr int NR = 2 * (TN + TM);                            // reads of 64 k
-  static_assert(!GATED || C::BN == 256, "a gated tile is one scale group wide");
-  // the thread index, hidden from the compiler, so that it does not keep every lane-dependent
-  // offset live across a tile loop
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
+  const int tid = threadIdx.x;
   const int lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wid % C::WN, wm = wid / C::WN;
+  const int wn = wid & 1, wm = wid >> 1;
   const int l32 = lane & 31, h = lane >> 5;
   const int SC = (int)f8_scale_cols(K);
   const int T = (K + 127) / 128;                               // groups (zeros past K)
 
-  // wave w stages weight rows 16 NA w .. of the tile (gated: waves 0, 1 gate, 2, 3 up) and token
-  // rows 16 NB w ..; the first waves also the scales of 64 rows each, in the same order
-  const int64_t arow = GATED ? (int64_t)(wid >> 1) * N + (n0 >> 1) + 64 * (wid & 1) : (int64_t)n0 + 16 * NA * wid;
-  const int64_t aleft = GATED ? N - (n0 >> 1) - 64 * (wid & 1) : N - n0 - 16 * NA * wid;
-  const int64_t srow = GATED ? arow : (int64_t)n0 + 64 * wid, sleft = GATED ? aleft : N - n0 - 64 * wid;
-  const v4i rA = rsrc_words(wcodes + arow * K, aleft * K);
-  const v4i rAS = rsrc_words(wscales + srow * SC, sleft * SC);
+  // wave w stages weight rows 16 NA w .. of the tile and token rows 16 NB w ..; the first waves also
+  // the scales of 64 rows each
+  const v4i rA = rsrc_words(wcodes + (int64_t)(n0 + 16 * NA * wid) * K, (int64_t)(N - n0 - 16 * NA * wid) * K);
+  const v4i rAS = rsrc_words(wscales + (int64_t)(n0 + 64 * wid) * SC, (int64_t)(N - n0 - 64 * wid) * SC);
   const int64_t mleft = min(M - m0, (int64_t)C::BM);
   const v4i rB = rsrc_words(xcodes + m0 * K, mleft * K);
   const v4i rBS = rsrc_words(xscales + m0 * SC, mleft * SC);
@@ -386,21 +313,19 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
         "s_mov_b32 m0, %3\n\t"
         "buffer_load_dwordx4 %5, %7, 0 offen lds\n"
         "2:"
-        :: "s"(__builtin_amdgcn_readfirstlane(wid < C::BN / 64 ? skip : 1)),
-           "s"(__builtin_amdgcn_readfirstlane(wid < C::BROWS / 64 ? skip : 1)), "s"(__builtin_amdgcn_readfirstlane(sc)),
+        :: "s"(__builtin_amdgcn_readfirstlane(wid < TN ? skip : 1)),
+           "s"(__builtin_amdgcn_readfirstlane(wid < TM ? skip : 1)), "s"(__builtin_amdgcn_readfirstlane(sc)),
            "s"(__builtin_amdgcn_readfirstlane(sc + C::BN * 16)), "v"(osc + ko), "v"(oscb + ko), "s"(rAS), "s"(rBS)
         : "memory", "m0", "scc");
   };
 
-  // weight block i of a wavefront is LDS rows wrow_a + 32 blk(i) ..
-  auto blk = [](int i) { return GATED ? 4 * (i / (TN / 2 > 0 ? TN / 2 : 1)) + i % (TN / 2 > 0 ? TN / 2 : 1) : i; };
-  const int wrow_a = (GATED ? 16 : 32) * TN * wn, wrow_b = 32 * TM * wm;
+  const int wrow_a = 32 * TN * wn, wrow_b = 32 * TM * wm;
   const int sw = f8_swz(l32);                                  // the same for every block of 32 rows
   const int fa = (wrow_a + l32) * 64, fb = C::A_BYTES + (wrow_b + l32) * 64;
   const int c0 = 16 * (h ^ sw), c1 = 16 * ((2 + h) ^ sw);
   auto read_half = [&](const uint8_t* st, int q, v8i* a, v8i* b) {   // half fragment q (0 .. NR - 1)
     const int f = q >> 1;
-    const v4i v = *reinterpret_cast<const v4i*>(st + (f < TN ? fa + 2048 * blk(f) : fb + 2048 * (f - TN)) + ((q & 1) ? c1 : c0));
+    const v4i v = *reinterpret_cast<const v4i*>(st + (f < TN ? fa + 2048 * f : fb + 2048 * (f - TN)) + ((q & 1) ? c1 : c0));
     v8i& d = f < TN ? a[f] : b[f - TN];
 #pragma unroll
     for (int e = 0; e < 4; ++e) d[4 * (q & 1) + e] = v[e];
@@ -408,7 +333,7 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
   const int sa_at = 16 * (wrow_a + l32), sb_at = C::BN * 16 + 16 * (wrow_b + l32);
   auto read_scale = [&](int grp, int q) -> int {               // scale of fragment q for a group of k
     const uint8_t* sc = lds + C::SC_OFF + ((grp >> 4) & 1) * C::SC_BYTES + (grp & 15);
-    return sc[q < TN ? sa_at + 512 * blk(q) : sb_at + 512 * (q - TN)];
+    return sc[q < TN ? sa_at + 512 * q : sb_at + 512 * (q - TN)];
   };
 
   v16f acc[TN][TM];
@@ -419,7 +344,7 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  if (!GATED && wid == 0) {                                    // without a bias, or past N: zeros
+  if (wid == 0) {                                    // without a bias, or past N: zeros
     const v4i rW = rsrc_words(bias + n0, bias ? (int64_t)(N - n0) * 2 : 0);
     lds_load16(rW, lds0 + C::BIAS_OFF, lane < C::BN / 8 ? 16 * lane : KQ_OOB);
   }
@@ -498,45 +423,40 @@ __device__ __forceinline__ void f8_tile(uint8_t* __restrict__ lds, const uint8_t
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));                   // no load may land in LDS after this tile
 
-  if constexpr (!GATED) {
-    const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, mleft * N * 2);
-    const uint32_t* const bias_t = reinterpret_cast<const uint32_t*>(lds + C::BIAS_OFF);
+  const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, mleft * N * 2);
+  const uint32_t* const bias_t = reinterpret_cast<const uint32_t*>(lds + C::BIAS_OFF);
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int ml = wrow_b + 32 * j + l32;
+  for (int j = 0; j < TM; ++j) {
+    const int ml = wrow_b + 32 * j + l32;
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
+    for (int i = 0; i < TN; ++i) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          uint32_t pk[2][2];
+      for (int p = 0; p < 2; ++p) {
+        uint32_t pk[2][2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int g = 2 * p + u;
-            float v[4];
+        for (int u = 0; u < 2; ++u) {
+          const int g = 2 * p + u;
+          float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
-            const uint32_t* const w = bias_t + (wrow_a + 32 * i + 8 * g + 4 * h) / 2;
-            const uint32_t w01 = w[0], w23 = w[1];
-            v[0] += unpack1_16<BF16>((uint16_t)(w01 & 0xFFFFu));
-            v[1] += unpack1_16<BF16>((uint16_t)(w01 >> 16));
-            v[2] += unpack1_16<BF16>((uint16_t)(w23 & 0xFFFFu));
-            v[3] += unpack1_16<BF16>((uint16_t)(w23 >> 16));
-            pk[u][0] = pack2_16<BF16>(v[0], v[1]);
-            pk[u][1] = pack2_16<BF16>(v[2], v[3]);
-          }
-          // a lane holds columns 8 g + 4 h .. + 3: one lane-half swap per dword leaves lanes
-          // 0 .. 31 with the eight columns of group 2 p and the others with those of 2 p + 1
-          const auto s0 = __builtin_amdgcn_permlane32_swap(pk[0][0], pk[1][0], false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(pk[0][1], pk[1][1], false, false);
-          const v4i outv = {(int)s0[0], (int)s1[0], (int)s0[1], (int)s1[1]};
-          const int col = n0 + wrow_a + 32 * i + 8 * (2 * p + h);
-          __builtin_amdgcn_raw_buffer_store_b128(outv, rY, col < N ? (ml * N + col) * 2 : KQ_OOB, 0, 0);
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+          const uint32_t* const w = bias_t + (wrow_a + 32 * i + 8 * g + 4 * h) / 2;
+          const uint32_t w01 = w[0], w23 = w[1];
+          v[0] += unpack1_16<BF16>((uint16_t)(w01 & 0xFFFFu));
+          v[1] += unpack1_16<BF16>((uint16_t)(w01 >> 16));
+          v[2] += unpack1_16<BF16>((uint16_t)(w23 & 0xFFFFu));
+          v[3] += unpack1_16<BF16>((uint16_t)(w23 >> 16));
+          pk[u][0] = pack2_16<BF16>(v[0], v[1]);
+          pk[u][1] = pack2_16<BF16>(v[2], v[3]);
         }
+        // a lane holds columns 8 g + 4 h .. + 3: one lane-half swap per dword leaves lanes
+        // 0 .. 31 with the eight columns of group 2 p and the others with those of 2 p + 1
+        const auto s0 = __builtin_amdgcn_permlane32_swap(pk[0][0], pk[1][0], false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(pk[0][1], pk[1][1], false, false);
+        const v4i outv = {(int)s0[0], (int)s1[0], (int)s0[1], (int)s1[1]};
+        const int col = n0 + wrow_a + 32 * i + 8 * (2 * p + h);
+        __builtin_amdgcn_raw_buffer_store_b128(outv, rY, col < N ? (ml * N + col) * 2 : KQ_OOB, 0, 0);
       }
     }
-  } else {
-    f8_gated_store<ACT, TN / 2, TM, C::WN, C::BM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1,
-                                                  N, out, oscales);
   }
 }
 
@@ -556,23 +476,81 @@ __device__ __forceinline__ int f8_remap(int pid, int n) {
 // 161 against 137 us).  Rows are XOR-swizzled so that the fragment reads hit distinct banks.
 // A stage goes in two halves of 64 k, 4 TM products each.  First half: the second half's fragments
 // are read under the first products; a barrier then frees the stage's slot, and half of the loads
-// of the stage after next go into it.  Second half: the other loads, and the next stage's first
-// fragments, for which the wait and barrier between the halves made that stage visible (its loads
-// are older than the half just issued).
+// of the stage NS on go into it.  Second half: the other loads, and the next stage's first
+// fragments, for which the wait and barrier between the halves made that stage visible.
 // What bounds it: the chip's power.  In the loop the products take 2050 of 2300 (K = 4096) to
 // 2550 (K = 11008) cycles of a whole tile's stage, at a clock of 1.67 to 1.78 GHz; alone on eight
 // compute units the same loop runs at 2.4 GHz.
-template <int TM_>
+template <int TM_, int NS_>
 struct F8Big {
-  static constexpr int TM = TM_, BM = 64 * TM;
+  static constexpr int TM = TM_, BM = 64 * TM, NS = NS_;       // NS slots
   static constexpr int A_BYTES = 256 * 128, STAGE = A_BYTES + BM * 128;
-  static constexpr int SC_OFF = 2 * STAGE;                     // two sets of 16 groups' bytes, 256 + BM rows
+  static constexpr int SC_OFF = NS * STAGE;                    // two sets of 16 groups' bytes, 256 + BM rows
   static constexpr int SC_BYTES = (256 + BM) * 16;
   static constexpr int BIAS_OFF = SC_OFF + 2 * SC_BYTES;       // 64 lanes x 16 bytes (256 biases used)
   static constexpr int TOP_OFF = BIAS_OFF + 1024;              // gated: 2 x BM maxima
-  static constexpr int LDS = TOP_OFF + 2 * BM * 4;             // TM = 4: 150528 bytes
+  static constexpr int LDS = TOP_OFF + 2 * BM * 4;             // TM, NS = 4, 2: 150528 bytes; 2, 3: 161792
 };
 
+// The gated tiles' epilogue.  acc[0], acc[1] are gates, acc[2], acc[3] the up values of the
+// same columns f0 + col0 + 32 i .., lane l's token of block j row0 + 32 j + l % 32.  Outputs in place
+// of the gates, the maximum of each token's columns in this wave to LDS, and after the barrier the
+// scale of all 128 (columns past F are zeros on both sides and stay zeros).
+template <int ACT, int TM>
+__device__ __forceinline__ void f8_gated_store(v16f (&acc)[4][TM], uint8_t* __restrict__ lds_tops, int wn, int col0,
+                                               int row0, int l32, int h, int64_t m0, int64_t mleft, int f0, int F,
+                                               uint8_t* __restrict__ out, uint8_t* __restrict__ oscales) {
+  uint32_t* const tops = reinterpret_cast<uint32_t*>(lds_tops);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float v = f8_act<ACT>(acc[i][j][e]) * acc[i + 2][j][e];
+        acc[i][j][e] = v;
+        top = umax32(top, abs_bits(v));
+      }
+    top = umax32(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    if (h == 0) tops[64 * TM * wn + row0 + 32 * j + l32] = top;
+  }
+  lds_barrier();
+  const int OS = (int)f8_scale_cols(F), grp = f0 >> 7;
+  const __amdgpu_buffer_rsrc_t rQ = make_rsrc(out + m0 * F, mleft * F);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int ml = row0 + 32 * j + l32;
+    const uint32_t byte = f8_scale_byte(umax32(tops[ml], tops[64 * TM + ml]));
+    const bool bad = byte == 255u;
+    const float inv = bad ? 1.0f : f8_inv_scale(byte);
+    if (wn == 0 && h == 0 && ml < mleft) {
+      uint8_t* const row = oscales + (m0 + ml) * OS;
+      row[grp] = (uint8_t)byte;
+      if (f0 + 128 >= F)
+        for (int q = grp + 1; q < OS; ++q) row[q] = 0;         // padding
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t c = f8_pack4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3], inv);
+        w[g] = bad ? 0x7F7F7F7Fu : c;
+      }
+      // dword g of half h is columns 8 g + 4 h .. + 3: swaps leave half h with 16 h .. + 15
+      const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+      const v4i outv = {(int)s0[0], (int)s0[1], (int)s1[0], (int)s1[1]};
+      const int col = f0 + col0 + 32 * i + 16 * h;
+      __builtin_amdgcn_raw_buffer_store_b128(outv, rQ, col < F ? ml * F + col : KQ_OOB, 0, 0);
+    }
+  }
+}
+
+// ACT -1: the linear, weight rows n0 .. n0 + 255.  Gated: rows f0 .. f0 + 127 of both halves, f0 =
+// n0 / 2, staged gate rows first; wavefront column wn takes gate and up of the same 64 columns, so
+// that a lane has both factors of an output, and the tile's 128 columns are one scale group.
 template <int ACT, bool BF16, class C>
 __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
                                             const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
@@ -580,7 +558,7 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
                                             const uint16_t* __restrict__ bias, uint8_t* __restrict__ out,
                                             uint8_t* __restrict__ oscales, int64_t m0, int n0) {
   constexpr bool GATED = ACT >= 0;
-  constexpr int TM = C::TM, NB = 2 * TM, NL = 8 + NB;          // loads (8 rows) of a wave and stage
+  constexpr int NS = C::NS, TM = C::TM, NB = 2 * TM, NL = 8 + NB;   // NL loads (8 rows) of a wave and stage
   constexpr int NM = 4 * TM, NR = 2 * (4 + TM);                // products and reads of a half
   // the thread index, hidden from the compiler, so that it does not keep every lane-dependent
   // offset live across the tile loop
@@ -674,10 +652,10 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
   }
   scale_loads(0, 0);
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
+  for (int p = 0; p < NS; ++p)
 #pragma unroll
     for (int g = 0; g < NL; ++g) code_load(p, k_off(p, g & 1), g);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(NL));                  // biases, scales and stage 0
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 1) * NL));       // biases, scales and stage 0
   lds_barrier();
   constexpr int ND = NM * 3 / 8, NE = NM * 3 / 4;              // products that the reads are spread under
   v8i a[2][4], b[2][TM];
@@ -686,10 +664,10 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
   for (int q = 0; q < 4 + TM; ++q) s[q] = read_scale(0, q);
 #pragma unroll
   for (int q = 0; q < NR; ++q) read_half(lds, 0, q, a[0], b[0]);
+  int slot = 0, after = 1;                                     // of stages p and p + 1
   for (int p = 0; p < T; ++p) {
-    const int slot = p & 1;
     const uint8_t* const cur = lds + slot * C::STAGE;
-    const uint8_t* const nxt = lds + (slot ^ 1) * C::STAGE;
+    const uint8_t* const nxt = lds + after * C::STAGE;
     uint32_t ko[2];
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -704,8 +682,8 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
       if (m == NM / 2 - 1) {
         lds_barrier();
         scale_loads((p >> 4) + 1, p & 15);
-        ko[0] = k_off(p + 2, 0);
-        ko[1] = k_off(p + 2, 1);
+        ko[0] = k_off(p + NS, 0);
+        ko[1] = k_off(p + NS, 1);
       }
       if (m >= NM / 2) {
 #pragma unroll
@@ -713,7 +691,7 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(NL / 2));
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 2) * NL + NL / 2));
     lds_barrier();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -735,6 +713,8 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
     }
 #pragma unroll
     for (int q = 0; q < 4 + TM; ++q) s[q] = ns[q];
+    slot = after;
+    after = after + 1 == NS ? 0 : after + 1;
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));                   // no load may land in LDS after this tile
 
@@ -773,10 +753,14 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
       __builtin_amdgcn_raw_buffer_store_b128(v, rY, col < N ? ((wrow_b + row) * N + col) * 2 : KQ_OOB, 0, 0);
     }
   } else {
-    f8_gated_store<ACT, 2, TM, 2, C::BM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out,
+    f8_gated_store<ACT, TM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out,
                                          oscales);
   }
 }
+
+using F8Large = F8Big<4, 2>;     // 256 x 256
+using F8Half = F8Big<2, 3>;      // 256 x 128 tokens
+using F8Low = F8Big<1, 3>;       // 256 x 64 tokens
 
 // The first full_rows rows of 256-token tiles are whole tiles, grouped eight along M for reuse
 // in the level-2 caches; the rows below them are tiles of 128 tokens.  Each workgroup loops over
@@ -786,7 +770,7 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
     uint8_t* __restrict__ out, uint8_t* __restrict__ oscales, int full_rows) {
-  __shared__ __align__(16) uint8_t lds[F8Big<4>::LDS];
+  __shared__ __align__(16) uint8_t lds[F8Large::LDS > F8Half::LDS ? F8Large::LDS : F8Half::LDS];
   const int tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256;
   const int nfull = tiles_n * full_rows;
   const int hrows = max(0, (int)((M + 127) / 128) - 2 * full_rows), nhalf = tiles_n * hrows;
@@ -795,39 +779,38 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
       constexpr int GM = 8;
       const int pid = f8_remap(t, nfull);
       const int first = pid / (GM * tiles_n) * GM, rows = min(full_rows - first, GM), in = pid % (GM * tiles_n);
-      f8_big_tile<ACT, BF16, F8Big<4>>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
+      f8_big_tile<ACT, BF16, F8Large>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
                                        256LL * (first + in % rows), 256 * (in / rows));
     } else {
       const int q = f8_remap(t - nfull, nhalf);
-      f8_big_tile<ACT, BF16, F8Big<2>>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
+      f8_big_tile<ACT, BF16, F8Half>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
                                        256LL * full_rows + 128LL * (q % hrows), 256 * (q / hrows));
     }
     __syncthreads();                         // the next tile's loads stay off what this one's epilogue reads
   }
 }
 
-// One tile of configuration C per workgroup.
-template <int ACT, bool BF16, class C>
+template <bool BF16, class C>
 __global__ __launch_bounds__(256, 1) void f8_small_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
-    uint8_t* __restrict__ out, uint8_t* __restrict__ oscales) {
+    uint8_t* __restrict__ out) {
   __shared__ __align__(16) uint8_t lds[C::LDS];
-  const int rows = (int)((M + C::BM - 1) / C::BM);
-  const int pid = f8_remap(blockIdx.x, gridDim.x);
-  f8_tile<ACT, BF16, C>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, (int64_t)C::BM * (pid % rows),
-                        C::BN * (pid / rows));
+  const int rows = (int)((M + C::BM - 1) / C::BM), pid = f8_remap(blockIdx.x, gridDim.x);
+  f8_small_tile<BF16, C>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, (int64_t)C::BM * (pid % rows),
+                         C::BN * (pid / rows));
 }
 
-template <int ACT, bool BF16, class C>
-static hipError_t small_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
-                               const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
-                               uint8_t* out, uint8_t* oscales, hipStream_t s) {
-  const int64_t cols = ACT >= 0 ? C::BN / 2 : C::BN;
-  const int64_t grid = (N + cols - 1) / cols * ((M + C::BM - 1) / C::BM);
-  hipLaunchKernelGGL((f8_small_kernel<ACT, BF16, C>), dim3((unsigned)grid), dim3(256), 0, s, wcodes, wscales, xcodes,
-                     xscales, M, (int)N, (int)K, bias, out, oscales);
-  return hipGetLastError();
+// Tiles of 256 x 64 tokens, one per workgroup: a gated call's middling token counts.
+template <int ACT>
+__global__ __launch_bounds__(256, 1) void f8_low_kernel(
+    const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
+    const uint8_t* __restrict__ xscales, int64_t M, int N, int K, uint8_t* __restrict__ out,
+    uint8_t* __restrict__ oscales) {
+  __shared__ __align__(16) uint8_t lds[F8Low::LDS];
+  const int rows = (int)((M + F8Low::BM - 1) / F8Low::BM), pid = f8_remap(blockIdx.x, gridDim.x);
+  f8_big_tile<ACT, false, F8Low>(lds, wcodes, wscales, xcodes, xscales, M, N, K, nullptr, out, oscales,
+                                 (int64_t)F8Low::BM * (pid % rows), 256 * (pid / rows));
 }
 
 template <int ACT, bool BF16>
@@ -865,16 +848,19 @@ static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, i
   if (M <= ROWS_LINEAR) return rows_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
   const int64_t cus = device_cu_count();
   auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
-#define KQ_TILE(...) \
-  small_launch<-1, BF16, F8Cfg<__VA_ARGS__>>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s)
+#define KQ_TILE(...)                                                                                                \
+  hipLaunchKernelGGL((f8_small_kernel<BF16, F8Small<__VA_ARGS__>>),                                                  \
+                     dim3((unsigned)tiles(F8Small<__VA_ARGS__>::BN, F8Small<__VA_ARGS__>::BM)), dim3(256), 0, s,     \
+                     wcodes, wscales, xcodes, xscales, M, (int)N, (int)K, bias, Y)
   // measured (us) at 4096 x 4096 with 64 x 64 / 128 x 64 / 128 x 128 / 256 x 256: 200 tokens 12.0 /
   // 15.1 / 18.0 / 27.6, 512 tokens 18.4 / 16.4 / 18.9 / 29.0, 1024 tokens 33.6 / 30.6 / 22.5 / 30.5,
   // 2048 tokens 79 / 60 / 43 / 39
-  if (tiles(64, 64) <= cus) return KQ_TILE(2, 1, 1, 8, 2);
-  if (tiles(128, 64) <= cus) return KQ_TILE(2, 2, 1, 8, 2);
-  if (tiles(128, 128) <= cus) return KQ_TILE(2, 2, 2, 4, 1);
+  if (tiles(64, 64) <= cus) KQ_TILE(1, 1, 8, 2);
+  else if (tiles(128, 64) <= cus) KQ_TILE(2, 1, 8, 2);
+  else if (tiles(128, 128) <= cus) KQ_TILE(2, 2, 4, 1);
+  else return gemm_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
 #undef KQ_TILE
-  return gemm_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
+  return hipGetLastError();
 }
 
 hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
@@ -899,14 +885,15 @@ static hipError_t gated_launch(const uint8_t* xcodes, const uint8_t* xscales, in
     if (e != hipSuccess) return e;
     return launch_f8_quantize_f32(static_cast<const float*>(workspace), M, F, codes, scales, s);
   }
-  const int64_t cols = (F + 127) / 128, cus = device_cu_count();
-#define KQ_TILE(...) \
-  small_launch<ACT, false, F8Cfg<__VA_ARGS__>>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s)
-  // as the linear's rule; measured (us) with 32 / 64 / 128 tokens a tile: 64 tokens, 11008 x 4096 31 /
-  // 36 / 35; 128 tokens 52 / 34 / 37; 203 tokens 73 / 56 / 37; 203 tokens, 5600 x 2240 29 / 18 / 21
-  if (cols * ((M + 31) / 32) <= cus) return KQ_TILE(4, 2, 1, 6, 1);
-  if (cols * ((M + 63) / 64) <= cus) return KQ_TILE(2, 4, 1, 6, 1);
-#undef KQ_TILE
+  // 64 tokens a tile while that is at most one workgroup per compute unit; measured (us) with 64 / 128
+  // / 256 tokens: 128 tokens, 11008 x 4096 26.6 / 30.9 / 37; 203 tokens 45 / 30 / 37; 203 tokens, 5600 x
+  // 2240 15.2 / 18.7 / 21
+  const int64_t tiles = (F + 127) / 128 * ((M + F8Low::BM - 1) / F8Low::BM);
+  if (tiles <= device_cu_count()) {
+    hipLaunchKernelGGL((f8_low_kernel<ACT>), dim3((unsigned)tiles), dim3(256), 0, s, wcodes, wscales, xcodes, xscales, M,
+                       (int)F, (int)K, codes, scales);
+    return hipGetLastError();
+  }
   return gemm_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
 }
 
