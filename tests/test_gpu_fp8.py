@@ -3,9 +3,8 @@
 Tolerances, derived before the first run (u = 2^-24, half a float32 step):
   quantizer   16-bit inputs, a power-of-two scale and one rounding: every byte equal.
   norm        h carries one rounding; the sum of K squares is a chain of at most 8 * 8 fused
-              products and 6 + 16 additions, halved by the root; mean, eps, root, reciprocal
-              and two products round once each: relative error below (1 + 43 + 7) u of y,
-              taken as 64 u.  The residual is one float32 sum rounded once more: equal bits.
+              products (then float64), halved by the root; the factor and two products round
+              once each: relative error below (1 + 32 + 3) u of y, taken as 64 u.  The residual is one float32 sum rounded once more: equal bits.
   linear      on small whole numbers with small power-of-two scales every partial sum is exact
               in float32, so the output is the exact value rounded once: every bit equal.  On
               random values each of the K additions rounds or truncates at 24 bits: K 2^-23 of
@@ -156,6 +155,20 @@ def test_norm_residual_in_place(kq):
     c1, s1, h1 = kq.rmsnorm_quantize_fp8(x, gamma, residual=h, residual_out=h)
     assert h1 is h and torch.equal(h, out)
     assert torch.equal(c0.view(torch.uint8), c1.view(torch.uint8)) and torch.equal(s0, s1)
+
+
+def test_norm_more_rows_than_a_grid(kq):
+    """More rows than workgroups: every row of the last turn is there."""
+    M, K = (1 << 22) + 1000, 32
+    x = torch.ones(M, K, dtype=torch.float16, device="cuda")
+    tail = _act_data(1003, K, "fp16", 6)
+    x[-1003:] = tail.cuda()
+    gamma = torch.full((K,), 0.5, dtype=torch.float16, device="cuda")
+    codes, scales, _ = kq.rmsnorm_quantize_fp8(x, gamma)
+    _, y = fp8.rmsnorm(_np(tail), None, np.full(K, 0.5), float(np.float32(1e-6)))
+    assert not fp8.check_codes(_bytes(codes[-1003:]), _bytes(scales[-1003:]), y, 64 * U * np.abs(y))
+    # rows of ones: 0.5 / sqrt(1 + 1e-6) is 256 2^-9 to within a code
+    assert torch.all(codes[:-1003].view(torch.uint8) == 0x78) and torch.all(scales[:-1003, 0] == 127 - 9)
 
 
 def test_norm_special_rows(kq):
@@ -379,6 +392,22 @@ def test_block_same_bits_every_time_and_on_another_stream(kq, M):
     for r in runs:
         for a, b in zip(first, r):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_two_blocks_at_once(kq):
+    """Two blocks in flight on two streams, each with its own workspaces, do not disturb each
+    other."""
+    w = _block_weights(kq, 512, 2064, 2)
+    args = [(_act_data(9 + k, 512, "bf16", k).cuda(), _act_data(9 + k, 512, "bf16", 20 + k).cuda()) for k in range(2)]
+    refs = [_block(kq, *a, w) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        outs = [_block(kq, *a, w, stream=s) for a, s in zip(args, streams)]
+        torch.cuda.synchronize()
+        for ref, out in zip(refs, outs):
+            for a, b in zip(ref, out):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 @pytest.mark.parametrize("M", [1, 70, 300])

@@ -76,74 +76,87 @@ hipError_t launch_f8_quantize_f32(const float* X, int64_t M, int64_t K, uint8_t*
   return quantize_launch<2>(X, M, K, codes, scales, s);
 }
 
-// One row per NT threads; thread t holds columns 8 (v NT + t) .. + 7 for v < VPT in float32.
-// h is normalized as summed in float32; only the stored residual is rounded to 16 bits.
+// 1 / sqrt(x) from the hardware's estimate (good to a step) by one Newton step in float64: with the
+// sum joined in float64 too, the factor of a whole row is off by its own rounding alone.
+__device__ __forceinline__ float f8_rsqrt(double x) {
+  const float r0 = __builtin_amdgcn_rsqf((float)x);
+  if (!(r0 > 0.0f && r0 < INFINITY)) return r0;                // of infinity, zero or NaN
+  const double r = (double)r0;
+  return (float)fma(0.5 * r, fma(-x * r, r, 1.0), r);
+}
+
+// One row per NT threads at a time; thread t holds columns 8 (v NT + t) .. + 7 for v < VPT in
+// float32.  h is normalized as summed in float32; only the stored residual is rounded to 16 bits.
+// A lane's squares are a float32 chain, the lanes' sums are joined in float64.
 template <bool BF16, bool RES, int NT, int VPT>
 __global__ __launch_bounds__(NT) void f8_rmsnorm_kernel(const uint8_t* __restrict__ X,
                                                         const uint8_t* residual,
-                                                        const uint8_t* __restrict__ gamma, float eps, int K,
+                                                        const uint8_t* __restrict__ gamma, float eps, int64_t M, int K,
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                                         uint8_t* residual_out) {
   const int t = threadIdx.x, lane = t & 63;
-  const int64_t row = blockIdx.x;
-  float h[VPT][8];
-  float sq = 0.0f;
+  __shared__ double part[NT / 64];
+  for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
+    float h[VPT][8];
+    float sq = 0.0f;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int col = 8 * (v * NT + t);
-    v4u a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-    if (col < K) {
-      a = *reinterpret_cast<const v4u*>(X + (row * K + col) * 2);
-      if (RES) b = *reinterpret_cast<const v4u*>(residual + (row * K + col) * 2);
-    }
-    unpack8_16<BF16>(a, h[v]);
-    if (RES) {
-      float r[8];
-      unpack8_16<BF16>(b, r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] += r[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(h[v][i], h[v][i], sq);
-  }
-  sq = wave_sum(sq);
-  if (NT > 64) {
-    __shared__ float part[NT / 64];
-    if (lane == 0) part[t >> 6] = sq;
-    __syncthreads();
-    sq = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NT / 64; ++w) sq += part[w];
-  }
-  const float rinv = 1.0f / sqrtf(sq / (float)K + eps);
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int col = 8 * (v * NT + t);
-    if (512 * ((v * NT + t) >> 6) >= K) break;               // the whole wavefront is past the row
-    v4u gw = {0, 0, 0, 0};
-    if (col < K) {
-      gw = *reinterpret_cast<const v4u*>(gamma + col * 2);
-      if (RES) {
-        const v4u o = {pack2_16<BF16>(h[v][0], h[v][1]), pack2_16<BF16>(h[v][2], h[v][3]),
-                       pack2_16<BF16>(h[v][4], h[v][5]), pack2_16<BF16>(h[v][6], h[v][7])};
-        *reinterpret_cast<v4u*>(residual_out + (row * K + col) * 2) = o;
+    for (int v = 0; v < VPT; ++v) {
+      const int col = 8 * (v * NT + t);
+      v4u a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+      if (col < K) {
+        a = *reinterpret_cast<const v4u*>(X + (row * K + col) * 2);
+        if (RES) b = *reinterpret_cast<const v4u*>(residual + (row * K + col) * 2);
       }
-    }
-    float g[8], y[8];
-    unpack8_16<BF16>(gw, g);
-    // lanes past K: 0 times a possibly infinite rinv is not to reach the group's maximum
+      unpack8_16<BF16>(a, h[v]);
+      if (RES) {
+        float r[8];
+        unpack8_16<BF16>(b, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = col < K ? h[v][i] * rinv * g[i] : 0.0f;
-    f8_store_512(y, row, col, K, lane, codes, scales);
+        for (int i = 0; i < 8; ++i) h[v][i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq = fmaf(h[v][i], h[v][i], sq);
+    }
+    double sum = (double)sq;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if (lane == 0) part[t >> 6] = sum;
+    __syncthreads();
+    sum = part[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) sum += part[w];
+    const float rinv = f8_rsqrt(sum / (double)K + (double)eps);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int col = 8 * (v * NT + t);
+      if (512 * ((v * NT + t) >> 6) >= K) break;               // the whole wavefront is past the row
+      v4u gw = {0, 0, 0, 0};
+      if (col < K) {
+        gw = *reinterpret_cast<const v4u*>(gamma + col * 2);
+        if (RES) {
+          const v4u o = {pack2_16<BF16>(h[v][0], h[v][1]), pack2_16<BF16>(h[v][2], h[v][3]),
+                         pack2_16<BF16>(h[v][4], h[v][5]), pack2_16<BF16>(h[v][6], h[v][7])};
+          *reinterpret_cast<v4u*>(residual_out + (row * K + col) * 2) = o;
+        }
+      }
+      float g[8], y[8];
+      unpack8_16<BF16>(gw, g);
+      // lanes past K: 0 times a possibly infinite rinv is not to reach the group's maximum
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = col < K ? h[v][i] * rinv * g[i] : 0.0f;
+      f8_store_512(y, row, col, K, lane, codes, scales);
+    }
+    __syncthreads();                                           // part is read before the next row's
   }
 }
 
 template <bool BF16, bool RES>
 static void rmsnorm_launch(const uint8_t* X, const uint8_t* residual, const uint8_t* gamma, float eps, int64_t M, int K,
                            uint8_t* codes, uint8_t* scales, uint8_t* out, hipStream_t s) {
-  const dim3 g((unsigned)M);
-#define KQ_NORM(NT, VPT) \
-  hipLaunchKernelGGL((f8_rmsnorm_kernel<BF16, RES, NT, VPT>), g, dim3(NT), 0, s, X, residual, gamma, eps, K, codes, scales, out)
+  const dim3 g((unsigned)(M < (1 << 22) ? M : 1 << 22));       // a launch is at most 2^32 threads
+#define KQ_NORM(NT, VPT)                                                                                             \
+  hipLaunchKernelGGL((f8_rmsnorm_kernel<BF16, RES, NT, VPT>), g, dim3(NT), 0, s, X, residual, gamma, eps, M, K, codes, \
+                     scales, out)
   if (K <= 2048) KQ_NORM(256, 1);
   else if (K <= 4096) KQ_NORM(256, 2);
   else if (K <= 8192) KQ_NORM(256, 4);
