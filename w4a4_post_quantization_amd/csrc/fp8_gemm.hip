@@ -229,6 +229,7 @@ static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int
     const int64_t wgs = (N + 15) / 16, cus = device_cu_count();
     if (M <= 16) return wgs < cus ? KQ_ROWS(1, 1, 8, 2) : KQ_ROWS(1, 1, 4, 4);
     if (M <= 32) return wgs <= cus ? KQ_ROWS(1, 2, 4, 4) : KQ_ROWS(2, 2, 4, 4);
+    if (M <= 48) return wgs <= cus ? KQ_ROWS(1, 3, 8, 2) : KQ_ROWS(2, 3, 4, 2);
     return wgs <= cus ? KQ_ROWS(1, 4, 4, 2) : KQ_ROWS(2, 4, 4, 2);
   }
 #undef KQ_ROWS
@@ -763,8 +764,8 @@ using F8Half = F8Big<2, 3>;      // 256 x 128 tokens
 using F8Low = F8Big<1, 3>;       // 256 x 64 tokens
 
 // The first full_rows rows of 256-token tiles are whole tiles, grouped eight along M for reuse
-// in the level-2 caches; the rows below them are tiles of 128 tokens.  Each workgroup loops over
-// every grid-th tile.
+// in the level-2 caches; the tokens below them are in tiles of 128.  Each workgroup takes every
+// grid-th tile.
 template <int ACT, bool BF16>
 __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
@@ -773,18 +774,18 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
   __shared__ __align__(16) uint8_t lds[F8Large::LDS > F8Half::LDS ? F8Large::LDS : F8Half::LDS];
   const int tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256;
   const int nfull = tiles_n * full_rows;
-  const int hrows = max(0, (int)((M + 127) / 128) - 2 * full_rows), nhalf = tiles_n * hrows;
-  for (int t = blockIdx.x; t < nfull + nhalf; t += gridDim.x) {
+  const int rest = max(0, (int)((M + 127) / 128) - 2 * full_rows), nrest = tiles_n * rest;
+  for (int t = blockIdx.x; t < nfull + nrest; t += gridDim.x) {
     if (t < nfull) {
       constexpr int GM = 8;
       const int pid = f8_remap(t, nfull);
       const int first = pid / (GM * tiles_n) * GM, rows = min(full_rows - first, GM), in = pid % (GM * tiles_n);
       f8_big_tile<ACT, BF16, F8Large>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                                       256LL * (first + in % rows), 256 * (in / rows));
+                                      256LL * (first + in % rows), 256 * (in / rows));
     } else {
-      const int q = f8_remap(t - nfull, nhalf);
+      const int q = f8_remap(t - nfull, nrest);
       f8_big_tile<ACT, BF16, F8Half>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                                       256LL * full_rows + 128LL * (q % hrows), 256 * (q / hrows));
+                                     256LL * full_rows + 128LL * (q % rest), 256 * (q / rest));
     }
     __syncthreads();                         // the next tile's loads stay off what this one's epilogue reads
   }
@@ -817,22 +818,27 @@ template <int ACT, bool BF16>
 static hipError_t gemm_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                               const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
                               uint8_t* out, uint8_t* oscales, hipStream_t s) {
-  // A last round of tiles that leaves compute units idle costs nearly as much as a full one:
-  // its tile rows go to tiles of 128 tokens when those fit in one round; otherwise the rounds
-  // are made even, each workgroup (a multiple of the 8 dies) taking every grid-th tile.
+  // A last round of tiles that leaves compute units idle costs nearly as much as a full one, so
+  // the last rows of tiles may be split into tiles of 128 tokens, which take about 0.6 of a whole
+  // one.  For each split: the fulls take their rounds, and the rest go to whichever compute units
+  // are free first (those that had one full fewer, until the others come).  Measured (us) without
+  // and with: gated 4096 x 11008 x 4096 (5.4 rounds) 306 and 298, linear 3000 x 8192 x 4096 (1.5) 89.5
+  // and 84.9, 8192 x 4608 x 1152 (2.25) 53.7 and 52.9; tiles of 64 tokens gained at none of nine shapes.
+  // Whole tiles only: as few workgroups as the largest round needs (a multiple of the 8 dies).
   const int64_t tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256, tiles_m = (M + 255) / 256;
-  const int64_t cus = device_cu_count(), ntiles = tiles_n * tiles_m, tail = ntiles % cus;
-  int64_t full_rows = tiles_m;
-  if (tail > 0) {
-    const int64_t hr = (tail + tiles_n - 1) / tiles_n;
-    if (tiles_n * ((M + 127) / 128 - 2 * (tiles_m - hr)) <= cus) full_rows = tiles_m - hr;
-  }
-  int64_t grid = tiles_n * full_rows;
-  if (full_rows == tiles_m) {
-    const int64_t rounds = (ntiles + cus - 1) / cus;
-    grid = std::min(grid, ((ntiles + rounds - 1) / rounds + 7) / 8 * 8);
-  } else {
-    grid += tiles_n * ((M + 127) / 128 - 2 * full_rows);
+  const int64_t cus = device_cu_count(), ntiles = tiles_n * tiles_m, rounds = (ntiles + cus - 1) / cus;
+  int64_t full_rows = tiles_m, grid = std::min(ntiles, ((ntiles + rounds - 1) / rounds + 7) / 8 * 8);
+  double best = (double)rounds - 0.02;       // a split has to gain
+  for (int64_t rows = ntiles <= cus ? 0 : std::max<int64_t>(tiles_m - 4, 0); rows < tiles_m; ++rows) {
+    const int64_t nfull = rows * tiles_n, nrest = tiles_n * ((M + 127) / 128 - 2 * rows);
+    const int64_t late = nfull % cus;        // compute units with one full more
+    double early_at = (double)(nfull / cus), late_at = early_at + 1.0, end = late ? late_at : early_at;
+    for (int64_t left = nrest; left > 0;) {
+      const bool l = late && late_at <= early_at;
+      left -= l ? late : cus - late;
+      end = std::max(end, (l ? late_at : early_at) += 0.6);
+    }
+    if (end < best) best = end, full_rows = rows, grid = nfull + nrest;
   }
   hipLaunchKernelGGL((f8_gemm_kernel<ACT, BF16>), dim3((unsigned)grid), dim3(256), 0, s, wcodes, wscales, xcodes,
                      xscales, M, (int)N, (int)K, bias, out, oscales, (int)full_rows);
