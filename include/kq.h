@@ -325,6 +325,8 @@ kq_status kq_w4a4_linear_t(int32_t fmt,
  * with max|y| <= 448 2^e (at least -127), its codes are y 2^-e rounded to nearest even; a
  * group of zeros has byte 0.  A group that holds an infinity or a NaN has byte 255 and code
  * 0x7F throughout (both NaN), and makes NaN every product that uses it.
+ * Codes and scales from elsewhere may be used if every value code 2^e is zero or a normal
+ * float32 number (others may over- or underflow to infinity or zero).
  * Weights are [N][K] ([out][in]) and are quantized by the same call as activations; scales
  * given for blocks of 128 x 128 are the special case in which 128 rows repeat the same bytes.
  * 16-bit inputs and outputs are fp16 or bf16 (KQ_DT_*), sums are float32.  M <= 2^30; N and

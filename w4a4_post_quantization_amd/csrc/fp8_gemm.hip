@@ -728,30 +728,46 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
     lds_barrier();                                             // every wave's loads have landed
     uint8_t* const own = lds + wid * (32 * TM * 256);
     const uint2* const bias_t = reinterpret_cast<const uint2*>(lds + C::BIAS_OFF);
+    uint2 bw[4][4];                                            // all biases before the first use
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) bw[i][g] = bias_t[(wrow_a + 32 * i + 8 * g + 4 * h) / 4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const uint2 w = bias_t[(wrow_a + 32 * i + 8 * g + 4 * h) / 4];
+        const uint2 w = bw[i][g];
         const float b0 = unpack1_16<BF16>((uint16_t)(w.x & 0xFFFFu)), b1 = unpack1_16<BF16>((uint16_t)(w.x >> 16));
         const float b2 = unpack1_16<BF16>((uint16_t)(w.y & 0xFFFFu)), b3 = unpack1_16<BF16>((uint16_t)(w.y >> 16));
+        uint8_t* const at = own + l32 * 256 + 16 * ((4 * i + g) ^ (l32 & 15)) + 8 * (h ^ (l32 >> 4));
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-          const int row = 32 * j + l32;
           uint2 o;
           o.x = pack2_16<BF16>(acc[i][j][4 * g] + b0, acc[i][j][4 * g + 1] + b1);
           o.y = pack2_16<BF16>(acc[i][j][4 * g + 2] + b2, acc[i][j][4 * g + 3] + b3);
-          *reinterpret_cast<uint2*>(own + row * 256 + 16 * ((4 * i + g) ^ (row & 15)) + 8 * (h ^ (l32 >> 4))) = o;
+          *reinterpret_cast<uint2*>(at + 32 * 256 * j) = o;
         }
       }
+    // eight reads in flight, then their stores: store x takes rows 4 x .. 4 x + 3, whose swizzle
+    // depends on x % 4
     const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, mleft * N * 2);
-    const int c = lane & 15, col = n0 + wrow_a + 8 * c;
+    const int c = lane & 15, r4 = lane >> 4, col = n0 + wrow_a + 8 * c;
+    const uint32_t to = col < N ? ((uint32_t)(wrow_b + r4) * N + col) * 2 : KQ_OOB;
+    const uint8_t* from[4];
 #pragma unroll
-    for (int x = 0; x < 8 * TM; ++x) {
-      const int row = 4 * x + (lane >> 4);
-      v4i v = *reinterpret_cast<const v4i*>(own + row * 256 + 16 * (c ^ (row & 15)));
-      if (x >> 2 & 1) v = v4i{v.z, v.w, v.x, v.y};
-      __builtin_amdgcn_raw_buffer_store_b128(v, rY, col < N ? ((wrow_b + row) * N + col) * 2 : KQ_OOB, 0, 0);
+    for (int y = 0; y < 4; ++y) from[y] = own + (4 * y + r4) * 256 + 16 * (c ^ (4 * y + r4));
+#pragma unroll
+    for (int x0 = 0; x0 < 8 * TM; x0 += 8) {
+      v4i v[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) v[y] = *reinterpret_cast<const v4i*>(from[y & 3] + 4096 * ((x0 + y) >> 2));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const v4i w = y < 4 ? v[y] : v4i{v[y].z, v[y].w, v[y].x, v[y].y};
+        __builtin_amdgcn_raw_buffer_store_b128(w, rY, (int)(to + 8u * N * (x0 + y)), 0, 0);
+      }
     }
   } else {
     f8_gated_store<ACT, TM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out,
