@@ -221,6 +221,46 @@ def test_linear_exact(kq, M, N, K):
     assert torch.equal(got, ref), (got - ref).abs().max()
 
 
+@pytest.mark.parametrize("M,N,K", [(4100, 4368, 144), (4100, 4368, 256), (9000, 2304, 528), (4352, 4352, 2048), (3850, 5136, 2064),
+                                   (4096, 8736, 2176), (4352, 4352, 4096), (4352, 4352, 4112)])
+def test_many_tiles_exact(kq, M, N, K):
+    """More whole tiles than compute units: sequences of tiles on a workgroup, of 2 to 33 stages, and behind them the
+    tiles of fewer tokens; the same codes as a gated pair where N is even in 32s."""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    ng = (K + 127) // 128
+
+    def whole(rows, low):
+        c = torch.randint(-3, 4, (rows, K), device="cuda", generator=g).float().to(torch.float8_e4m3fn)
+        s = torch.zeros(rows, kq.fp8_scale_cols(K), dtype=torch.uint8, device="cuda")
+        s[:, :ng] = torch.randint(low, low + 3, (rows, ng), device="cuda", generator=g, dtype=torch.uint8)
+        return c, s
+
+    def value(c, s):
+        unit = torch.exp2(torch.arange(256, device="cuda", dtype=torch.float64) - 127)[s[:, :(c.shape[1] + 127) // 128].long()]
+        return c.double() * unit.repeat_interleave(128, 1)[:, :c.shape[1]]
+
+    w, ws = whole(N, 126)
+    x, xs = whole(M, 126)
+    bias = torch.randint(-9, 10, (N,), device="cuda", generator=g).to(torch.bfloat16)
+    ref = (value(x, xs) @ value(w, ws).t() + bias.double()).float().to(torch.bfloat16)      # sums exact in float32
+    assert torch.equal(kq.fp8_linear(x, xs, w, ws, bias=bias, dtype=torch.bfloat16), ref)
+    if N % 32:
+        return
+    F = N // 2
+    x, xs = whole(M, 120)
+    codes, scales = kq.fp8_gated_linear(x, xs, w, ws, act="silu")
+    y = value(x, xs) @ value(w, ws).t()
+    h = y[:, :F] * torch.sigmoid(y[:, :F]) * y[:, F:]
+    G = (F + 127) // 128
+    top = torch.nn.functional.pad(h, (0, 128 * G - F)).view(M, G, 128).abs().amax(2)
+    unit = torch.exp2(torch.arange(256, device="cuda", dtype=torch.float64) - 127)[scales[:, :G].long()]
+    # the scale is the smallest without saturation, a code within half a step of E4M3 (2^-4 relative,
+    # 2^-10 of the unit below its normal numbers); 1e-4 for the float32 activation
+    assert bool(((top <= 448 * unit * (1 + 1e-4)) & ((top >= 224 * unit * (1 - 1e-4)) | (top == 0))).all())
+    err, step = (value(codes, scales) - h).abs(), torch.maximum(h.abs() * 2.0 ** -4, unit.repeat_interleave(128, 1)[:, :F] * 2.0 ** -10)
+    assert bool((err <= step + 1e-4 * h.abs() + 1e-30).all())
+
+
 @pytest.mark.parametrize("M", list(range(1, 20)) + [24, 40, 56, 72, 88, 112, 144, 160, 192, 224])
 def test_linear_rows(kq, M):
     got, ref = _linear_case(kq, M, 208, 656, "bf16", True, seed=3)

@@ -552,41 +552,47 @@ __device__ __forceinline__ void f8_gated_store(v16f (&acc)[4][TM], uint8_t* __re
 // ACT -1: the linear, weight rows n0 .. n0 + 255.  Gated: rows f0 .. f0 + 127 of both halves, f0 =
 // n0 / 2, staged gate rows first; wavefront column wn takes gate and up of the same 64 columns, so
 // that a lane has both factors of an output, and the tile's 128 columns are one scale group.
-template <int ACT, bool BF16, class C>
-__device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
+// at(t, m0, n0) gives tile t's place.  SEQ: the workgroup takes tiles t0, t0 + step, .. below end, and
+// the loads past one tile's last stage are the next one's first: both slots of a gated tile, one of the
+// linear's, whose outputs go through the other.  So only the first tile waits for memory.  T >= NS.
+template <int ACT, bool BF16, class C, bool SEQ, class At>
+__device__ __forceinline__ void f8_big_tiles(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
                                             const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
                                             const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
                                             const uint16_t* __restrict__ bias, uint8_t* __restrict__ out,
-                                            uint8_t* __restrict__ oscales, int64_t m0, int n0) {
+                                            uint8_t* __restrict__ oscales, At at, int t0, int end, int step) {
   constexpr bool GATED = ACT >= 0;
   constexpr int NS = C::NS, TM = C::TM, NB = 2 * TM, NL = 8 + NB;   // NL loads (8 rows) of a wave and stage
   constexpr int NM = 4 * TM, NR = 2 * (4 + TM);                // products and reads of a half
-  // the thread index, hidden from the compiler, so that it does not keep every lane-dependent
-  // offset live across the tile loop
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const int lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wid & 1, wm = wid >> 1;
   const int l32 = lane & 31, h = lane >> 5;
   const int SC = (int)f8_scale_cols(K), T = (K + 127) / 128;
 
   // wave w stages weight rows 64 w .. of the tile (gated: waves 0, 1 gate, 2, 3 up) and token rows
   // 8 NB w ..; the first waves also the scales of 64 token rows each
-  const int64_t arow = GATED ? (int64_t)(wid >> 1) * N + (n0 >> 1) + 64 * (wid & 1) : (int64_t)n0 + 64 * wid;
-  const int64_t aleft = GATED ? N - (n0 >> 1) - 64 * (wid & 1) : N - n0 - 64 * wid;
-  const v4i rA = rsrc_words(wcodes + arow * K, aleft * K);
-  const v4i rAS = rsrc_words(wscales + arow * SC, aleft * SC);
-  const int64_t mleft = min(M - m0, (int64_t)C::BM);
-  const v4i rB = rsrc_words(xcodes + m0 * K, mleft * K);
-  const v4i rBS = rsrc_words(xscales + m0 * SC, mleft * SC);
+  auto rows_at = [&](int t, const uint8_t* w, const uint8_t* x, int stride, v4i& rw, v4i& rx) {
+    int64_t m0;
+    int n0;
+    at(t < end ? t : t0, m0, n0);
+    const int64_t row = GATED ? (int64_t)(wid >> 1) * N + (n0 >> 1) + 64 * (wid & 1) : (int64_t)n0 + 64 * wid;
+    const int64_t left = GATED ? N - (n0 >> 1) - 64 * (wid & 1) : N - n0 - 64 * wid;
+    rw = rsrc_words(w + row * stride, t < end ? left * stride : 0);   // no tile: nothing to load
+    rx = rsrc_words(x + m0 * stride, t < end ? min(M - m0, (int64_t)C::BM) * stride : 0);
+  };
+  v4i rA, rB, rAS, rBS;
+  auto codes_at = [&](int t) { rows_at(t, wcodes, xcodes, K, rA, rB); };
+  auto scales_at = [&](int t) { rows_at(t, wscales, xscales, SC, rAS, rBS); };
+  codes_at(t0);
+  scales_at(t0);
 
   const uint32_t lds0 = lds_addr(lds);
   // a load's row and first byte of this lane; rows 8 .. 15 of each 16 have another swizzle
   const int lrow = lane >> 3, lcol = 16 * ((lane ^ lrow) & 7);
   // unsigned: an offset past the end is KQ_OOB plus at most 2^28 and stays past every range
   const uint32_t ogA = lrow * K, ogB = (8 * NB * wid + lrow) * K;
-  auto k_off = [&](int p, int odd) -> uint32_t {
-    const int k = 128 * p + (lcol ^ (16 * odd));
+  auto k_off = [&](int k0, int odd) -> uint32_t {
+    const int k = k0 + (lcol ^ (16 * odd));
     return k < K ? k : KQ_OOB;
   };
   auto code_load = [&](int slot, uint32_t ko, int g) {         // load g (0 .. NL - 1) of a stage
@@ -598,9 +604,10 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
   // have rows: the branches are inside the assembly so that the loop body stays one block for
   // the scheduler.  A row's last piece may run into the next row; those bytes are never used.
   const uint32_t osc = lane * SC, oscb = (64 * wid + lane) * SC;
+  int sbuf = 0;                                                // buffer of group 0 of this tile
   auto scale_loads = [&](int grp, int skip) {
-    const uint32_t sc = lds0 + (uint32_t)(C::SC_OFF + (grp & 1) * C::SC_BYTES + 16 * 64 * wid);
-    const uint32_t ko = 16 * grp < T ? 16 * grp : KQ_OOB;
+    const uint32_t sc = lds0 + (uint32_t)(C::SC_OFF + ((sbuf + grp) & 1) * C::SC_BYTES + 16 * 64 * wid);
+    const uint32_t ko = 16 * grp < T ? 16 * grp : SEQ ? 0 : KQ_OOB;
     asm volatile(
         "s_cmp_lg_u32 %0, 0\n\t"
         "s_cbranch_scc1 1f\n\t"
@@ -635,143 +642,183 @@ __device__ __forceinline__ void f8_big_tile(uint8_t* __restrict__ lds, const uin
   };
   const int sa_at = 16 * (wrow_a + l32), sb_at = 256 * 16 + 16 * (wrow_b + l32);
   auto read_scale = [&](int p, int q) -> int {                 // scale of fragment q for a stage
-    const uint8_t* sc = lds + C::SC_OFF + ((p >> 4) & 1) * C::SC_BYTES + (p & 15);
+    const uint8_t* sc = lds + C::SC_OFF + ((sbuf + (p >> 4)) & 1) * C::SC_BYTES + (p & 15);
     return sc[q < 4 ? sa_at + 512 * blk(q) : sb_at + 512 * (q - 4)];
   };
 
-  v16f acc[4][TM];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-
-  if (!GATED && wid == 0) {                                    // without a bias, or past N: zeros
-    const v4i rW = rsrc_words(bias + n0, bias ? (int64_t)(N - n0) * 2 : 0);
-    lds_load16(rW, lds0 + C::BIAS_OFF, lane < 32 ? 16 * lane : KQ_OOB);
+  auto bias_load = [&](int n0) {
+    if (!GATED && wid == 0) {                                  // without a bias, or past N: zeros
+      const v4i rW = rsrc_words(bias + n0, bias ? (int64_t)(N - n0) * 2 : 0);
+      lds_load16(rW, lds0 + C::BIAS_OFF, lane < 32 ? 16 * lane : KQ_OOB);
+    }
+  };
+  {
+    int64_t m0;
+    int n0;
+    at(t0, m0, n0);
+    bias_load(n0);
   }
   scale_loads(0, 0);
 #pragma unroll
   for (int p = 0; p < NS; ++p)
 #pragma unroll
-    for (int g = 0; g < NL; ++g) code_load(p, k_off(p, g & 1), g);
+    for (int g = 0; g < NL; ++g) code_load(p, k_off(128 * p, g & 1), g);
   __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 1) * NL));       // biases, scales and stage 0
   lds_barrier();
-  constexpr int ND = NM * 3 / 8, NE = NM * 3 / 4;              // products that the reads are spread under
-  v8i a[2][4], b[2][TM];
-  int s[4 + TM], ns[4 + TM];
-#pragma unroll
-  for (int q = 0; q < 4 + TM; ++q) s[q] = read_scale(0, q);
-#pragma unroll
-  for (int q = 0; q < NR; ++q) read_half(lds, 0, q, a[0], b[0]);
   int slot = 0, after = 1;                                     // of stages p and p + 1
-  for (int p = 0; p < T; ++p) {
-    const uint8_t* const cur = lds + slot * C::STAGE;
-    const uint8_t* const nxt = lds + after * C::STAGE;
-    uint32_t ko[2];
-    __builtin_amdgcn_sched_barrier(0);
+  for (int t = t0;;) {
+    v16f acc[4][TM];
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      const int i = m / TM, j = m % TM;
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[0][i], b[0][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
-      __builtin_amdgcn_sched_barrier(0);
-      if (m < ND) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int q = NR * m / ND; q < NR * (m + 1) / ND; ++q) read_half(cur, 1, q, a[1], b[1]);
-      }
-      if (m == NM / 2 - 1) {
-        lds_barrier();
-        scale_loads((p >> 4) + 1, p & 15);
-        ko[0] = k_off(p + NS, 0);
-        ko[1] = k_off(p + NS, 1);
-      }
-      if (m >= NM / 2) {
+      for (int j = 0; j < TM; ++j)
 #pragma unroll
-        for (int g = NL * (m - NM / 2) / NM; g < NL * (m + 1 - NM / 2) / NM; ++g) code_load(slot, ko[g & 1], g);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 2) * NL + NL / 2));
-    lds_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      const int i = m / TM, j = m % TM;
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[1][i], b[1][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
-      __builtin_amdgcn_sched_barrier(0);
-      if (m < NE) {
-#pragma unroll
-        for (int q = NR * m / NE; q < NR * (m + 1) / NE; ++q) read_half(nxt, 0, q, a[0], b[0]);
-#pragma unroll
-        for (int q = (4 + TM) * m / NE; q < (4 + TM) * (m + 1) / NE; ++q) ns[q] = read_scale(p + 1, q);
-      }
-      if (m < NM / 2) {
-#pragma unroll
-        for (int g = NL / 2 + NL * m / NM; g < NL / 2 + NL * (m + 1) / NM; ++g) code_load(slot, ko[g & 1], g);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int q = 0; q < 4 + TM; ++q) s[q] = ns[q];
-    slot = after;
-    after = after + 1 == NS ? 0 : after + 1;
-  }
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));                   // no load may land in LDS after this tile
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  if constexpr (!GATED) {
-    // Outputs go through the slots, which a token's columns leave in whole cache lines: a lane
-    // holds four columns of one token, and stored as they are the 64 lanes of a store touch 32
-    // rows.  A wave's 32 TM tokens x 128 columns, rows of 16 chunks swizzled by the row, the halves
-    // of a chunk swapped in rows 16 .. 31 of each 32 (a write's 32 lanes hit every bank).  (4096 x
-    // 4096 x 1024: 23.4 against 29.4 us.)
-    lds_barrier();                                             // every wave's loads have landed
-    uint8_t* const own = lds + wid * (32 * TM * 256);
-    const uint2* const bias_t = reinterpret_cast<const uint2*>(lds + C::BIAS_OFF);
-    uint2 bw[4][4];                                            // all biases before the first use
+    constexpr int ND = NM * 3 / 8, NE = NM * 3 / 4;            // products that the reads are spread under
+    v8i a[2][4], b[2][TM];
+    int s[4 + TM], ns[4 + TM];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int q = 0; q < 4 + TM; ++q) s[q] = read_scale(0, q);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) bw[i][g] = bias_t[(wrow_a + 32 * i + 8 * g + 4 * h) / 4];
+    for (int q = 0; q < NR; ++q) read_half(lds + slot * C::STAGE, 0, q, a[0], b[0]);
+    int kb = 128 * NS;                                         // of the stage that is loaded
+    const int e1 = (T - 1) & ~15, e2 = T - NS, ev = min(e1, e2);
+    for (int p = 0; p < T; ++p, kb += 128) {
+      if (SEQ && __builtin_expect(p >= ev, 0)) {               // from here on loads of the next tile
+        if (p == e1) scales_at(t + step);
+        if (p == e2) codes_at(t + step), kb = 0;
+        if (!GATED && p > e2) kb = 1 << 20;                    // the outputs' slot
+      }
+      const uint8_t* const cur = lds + slot * C::STAGE;
+      const uint8_t* const nxt = lds + after * C::STAGE;
+      uint32_t ko[2];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int m = 0; m < NM; ++m) {
+        const int i = m / TM, j = m % TM;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[0][i], b[0][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (m < ND) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint2 w = bw[i][g];
-        const float b0 = unpack1_16<BF16>((uint16_t)(w.x & 0xFFFFu)), b1 = unpack1_16<BF16>((uint16_t)(w.x >> 16));
-        const float b2 = unpack1_16<BF16>((uint16_t)(w.y & 0xFFFFu)), b3 = unpack1_16<BF16>((uint16_t)(w.y >> 16));
-        uint8_t* const at = own + l32 * 256 + 16 * ((4 * i + g) ^ (l32 & 15)) + 8 * (h ^ (l32 >> 4));
+          for (int q = NR * m / ND; q < NR * (m + 1) / ND; ++q) read_half(cur, 1, q, a[1], b[1]);
+        }
+        if (m == NM / 2 - 1) {
+          lds_barrier();
+          scale_loads((p >> 4) + 1, p & 15);
+          ko[0] = k_off(kb, 0);
+          ko[1] = k_off(kb, 1);
+        }
+        if (m >= NM / 2) {
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-          uint2 o;
-          o.x = pack2_16<BF16>(acc[i][j][4 * g] + b0, acc[i][j][4 * g + 1] + b1);
-          o.y = pack2_16<BF16>(acc[i][j][4 * g + 2] + b2, acc[i][j][4 * g + 3] + b3);
-          *reinterpret_cast<uint2*>(at + 32 * 256 * j) = o;
+          for (int g = NL * (m - NM / 2) / NM; g < NL * (m + 1 - NM / 2) / NM; ++g) code_load(slot, ko[g & 1], g);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 2) * NL + NL / 2));
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        const int i = m / TM, j = m % TM;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[1][i], b[1][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (m < NE) {
+#pragma unroll
+          for (int q = NR * m / NE; q < NR * (m + 1) / NE; ++q) read_half(nxt, 0, q, a[0], b[0]);
+#pragma unroll
+          for (int q = (4 + TM) * m / NE; q < (4 + TM) * (m + 1) / NE; ++q) ns[q] = read_scale(p + 1, q);
+        }
+        if (m < NM / 2) {
+#pragma unroll
+          for (int g = NL / 2 + NL * m / NM; g < NL / 2 + NL * (m + 1) / NM; ++g) code_load(slot, ko[g & 1], g);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int q = 0; q < 4 + TM; ++q) s[q] = ns[q];
+      slot = after;
+      after = after + 1 == NS ? 0 : after + 1;
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));                 // no load may land in LDS after this tile
+    int64_t m0;
+    int n0;
+    at(t, m0, n0);
+    const int64_t mleft = min(M - m0, (int64_t)C::BM);
+    // the lane, hidden from the compiler, which would keep the epilogue's addresses live in the loop
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int l32 = el & 31, h = el >> 5;
+
+    if constexpr (!GATED) {
+      // Outputs go through the slots, which a token's columns leave in whole cache lines: a lane
+      // holds four columns of one token, and stored as they are the 64 lanes of a store touch 32
+      // rows.  A wave's 32 TM tokens x 128 columns, rows of 16 chunks swizzled by the row, the halves
+      // of a chunk swapped in rows 16 .. 31 of each 32 (a write's 32 lanes hit every bank).  (4096 x
+      // 4096 x 1024: 23.4 against 29.4 us.)
+      lds_barrier();                                           // every wave's loads have landed
+      // SEQ: two of a wave's blocks of tokens at a time, in the slot that holds nothing
+      constexpr int PJ = 2;
+      uint8_t* const own = lds + (SEQ ? after * C::STAGE : 0) + wid * (32 * PJ * 256);
+      const uint2* const bias_t = reinterpret_cast<const uint2*>(lds + C::BIAS_OFF);
+      uint2 bw[4][4];                                          // all biases before the first use
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) bw[i][g] = bias_t[(wrow_a + 32 * i + 8 * g + 4 * h) / 4];
+      const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, mleft * N * 2);
+      const int c = el & 15, r4 = el >> 4, col = n0 + wrow_a + 8 * c;
+      const uint32_t to = col < N ? ((uint32_t)(wrow_b + r4) * N + col) * 2 : KQ_OOB;
+      const uint8_t* from[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) from[y] = own + (4 * y + r4) * 256 + 16 * (c ^ (4 * y + r4));
+#pragma unroll
+      for (int j0 = 0; j0 < TM; j0 += PJ) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint2 w = bw[i][g];
+            const float b0 = unpack1_16<BF16>((uint16_t)(w.x & 0xFFFFu)), b1 = unpack1_16<BF16>((uint16_t)(w.x >> 16));
+            const float b2 = unpack1_16<BF16>((uint16_t)(w.y & 0xFFFFu)), b3 = unpack1_16<BF16>((uint16_t)(w.y >> 16));
+            uint8_t* const at = own + l32 * 256 + 16 * ((4 * i + g) ^ (l32 & 15)) + 8 * (h ^ (l32 >> 4));
+#pragma unroll
+            for (int j = j0; j < j0 + PJ; ++j) {
+              uint2 o;
+              o.x = pack2_16<BF16>(acc[i][j][4 * g] + b0, acc[i][j][4 * g + 1] + b1);
+              o.y = pack2_16<BF16>(acc[i][j][4 * g + 2] + b2, acc[i][j][4 * g + 3] + b3);
+              *reinterpret_cast<uint2*>(at + 32 * 256 * (j - j0)) = o;
+            }
+          }
+        // eight reads in flight, then their stores: store x takes rows 4 x .. 4 x + 3, whose swizzle
+        // depends on x % 4
+#pragma unroll
+        for (int x0 = 0; x0 < 8 * PJ; x0 += 8) {
+          v4i v[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) v[y] = *reinterpret_cast<const v4i*>(from[y & 3] + 4096 * ((x0 + y) >> 2));
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const v4i w = y < 4 ? v[y] : v4i{v[y].z, v[y].w, v[y].x, v[y].y};
+            __builtin_amdgcn_raw_buffer_store_b128(w, rY, (int)(to + 8u * N * (8 * j0 + x0 + y)), 0, 0);
+          }
         }
       }
-    // eight reads in flight, then their stores: store x takes rows 4 x .. 4 x + 3, whose swizzle
-    // depends on x % 4
-    const __amdgpu_buffer_rsrc_t rY = make_rsrc(out + m0 * N * 2, mleft * N * 2);
-    const int c = lane & 15, r4 = lane >> 4, col = n0 + wrow_a + 8 * c;
-    const uint32_t to = col < N ? ((uint32_t)(wrow_b + r4) * N + col) * 2 : KQ_OOB;
-    const uint8_t* from[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) from[y] = own + (4 * y + r4) * 256 + 16 * (c ^ (4 * y + r4));
-#pragma unroll
-    for (int x0 = 0; x0 < 8 * TM; x0 += 8) {
-      v4i v[8];
-#pragma unroll
-      for (int y = 0; y < 8; ++y) v[y] = *reinterpret_cast<const v4i*>(from[y & 3] + 4096 * ((x0 + y) >> 2));
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const v4i w = y < 4 ? v[y] : v4i{v[y].z, v[y].w, v[y].x, v[y].y};
-        __builtin_amdgcn_raw_buffer_store_b128(w, rY, (int)(to + 8u * N * (x0 + y)), 0, 0);
-      }
+    } else {
+      f8_gated_store<ACT, TM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out, oscales);
     }
-  } else {
-    f8_gated_store<ACT, TM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out,
-                                         oscales);
+    if (!SEQ || (t += step) >= end) break;
+    sbuf = (sbuf + (T + 15) / 16) & 1;
+    lds_barrier();                             // the slot's reads are done, and all see the next stage 0
+    if constexpr (!GATED) {
+      at(t, m0, n0);
+      bias_load(n0);
+      uint32_t ko[2] = {k_off(128, 0), k_off(128, 1)};
+      asm volatile("" : "+v"(ko[0]), "+v"(ko[1]));             // likewise
+#pragma unroll
+      for (int g = 0; g < NL; ++g) code_load(after, ko[g & 1], g);
+    }
   }
 }
 
@@ -780,9 +827,9 @@ using F8Half = F8Big<2, 3>;      // 256 x 128 tokens
 using F8Low = F8Big<1, 3>;       // 256 x 64 tokens
 
 // The first full_rows rows of 256-token tiles are whole tiles, grouped eight along M for reuse
-// in the level-2 caches; the tokens below them are in tiles of 128.  Each workgroup takes every
-// grid-th tile.
-template <int ACT, bool BF16>
+// in the level-2 caches; the tokens below them are in tiles of 128, one for each of the last
+// workgroups.  The others take whole tiles, one each or (SEQ) in turn.
+template <int ACT, bool BF16, bool SEQ>
 __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
@@ -791,19 +838,25 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
   const int tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256;
   const int nfull = tiles_n * full_rows;
   const int rest = max(0, (int)((M + 127) / 128) - 2 * full_rows), nrest = tiles_n * rest;
-  for (int t = blockIdx.x; t < nfull + nrest; t += gridDim.x) {
-    if (t < nfull) {
+  const int gfull = (int)gridDim.x - nrest;
+  if ((int)blockIdx.x < gfull) {
+    auto at = [&](int t, int64_t& m0, int& n0) {
       constexpr int GM = 8;
       const int pid = f8_remap(t, nfull);
       const int first = pid / (GM * tiles_n) * GM, rows = min(full_rows - first, GM), in = pid % (GM * tiles_n);
-      f8_big_tile<ACT, BF16, F8Large>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                                      256LL * (first + in % rows), 256 * (in / rows));
-    } else {
-      const int q = f8_remap(t - nfull, nrest);
-      f8_big_tile<ACT, BF16, F8Half>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales,
-                                     256LL * full_rows + 128LL * (q % rest), 256 * (q / rest));
-    }
-    __syncthreads();                         // the next tile's loads stay off what this one's epilogue reads
+      m0 = 256LL * (first + in % rows);
+      n0 = 256 * (in / rows);
+    };
+    f8_big_tiles<ACT, BF16, F8Large, SEQ>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, at,
+                                           blockIdx.x, nfull, gfull);
+  } else {
+    auto at = [&](int t, int64_t& m0, int& n0) {
+      const int q = f8_remap(t, nrest);
+      m0 = 256LL * full_rows + 128LL * (q % rest);
+      n0 = 256 * (q / rest);
+    };
+    f8_big_tiles<ACT, BF16, F8Half, false>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, at,
+                                           (int)blockIdx.x - gfull, nrest, 1);
   }
 }
 
@@ -826,8 +879,12 @@ __global__ __launch_bounds__(256, 1) void f8_low_kernel(
     uint8_t* __restrict__ oscales) {
   __shared__ __align__(16) uint8_t lds[F8Low::LDS];
   const int rows = (int)((M + F8Low::BM - 1) / F8Low::BM), pid = f8_remap(blockIdx.x, gridDim.x);
-  f8_big_tile<ACT, false, F8Low>(lds, wcodes, wscales, xcodes, xscales, M, N, K, nullptr, out, oscales,
-                                 (int64_t)F8Low::BM * (pid % rows), 256 * (pid / rows));
+  auto at = [&](int, int64_t& m0, int& n0) {
+    m0 = (int64_t)F8Low::BM * (pid % rows);
+    n0 = 256 * (pid / rows);
+  };
+  f8_big_tiles<ACT, false, F8Low, false>(lds, wcodes, wscales, xcodes, xscales, M, N, K, nullptr, out, oscales, at, 0,
+                                         1, 1);
 }
 
 template <int ACT, bool BF16>
@@ -840,10 +897,9 @@ static hipError_t gemm_launch(const uint8_t* xcodes, const uint8_t* xscales, int
   // are free first (those that had one full fewer, until the others come).  Measured (us) without
   // and with: gated 4096 x 11008 x 4096 (5.4 rounds) 306 and 298, linear 3000 x 8192 x 4096 (1.5) 89.5
   // and 84.9, 8192 x 4608 x 1152 (2.25) 53.7 and 52.9; tiles of 64 tokens gained at none of nine shapes.
-  // Whole tiles only: as few workgroups as the largest round needs (a multiple of the 8 dies).
   const int64_t tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256, tiles_m = (M + 255) / 256;
   const int64_t cus = device_cu_count(), ntiles = tiles_n * tiles_m, rounds = (ntiles + cus - 1) / cus;
-  int64_t full_rows = tiles_m, grid = std::min(ntiles, ((ntiles + rounds - 1) / rounds + 7) / 8 * 8);
+  int64_t full_rows = tiles_m;
   double best = (double)rounds - 0.02;       // a split has to gain
   for (int64_t rows = ntiles <= cus ? 0 : std::max<int64_t>(tiles_m - 4, 0); rows < tiles_m; ++rows) {
     const int64_t nfull = rows * tiles_n, nrest = tiles_n * ((M + 127) / 128 - 2 * rows);
@@ -854,10 +910,21 @@ static hipError_t gemm_launch(const uint8_t* xcodes, const uint8_t* xscales, int
       left -= l ? late : cus - late;
       end = std::max(end, (l ? late_at : early_at) += 0.6);
     }
-    if (end < best) best = end, full_rows = rows, grid = nfull + nrest;
+    if (end < best) best = end, full_rows = rows;
   }
-  hipLaunchKernelGGL((f8_gemm_kernel<ACT, BF16>), dim3((unsigned)grid), dim3(256), 0, s, wcodes, wscales, xcodes,
-                     xscales, M, (int)N, (int)K, bias, out, oscales, (int)full_rows);
+  // Several whole tiles in sequence on a workgroup, the next one's first loads under the present one's last
+  // products: the more, the shorter their k.  Measured (us) without and with: linear 16384 x 6144 x 512
+  // 83.6 and 77.2, 8192 x 8192 x 1024 80.3 and 76.7, 8192 x 4608 x 1152 54.6 and 52.3, 8192 x 4608 x 4096
+  // 129.1 and 128.9, x 8192 244 and 244 (on another card 237 and 246), gated 4096 x 11008 x 2240 195 and 189.
+  const int64_t nfull = full_rows * tiles_n, nrest = tiles_n * std::max<int64_t>((M + 127) / 128 - 2 * full_rows, 0);
+  const bool seq = nfull > cus && K > 128 && K <= 4096;
+  const dim3 blocks((unsigned)((seq ? cus : nfull) + nrest));
+#define KQ_GEMM(SEQ)                                                                                                 \
+  hipLaunchKernelGGL((f8_gemm_kernel<ACT, BF16, SEQ>), blocks, dim3(256), 0, s, wcodes, wscales, xcodes, xscales, M, \
+                     (int)N, (int)K, bias, out, oscales, (int)full_rows)
+  if (seq) KQ_GEMM(true);
+  else KQ_GEMM(false);
+#undef KQ_GEMM
   return hipGetLastError();
 }
 
