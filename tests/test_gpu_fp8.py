@@ -221,6 +221,14 @@ def test_linear_exact(kq, M, N, K):
     assert torch.equal(got, ref), (got - ref).abs().max()
 
 
+@pytest.mark.parametrize("M", [1, 16, 30, 45, 61])
+@pytest.mark.parametrize("N,K", [(2048, 528), (4096, 6160), (4112, 528), (4112, 6160), (8192, 144), (8208, 528)])
+def test_linear_few_tokens_exact(kq, M, N, K):
+    """Up to 64 tokens, to each side of one and two workgroups of 16 weight rows on a compute unit."""
+    got, ref = _linear_case(kq, M, N, K, "fp16", M % 2 == 0, seed=M + N)
+    assert torch.equal(got, ref)
+
+
 @pytest.mark.parametrize("M,N,K", [(4100, 4368, 144), (4100, 4368, 256), (9000, 2304, 528), (4352, 4352, 2048), (3850, 5136, 2064),
                                    (4096, 8736, 2176), (4352, 4352, 4096), (4352, 4352, 4112)])
 def test_many_tiles_exact(kq, M, N, K):

@@ -220,17 +220,25 @@ static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int
 #define KQ_ROWS(RT, MT, NW, S) \
   rows_go<ACT, BF16, RT, MT, NW, S>(xcodes, xscales, M, K, wcodes, wscales, N, bias, out, s)
   if constexpr (ACT >= 0) {
-    return M <= 16 ? KQ_ROWS(2, 1, 8, 2) : KQ_ROWS(2, 2, 4, 4);
+    // two workgroups on a compute unit; one of twice the LDS took 20.7 against 17.7 us (one token, 11008 x
+    // 4096) and 22.6 against 19.0 (32 tokens)
+    return M <= 16 ? KQ_ROWS(2, 1, 4, 3) : KQ_ROWS(2, 2, 4, 2);
   } else {
-    // 16 weight rows a workgroup while that is at most one workgroup per compute unit, with twice
-    // the wavefronts if it leaves some idle (one token, 1024 x 4096: 3.9 against 4.3 us; 11008 x
-    // 4096: 13.0 against 12.2); else, from 17 tokens, 32, which halves what the tokens' codes
-    // cost (24 tokens, 6144 x 4096: 8.3 against 11.2 us; 1152 x 1152: 4.0 against 3.3)
+    // 16 weight rows a workgroup while that is at most one workgroup per compute unit, with twice the
+    // wavefronts if one token leaves some idle (2048 x 11008: 6.5 against 7.3 us); else 32, which halves
+    // what the tokens' codes cost, in workgroups small enough for two or three on a unit.  Measured (us)
+    // with 16 and 32 rows, weights from HBM: one token, 11008 x 4096 13.8 and 12.3, 5120 x 6144 9.6 and
+    // 8.1, but 8192 x 8192 14.6 and 18.8; 24 tokens, 11008 x 4096 16.0 and 13.9, 4096 x 4096 7.1 and 7.8.
+    // Two wavefronts instead of four once 32 rows a workgroup are more than one per unit: 37
+    // tokens, 16384 x 4096 17.3 against 20.3, 6144 x 4096 10.3 against 9.4.
     const int64_t wgs = (N + 15) / 16, cus = device_cu_count();
-    if (M <= 16) return wgs < cus ? KQ_ROWS(1, 1, 8, 2) : KQ_ROWS(1, 1, 4, 4);
-    if (M <= 32) return wgs <= cus ? KQ_ROWS(1, 2, 4, 4) : KQ_ROWS(2, 2, 4, 4);
-    if (M <= 48) return wgs <= cus ? KQ_ROWS(1, 3, 8, 2) : KQ_ROWS(2, 3, 4, 2);
-    return wgs <= cus ? KQ_ROWS(1, 4, 4, 2) : KQ_ROWS(2, 4, 4, 2);
+    if (M <= 16) {
+      if (wgs < cus) return KQ_ROWS(1, 1, 8, 2);
+      return wgs > cus && K <= 6144 ? KQ_ROWS(2, 1, 4, 3) : KQ_ROWS(1, 1, 4, 4);
+    }
+    if (M <= 32) return wgs <= cus ? KQ_ROWS(1, 2, 4, 2) : KQ_ROWS(2, 2, 4, 2);
+    if (M <= 48) return wgs <= cus ? KQ_ROWS(1, 3, 4, 2) : wgs <= 2 * cus ? KQ_ROWS(2, 3, 4, 2) : KQ_ROWS(2, 3, 2, 2);
+    return wgs <= cus ? KQ_ROWS(1, 4, 4, 2) : wgs <= 2 * cus ? KQ_ROWS(2, 4, 4, 2) : KQ_ROWS(2, 4, 2, 2);
   }
 #undef KQ_ROWS
 }
