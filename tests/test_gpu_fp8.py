@@ -329,7 +329,7 @@ GATED_SHAPES = [(1, 16, 16), (1, 128, 4096), (1, 1152, 512), (2, 144, 528), (3, 
                 (128, 128, 512), (130, 144, 400), (203, 1104, 2240), (256, 256, 1024), (300, 528, 272), (513, 1152, 640),
                 (1030, 784, 528), (2050, 272, 128),
                 (3, 48, 16400), (40, 144, 16656), (1030, 2064, 528), (2050, 4112, 400), (600, 11024, 272),
-                (1100, 2192, 4240)]
+                (1100, 2192, 4240), (30, 12304, 144), (45, 12288, 144), (48, 12304, 272), (60, 8192, 144), (49, 8208, 272)]
 
 
 @pytest.mark.parametrize("M,F,K", GATED_SHAPES)

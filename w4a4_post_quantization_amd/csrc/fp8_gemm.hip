@@ -209,9 +209,14 @@ static hipError_t rows_go(const uint8_t* xcodes, const uint8_t* xscales, int64_t
 }
 
 // Tokens the rows kernel takes; above, tiles.  Measured (us): linear 6144 x 4096, 64 tokens 9.8
-// against 11.7 in tiles, 128 tokens 13.1 against 12.3; gated 11008 x 4096, 32 tokens 27.6 against
-// 33.3, 64 tokens 30.5 against 31.2 (a second launch and 2.8 MB of float32 between them).
-constexpr int64_t ROWS_LINEAR = 64, ROWS_GATED = 32;
+// against 11.7 in tiles, 128 tokens 13.1 against 12.3.
+constexpr int64_t ROWS_LINEAR = 64;
+
+// The gated pair, where a second launch and the float32 outputs between them count too: to 32 tokens, and to 48
+// and 64 while its workgroups of 16 columns all run at once, three and two on each of 256 compute units.
+// Measured (us) in rows and in tiles, K = 4096: 40 tokens, F = 2816 12.7 and 18.6, 11008 23.3 and 25.9, 14336 36.7
+// and 33.0; 64 tokens, 2816 13.4 and 19.0, 8192 17.2 and 19.3, 11008 32.2 and 26.5; 32 tokens, 14336 33.2 and 33.0.
+static bool gated_rows(int64_t M, int64_t F) { return M <= 32 || (M <= 48 && F <= 12288) || (M <= 64 && F <= 8192); }
 
 template <int ACT, bool BF16>
 static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
@@ -222,7 +227,8 @@ static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int
   if constexpr (ACT >= 0) {
     // two workgroups on a compute unit; one of twice the LDS took 20.7 against 17.7 us (one token, 11008 x
     // 4096) and 22.6 against 19.0 (32 tokens)
-    return M <= 16 ? KQ_ROWS(2, 1, 4, 3) : KQ_ROWS(2, 2, 4, 2);
+    if (M <= 32) return M <= 16 ? KQ_ROWS(2, 1, 4, 3) : KQ_ROWS(2, 2, 4, 2);
+    return M <= 48 ? KQ_ROWS(2, 3, 2, 2) : KQ_ROWS(2, 4, 2, 2);
   } else {
     // 16 weight rows a workgroup while that is at most one workgroup per compute unit, with twice the
     // wavefronts if one token leaves some idle (2048 x 11008: 6.5 against 7.3 us); else 32, which halves
@@ -969,13 +975,13 @@ hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xsc
               : linear_launch<false>(xcodes, xscales, M, K, wcodes, wscales, N, b, y, s);
 }
 
-size_t f8_gated_workspace_bytes(int64_t M, int64_t F, int64_t) { return M > ROWS_GATED ? 0 : (size_t)M * F * 4; }
+size_t f8_gated_workspace_bytes(int64_t M, int64_t F, int64_t) { return gated_rows(M, F) ? (size_t)M * F * 4 : 0; }
 
 template <int ACT>
 static hipError_t gated_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                                const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,
                                uint8_t* scales, void* workspace, hipStream_t s) {
-  if (M <= ROWS_GATED) {
+  if (gated_rows(M, F)) {
     // a workgroup's 16 columns are an eighth of a scale group: the outputs go through the
     // workspace in float32 and the quantizer
     const hipError_t e = rows_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, workspace, s);
