@@ -957,9 +957,9 @@ static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, i
                      wcodes, wscales, xcodes, xscales, M, (int)N, (int)K, bias, Y)
   // measured (us) at 4096 x 4096 with 64 x 64 / 128 x 64 / 128 x 128 / 256 x 256: 200 tokens 12.0 /
   // 15.1 / 18.0 / 27.6, 512 tokens 18.4 / 16.4 / 18.9 / 29.0, 1024 tokens 33.6 / 30.6 / 22.5 / 30.5,
-  // 2048 tokens 79 / 60 / 43 / 39
+  // 2048 tokens 79 / 60 / 43 / 39; 512 tokens, 4096 x 1152 8.2 / 7.2 / 8.3 / 11.2
   if (tiles(64, 64) <= cus) KQ_TILE(1, 1, 8, 2);
-  else if (tiles(128, 64) <= cus) KQ_TILE(2, 1, 8, 2);
+  else if (tiles(128, 64) <= cus) KQ_TILE(2, 1, 4, 1);
   else if (tiles(128, 128) <= cus) KQ_TILE(2, 2, 4, 1);
   else return gemm_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
 #undef KQ_TILE
