@@ -78,7 +78,7 @@ def _random_codes(rows, K, seed):
 # ------------------------------------------------------------------------- quantizer
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-@pytest.mark.parametrize("M,K", [(1, 16), (1, 128), (3, 144), (77, 2240), (5, 512), (130, 528), (9, 4096), (2, 16400)])
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 128), (3, 144), (77, 2240), (5, 512), (130, 528), (9, 4096), (2, 16400), (1100, 2064)])
 def test_quantize(kq, M, K, dtype):
     x = _act_data(M, K, dtype, M + K)
     codes, scales = kq.quantize_fp8(x.cuda())
