@@ -662,10 +662,11 @@ def fp8_scale_cols(K):
 
 def _fp8_out(torch, rows, K, codes, scales, index, made, like=None):
     """codes and scales (made here where not given) and their addresses; like: a checked tensor of
-    codes' shape, from which torch makes them a third faster than from a shape."""
+    codes' shape.  torch makes a tensor in 1.2 us like another, 1.3 from shape and strides, 1.7 from
+    a shape alone."""
     if codes is None:
         if like is None:
-            codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=index)
+            codes = torch.empty_strided((rows, K), (K, 1), dtype=torch.float8_e4m3fn, device=index)
         else:
             codes = torch.empty_like(like, dtype=torch.float8_e4m3fn)
         made.append(codes)
@@ -674,7 +675,7 @@ def _fp8_out(torch, rows, K, codes, scales, index, made, like=None):
         c = _same(codes, "codes", torch.float8_e4m3fn, (rows, K), index)
     cols = (K + 511) // 512 * 4
     if scales is None:
-        scales = torch.empty((rows, cols), dtype=torch.uint8, device=index)
+        scales = torch.empty_strided((rows, cols), (cols, 1), dtype=torch.uint8, device=index)
         made.append(scales)
         return codes, scales, c, scales.data_ptr()
     return codes, scales, c, _same(scales, "scales", torch.uint8, (rows, cols), index)
@@ -743,7 +744,7 @@ def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, 
     made = []
     b = None if bias is None else _same(bias, "bias", dtype, (N,), index)
     if Y is None:
-        Y = torch.empty((M, N), dtype=dtype, device=index)
+        Y = torch.empty_strided((M, N), (N, 1), dtype=dtype, device=index)
         made.append(Y)
         y = Y.data_ptr()
     else:
