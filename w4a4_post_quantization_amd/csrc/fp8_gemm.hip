@@ -208,8 +208,8 @@ static hipError_t rows_go(const uint8_t* xcodes, const uint8_t* xscales, int64_t
   return hipGetLastError();
 }
 
-// Tokens the rows kernel takes; above, tiles.  Measured (us): linear 6144 x 4096, 64 tokens 9.8
-// against 11.7 in tiles, 128 tokens 13.1 against 12.3.
+// Tokens the rows kernel takes; above, tiles.  Measured (us): linear 6144 x 4096, 64 tokens 9.0
+// against 11.1 in tiles, 128 tokens 13.1 against 12.3.
 constexpr int64_t ROWS_LINEAR = 64;
 
 // The gated pair, where a second launch and the float32 outputs between them count too: to 32 tokens, and to 48
@@ -805,7 +805,8 @@ __device__ __forceinline__ void f8_big_tiles(uint8_t* __restrict__ lds, const ui
             }
           }
         // eight reads in flight, then their stores: store x takes rows 4 x .. 4 x + 3, whose swizzle
-        // depends on x % 4
+        // depends on x % 4.  SEQ: written through the level-2 cache (sc0 sc1), so that one round's
+        // outputs leave under the next one's products (16384 x 4608 x 1152: 93.5 against 98.2 us).
 #pragma unroll
         for (int x0 = 0; x0 < 8 * PJ; x0 += 8) {
           v4i v[8];
@@ -815,7 +816,7 @@ __device__ __forceinline__ void f8_big_tiles(uint8_t* __restrict__ lds, const ui
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             const v4i w = y < 4 ? v[y] : v4i{v[y].z, v[y].w, v[y].x, v[y].y};
-            __builtin_amdgcn_raw_buffer_store_b128(w, rY, (int)(to + 8u * N * (8 * j0 + x0 + y)), 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(w, rY, (int)(to + 8u * N * (8 * j0 + x0 + y)), 0, SEQ ? 17 : 0);
           }
         }
       }
