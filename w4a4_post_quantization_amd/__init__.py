@@ -42,6 +42,7 @@ KQ_OK = 0
 XFORM_NONE, XFORM_KRON, XFORM_RPBH, XFORM_DENSE, XFORM_KRON_BLOCKS = 0, 1, 2, 3, 4
 FMT_MXFP4, FMT_LM4, FMT_LM2 = 0, 1, 2
 DT_F16, DT_BF16 = 0, 1
+_PRECISE = 0x100
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _FMT = {"mxfp4": FMT_MXFP4, "lm4": FMT_LM4, "lm2": FMT_LM2}
 
@@ -732,10 +733,13 @@ def _fp8_operands(torch, xcodes, xscales, wcodes, wscales):
             _same(wcodes, "wcodes", f8, (N, K), index), _same(wscales, "wscales", u8, (N, cols), index))
 
 
-def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, stream=None):
+def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, stream=None, precise=False):
     """Y = Xq Wq^T (+ bias), fp16 or bf16 [M][N], float32 accumulation.  xcodes [M][K] and
     wcodes [N][K] float8_e4m3fn with their scale bytes (quantize_fp8); N a multiple of 16; bias
-    [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16)."""
+    [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16).  precise: every
+    product exact and added in float32, as up to 16 tokens always; else calls of more tokens take
+    the 8-bit matrix instructions, which cut products off at 2^-13 of the largest of each eight and
+    are up to twice as fast (KQ_FP8_PRECISE in kq.h)."""
     torch = _torch()
     M, N, K, index, x, xs, w, ws = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if dtype is None:
@@ -749,7 +753,7 @@ def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, 
         y = Y.data_ptr()
     else:
         y = _same(Y, "Y", dtype, (M, N), index)
-    _call(torch, "kq_fp8_linear", index, stream, made, (dt, x, xs, M, K, w, ws, N, b, y))
+    _call(torch, "kq_fp8_linear", index, stream, made, (dt | _PRECISE if precise else dt, x, xs, M, K, w, ws, N, b, y))
     return Y
 
 
@@ -759,12 +763,12 @@ def fp8_gated_linear_workspace_bytes(M, F, K):
 
 
 def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, scales=None, workspace=None,
-                     stream=None):
+                     stream=None, precise=False):
     """codes and scales (as quantize_fp8, [M][F]) of act(Xq Wg^T) * (Xq Wu^T).  wcodes [2 F][K]
     holds the F rows of Wg, then the F rows of Wu; F a multiple of 16.  act: 'silu', 'gelu' or
     'gelu_tanh'.  The result feeds fp8_linear with the down-projection's weights.  workspace: a
     uint8 device tensor of fp8_gated_linear_workspace_bytes(M, F, K) bytes (256-byte aligned); by
-    default one is taken from torch's allocator."""
+    default one is taken from torch's allocator.  precise: as in fp8_linear."""
     torch = _torch()
     if act not in _ACT:
         raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
@@ -783,5 +787,5 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
             workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
             made.append(workspace)
             wk = workspace.data_ptr()
-    _call(torch, "kq_fp8_gated_linear", index, stream, made, (_ACT[act], x, xs, M, K, w, ws, F, c, s, wk or None, nb))
+    _call(torch, "kq_fp8_gated_linear", index, stream, made, (_ACT[act] | _PRECISE if precise else _ACT[act], x, xs, M, K, w, ws, F, c, s, wk or None, nb))
     return codes, scales

@@ -12,11 +12,14 @@
 namespace kq {
 
 // act: 0 SiLU, 1 GELU, 2 GELU's tanh form, which is g / (1 + exp -2z) without tanh's cancellation.
-// GELU's g Phi(g) goes through erfc for the same reason.  The exponential is the hardware's
-// exp2 and the quotient its reciprocal (each good to one step): the correctly rounded forms
-// cost five times as many instructions, and the result is rounded to four bits next.
-template <int ACT>
+// GELU's g Phi(g) goes through erfc for the same reason.  Beside 8-bit products (not WIDE) the
+// exponential is the hardware's exp2, whose rounded argument moves the result by up to |x| 2^-24, and
+// the quotient its reciprocal: the library's forms cost five times as many instructions, and the
+// products before them are good to 1e-5 and the result is rounded to four bits next.
+template <int ACT, bool WIDE>
 __device__ __forceinline__ float f8_act(float g) {
+  if (WIDE && ACT == 0) return g / (1.0f + expf(-g));
+  if (WIDE && ACT == 2) return g / (1.0f + expf(-1.5957691216057308f * fmaf(0.044715f * g * g, g, g)));
   if (ACT == 1) return 0.5f * g * erfcf(-0.70710678118654752f * g);
   constexpr float L = 1.4426950408889634f;              // log2 e
   const float x = ACT == 0 ? -L * g : -1.5957691216057308f * L * fmaf(0.044715f * g * g, g, g);
@@ -36,9 +39,13 @@ __device__ __forceinline__ float f8_act(float g) {
 // same k for both operands.  Scale bytes of 128 groups (16384 k) at a time are staged for all.
 // WIDE: the codes are widened to bf16 with their scale applied (exact: four significant bits)
 // and multiplied by the bf16 matrix instruction, which sums in float32.  The 8-bit instruction
-// keeps about 14 bits below the largest of each four products (relative error of a sum 2e-5 to
-// 5e-5 measured, a hundredth of bf16's rounding); for up to 16 tokens there is time under the
-// loads to do without that.
+// cuts each of eight consecutive products off, towards zero, at 2^(E - 13), E the largest of their sums of
+// two exponents (norm of the errors over norm of the sums 1.0e-5 to 1.6e-5 on Gaussian values, to 7e-5 with
+// outlier channels; WIDE 1e-8 to 2e-7).  For up to 16 tokens there is time under the loads to do without
+// that; above, the caller chooses.  Measured (us) 8-bit and WIDE: linear 6144 x 4096, 17 tokens 7.7 and 7.7,
+// 37 8.2 and 8.5, 64 9.6 and 10.1; gated 11008 x 4096, 32 tokens 20.3 and 20.9; in tiles, 4096 tokens: linear 4096 x
+// 11008 144 and 308, gated 11008 x 4096 309 and 645 (bf16 instructions at half the rate, and no 256 x 256 tiles:
+// the widened fragments beside 256 accumulators exceed the registers).
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
@@ -53,13 +60,26 @@ __device__ __forceinline__ v8b f8_widen8(const v4i& w, float scale) {
   return v8b{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-template <int ACT, bool BF16, int RT, int MT, int NW, int S>   // ACT -1: the linear
+// acc + one 32 x 32 block's products of 64 k, 32 codes a lane; the order of k is the lanes' own.
+template <bool WIDE>
+__device__ __forceinline__ v16f f8_product(const v8i& a, const v8i& b, const v16f& acc, int sa, int sb) {
+  if constexpr (!WIDE) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, sa, 0, sb);
+  const v4i a0 = {a[0], a[1], a[2], a[3]}, a1 = {a[4], a[5], a[6], a[7]};
+  const v4i b0 = {b[0], b[1], b[2], b[3]}, b1 = {b[4], b[5], b[6], b[7]};
+  const float fa = __uint_as_float((uint32_t)sa << 23), fb = __uint_as_float((uint32_t)sb << 23);
+  v16f c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f8_widen8<0>(a0, fa), f8_widen8<0>(b0, fb), acc, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f8_widen8<1>(a0, fa), f8_widen8<1>(b0, fb), c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f8_widen8<0>(a1, fa), f8_widen8<0>(b1, fb), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(f8_widen8<1>(a1, fa), f8_widen8<1>(b1, fb), c, 0, 0, 0);
+}
+
+template <int ACT, bool BF16, bool WIDE, int RT, int MT, int NW, int S>   // ACT -1: the linear
 __global__ __launch_bounds__(64 * NW) void f8_rows_kernel(const uint8_t* __restrict__ wcodes,
                                                           const uint8_t* __restrict__ wscales,
                                                           const uint8_t* __restrict__ xcodes,
                                                           const uint8_t* __restrict__ xscales, int M, int N, int K,
                                                           const uint16_t* __restrict__ bias, void* __restrict__ out) {
-  constexpr bool GATED = ACT >= 0, WIDE = MT == 1;
+  constexpr bool GATED = ACT >= 0;
   constexpr int NF = RT + MT;                                  // 16-row fragments of a group: RT weight, MT token
   constexpr int SLOT = 2048 * NF, RING = NW * S * SLOT, SCALES = 2048 * NF, PART = NW * RT * MT * 1024;
   static_assert(!GATED || RT == 2, "gate and up");
@@ -134,19 +154,24 @@ __global__ __launch_bounds__(64 * NW) void f8_rows_kernel(const uint8_t* __restr
       __builtin_amdgcn_sched_barrier(0);
       slot = slot + 1 == S ? 0 : slot + 1;
       if constexpr (WIDE) {
-        v8b xb[4];
-        const float sx = __uint_as_float((uint32_t)s[RT] << 23);
-        xb[0] = f8_widen8<0>(lo[RT], sx);
-        xb[1] = f8_widen8<1>(lo[RT], sx);
-        xb[2] = f8_widen8<0>(hi[RT], sx);
-        xb[3] = f8_widen8<1>(hi[RT], sx);
+        v8b xb[MT][4];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const float sx = __uint_as_float((uint32_t)s[RT + j] << 23);
+          xb[j][0] = f8_widen8<0>(lo[RT + j], sx);
+          xb[j][1] = f8_widen8<1>(lo[RT + j], sx);
+          xb[j][2] = f8_widen8<0>(hi[RT + j], sx);
+          xb[j][3] = f8_widen8<1>(hi[RT + j], sx);
+        }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          const float w = __uint_as_float((uint32_t)s[i] << 23);
-          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<0>(lo[i], w), xb[0], acc[i][0], 0, 0, 0);
-          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<1>(lo[i], w), xb[1], acc[i][0], 0, 0, 0);
-          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<0>(hi[i], w), xb[2], acc[i][0], 0, 0, 0);
-          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen8<1>(hi[i], w), xb[3], acc[i][0], 0, 0, 0);
+          const float sw = __uint_as_float((uint32_t)s[i] << 23);
+          const v8b w[4] = {f8_widen8<0>(lo[i], sw), f8_widen8<1>(lo[i], sw), f8_widen8<0>(hi[i], sw), f8_widen8<1>(hi[i], sw)};
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[p], xb[j][p], acc[i][j], 0, 0, 0);
         }
       } else {
         auto join = [&](int f) { return v8i{lo[f].x, lo[f].y, lo[f].z, lo[f].w, hi[f].x, hi[f].y, hi[f].z, hi[f].w}; };
@@ -181,7 +206,7 @@ __global__ __launch_bounds__(64 * NW) void f8_rows_kernel(const uint8_t* __restr
     if constexpr (GATED) {
       v4f y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = f8_act<ACT>(s[0][e]) * s[1][e];
+      for (int e = 0; e < 4; ++e) y[e] = f8_act<ACT, WIDE>(s[0][e]) * s[1][e];
       *reinterpret_cast<v4f*>(static_cast<float*>(out) + (int64_t)m * N + col) = y;
     } else {
       if (bias) {
@@ -199,11 +224,11 @@ __global__ __launch_bounds__(64 * NW) void f8_rows_kernel(const uint8_t* __restr
   }
 }
 
-template <int ACT, bool BF16, int RT, int MT, int NW, int S>
+template <int ACT, bool BF16, bool WIDE, int RT, int MT, int NW, int S>
 static hipError_t rows_go(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K, const uint8_t* wcodes,
                           const uint8_t* wscales, int64_t N, const uint16_t* bias, void* out, hipStream_t s) {
   const int64_t per = ACT >= 0 ? 16 : 16 * RT;
-  hipLaunchKernelGGL((f8_rows_kernel<ACT, BF16, RT, MT, NW, S>), dim3((unsigned)((N + per - 1) / per)), dim3(64 * NW), 0,
+  hipLaunchKernelGGL((f8_rows_kernel<ACT, BF16, WIDE, RT, MT, NW, S>), dim3((unsigned)((N + per - 1) / per)), dim3(64 * NW), 0,
                      s, wcodes, wscales, xcodes, xscales, (int)M, (int)N, (int)K, bias, out);
   return hipGetLastError();
 }
@@ -219,11 +244,11 @@ constexpr int64_t ROWS_LINEAR = 64;
 static bool gated_rows(int64_t M, int64_t F) { return M <= 32 || (M <= 48 && F <= 12288) || (M <= 64 && F <= 8192); }
 
 template <int ACT, bool BF16>
-static hipError_t rows_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+static hipError_t rows_launch(bool precise, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                               const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
                               void* out, hipStream_t s) {
 #define KQ_ROWS(RT, MT, NW, S) \
-  rows_go<ACT, BF16, RT, MT, NW, S>(xcodes, xscales, M, K, wcodes, wscales, N, bias, out, s)
+  (precise || MT == 1 ? rows_go<ACT, BF16, true, RT, MT, NW, S> : rows_go<ACT, BF16, (MT == 1), RT, MT, NW, S>)(xcodes, xscales, M, K, wcodes, wscales, N, bias, out, s)
   if constexpr (ACT >= 0) {
     // two workgroups on a compute unit; one of twice the LDS took 20.7 against 17.7 us (one token, 11008 x
     // 4096) and 22.6 against 19.0 (32 tokens)
@@ -276,7 +301,7 @@ struct F8Small {
 __device__ __forceinline__ int f8_swz(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
 
 // Weight rows n0 .. n0 + BN - 1, token rows m0 .. m0 + BM - 1.
-template <bool BF16, class C>
+template <bool BF16, bool WIDE, class C>
 __device__ __forceinline__ void f8_small_tile(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
                                               const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
                                               const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
@@ -413,7 +438,7 @@ __device__ __forceinline__ void f8_small_tile(uint8_t* __restrict__ lds, const u
         const int* const sc = s[G == 1 ? 0 : u];
         // behind the last group the codes are zeros, and no scale byte found there may be NaN
         const int on = G == 1 || k0 + c < nk ? -1 : 0;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[u][c][i], b[u][c][j], acc[i][j], 0, 0, 0, sc[i] & on, 0, sc[TN + j] & on);
+        acc[i][j] = f8_product<WIDE>(a[u][c][i], b[u][c][j], acc[i][j], sc[i] & on, sc[TN + j] & on);
         __builtin_amdgcn_sched_barrier(0);
         if (m == 0) {
           if (u == 0) scale_loads((ks >> 5) + 1, ks & 31);
@@ -511,7 +536,7 @@ struct F8Big {
 // same columns f0 + col0 + 32 i .., lane l's token of block j row0 + 32 j + l % 32.  Outputs in place
 // of the gates, the maximum of each token's columns in this wave to LDS, and after the barrier the
 // scale of all 128 (columns past F are zeros on both sides and stay zeros).
-template <int ACT, int TM>
+template <int ACT, bool WIDE, int TM>
 __device__ __forceinline__ void f8_gated_store(v16f (&acc)[4][TM], uint8_t* __restrict__ lds_tops, int wn, int col0,
                                                int row0, int l32, int h, int64_t m0, int64_t mleft, int f0, int F,
                                                uint8_t* __restrict__ out, uint8_t* __restrict__ oscales) {
@@ -523,7 +548,7 @@ __device__ __forceinline__ void f8_gated_store(v16f (&acc)[4][TM], uint8_t* __re
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float v = f8_act<ACT>(acc[i][j][e]) * acc[i + 2][j][e];
+        const float v = f8_act<ACT, WIDE>(acc[i][j][e]) * acc[i + 2][j][e];
         acc[i][j][e] = v;
         top = umax32(top, abs_bits(v));
       }
@@ -569,7 +594,7 @@ __device__ __forceinline__ void f8_gated_store(v16f (&acc)[4][TM], uint8_t* __re
 // at(t, m0, n0) gives tile t's place.  SEQ: the workgroup takes tiles t0, t0 + step, .. below end, and
 // the loads past one tile's last stage are the next one's first: both slots of a gated tile, one of the
 // linear's, whose outputs go through the other.  So only the first tile waits for memory.  T >= NS.
-template <int ACT, bool BF16, class C, bool SEQ, class At>
+template <int ACT, bool BF16, bool WIDE, class C, bool SEQ, class At>
 __device__ __forceinline__ void f8_big_tiles(uint8_t* __restrict__ lds, const uint8_t* __restrict__ wcodes,
                                             const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
                                             const uint8_t* __restrict__ xscales, int64_t M, int N, int K,
@@ -711,7 +736,7 @@ __device__ __forceinline__ void f8_big_tiles(uint8_t* __restrict__ lds, const ui
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         const int i = m / TM, j = m % TM;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[0][i], b[0][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
+        acc[i][j] = f8_product<WIDE>(a[0][i], b[0][j], acc[i][j], s[i], s[4 + j]);
         __builtin_amdgcn_sched_barrier(0);
         if (m < ND) {
 #pragma unroll
@@ -735,7 +760,7 @@ __device__ __forceinline__ void f8_big_tiles(uint8_t* __restrict__ lds, const ui
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         const int i = m / TM, j = m % TM;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[1][i], b[1][j], acc[i][j], 0, 0, 0, s[i], 0, s[4 + j]);
+        acc[i][j] = f8_product<WIDE>(a[1][i], b[1][j], acc[i][j], s[i], s[4 + j]);
         __builtin_amdgcn_sched_barrier(0);
         if (m < NE) {
 #pragma unroll
@@ -821,7 +846,7 @@ __device__ __forceinline__ void f8_big_tiles(uint8_t* __restrict__ lds, const ui
         }
       }
     } else {
-      f8_gated_store<ACT, TM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out, oscales);
+      f8_gated_store<ACT, WIDE, TM>(acc, lds + C::TOP_OFF, wn, wrow_a, wrow_b, l32, h, m0, mleft, n0 >> 1, N, out, oscales);
     }
     if (!SEQ || (t += step) >= end) break;
     sbuf = (sbuf + (T + 15) / 16) & 1;
@@ -862,7 +887,7 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
       m0 = 256LL * (first + in % rows);
       n0 = 256 * (in / rows);
     };
-    f8_big_tiles<ACT, BF16, F8Large, SEQ>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, at,
+    f8_big_tiles<ACT, BF16, false, F8Large, SEQ>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, at,
                                            blockIdx.x, nfull, gfull);
   } else {
     auto at = [&](int t, int64_t& m0, int& n0) {
@@ -870,36 +895,50 @@ __global__ __launch_bounds__(256, 1) void f8_gemm_kernel(
       m0 = 256LL * full_rows + 128LL * (q % rest);
       n0 = 256 * (q / rest);
     };
-    f8_big_tiles<ACT, BF16, F8Half, false>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, at,
+    f8_big_tiles<ACT, BF16, false, F8Half, false>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, at,
                                            (int)blockIdx.x - gfull, nrest, 1);
   }
 }
 
-template <bool BF16, class C>
+template <bool BF16, bool WIDE, class C>
 __global__ __launch_bounds__(256, 1) void f8_small_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
     uint8_t* __restrict__ out) {
   __shared__ __align__(16) uint8_t lds[C::LDS];
   const int rows = (int)((M + C::BM - 1) / C::BM), pid = f8_remap(blockIdx.x, gridDim.x);
-  f8_small_tile<BF16, C>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, (int64_t)C::BM * (pid % rows),
+  f8_small_tile<BF16, WIDE, C>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, (int64_t)C::BM * (pid % rows),
                          C::BN * (pid / rows));
 }
 
-// Tiles of 256 x 64 tokens, one per workgroup: a gated call's middling token counts.
-template <int ACT>
-__global__ __launch_bounds__(256, 1) void f8_low_kernel(
+// One tile per workgroup, grouped eight along M: 256 x 64 tokens for a gated call's middling token
+// counts, 256 x 128 for all calls of more tokens whose products are to be in float32.
+template <int ACT, bool BF16, bool WIDE, class C>
+__global__ __launch_bounds__(256, 1) void f8_tiles_kernel(
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, const uint8_t* __restrict__ xcodes,
-    const uint8_t* __restrict__ xscales, int64_t M, int N, int K, uint8_t* __restrict__ out,
-    uint8_t* __restrict__ oscales) {
-  __shared__ __align__(16) uint8_t lds[F8Low::LDS];
-  const int rows = (int)((M + F8Low::BM - 1) / F8Low::BM), pid = f8_remap(blockIdx.x, gridDim.x);
+    const uint8_t* __restrict__ xscales, int64_t M, int N, int K, const uint16_t* __restrict__ bias,
+    uint8_t* __restrict__ out, uint8_t* __restrict__ oscales) {
+  __shared__ __align__(16) uint8_t lds[C::LDS];
+  constexpr int GM = 8;
+  const int tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256, tiles_m = (int)((M + C::BM - 1) / C::BM);
   auto at = [&](int, int64_t& m0, int& n0) {
-    m0 = (int64_t)F8Low::BM * (pid % rows);
-    n0 = 256 * (pid / rows);
+    const int pid = f8_remap(blockIdx.x, gridDim.x);
+    const int first = pid / (GM * tiles_n) * GM, rows = min(tiles_m - first, GM), in = pid % (GM * tiles_n);
+    m0 = (int64_t)C::BM * (first + in % rows);
+    n0 = 256 * (in / rows);
   };
-  f8_big_tiles<ACT, false, F8Low, false>(lds, wcodes, wscales, xcodes, xscales, M, N, K, nullptr, out, oscales, at, 0,
-                                         1, 1);
+  f8_big_tiles<ACT, BF16, WIDE, C, false>(lds, wcodes, wscales, xcodes, xscales, M, N, K, bias, out, oscales, at, 0, 1,
+                                          1);
+}
+
+template <int ACT, bool BF16, bool WIDE, class C>
+static hipError_t tiles_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+                               const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
+                               uint8_t* out, uint8_t* oscales, hipStream_t s) {
+  const int64_t tiles_n = ACT >= 0 ? (N + 127) / 128 : (N + 255) / 256, tiles_m = (M + C::BM - 1) / C::BM;
+  hipLaunchKernelGGL((f8_tiles_kernel<ACT, BF16, WIDE, C>), dim3((unsigned)(tiles_n * tiles_m)), dim3(256), 0, s, wcodes,
+                     wscales, xcodes, xscales, M, (int)N, (int)K, bias, out, oscales);
+  return hipGetLastError();
 }
 
 template <int ACT, bool BF16>
@@ -945,15 +984,15 @@ static hipError_t gemm_launch(const uint8_t* xcodes, const uint8_t* xscales, int
 
 // The smallest tiles that give at most one workgroup per compute unit: fewer, larger tiles read
 // less, but a chain of k over few compute units is bound by what one of them can take in.
-template <bool BF16>
+template <bool BF16, bool WIDE>
 static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                                 const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
                                 uint8_t* Y, hipStream_t s) {
-  if (M <= ROWS_LINEAR) return rows_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
+  if (M <= ROWS_LINEAR) return rows_launch<-1, BF16>(WIDE, xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
   const int64_t cus = device_cu_count();
   auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
 #define KQ_TILE(...)                                                                                                \
-  hipLaunchKernelGGL((f8_small_kernel<BF16, F8Small<__VA_ARGS__>>),                                                  \
+  hipLaunchKernelGGL((f8_small_kernel<BF16, WIDE, F8Small<__VA_ARGS__>>),                                                  \
                      dim3((unsigned)tiles(F8Small<__VA_ARGS__>::BN, F8Small<__VA_ARGS__>::BM)), dim3(256), 0, s,     \
                      wcodes, wscales, xcodes, xscales, M, (int)N, (int)K, bias, Y)
   // measured (us) at 4096 x 4096 with 64 x 64 / 128 x 64 / 128 x 128 / 256 x 256: 200 tokens 12.0 /
@@ -962,30 +1001,30 @@ static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, i
   if (tiles(64, 64) <= cus) KQ_TILE(1, 1, 8, 2);
   else if (tiles(128, 64) <= cus) KQ_TILE(2, 1, 4, 1);
   else if (tiles(128, 128) <= cus) KQ_TILE(2, 2, 4, 1);
+  else if constexpr (WIDE) return tiles_launch<-1, BF16, true, F8Half>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
   else return gemm_launch<-1, BF16>(xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, nullptr, s);
 #undef KQ_TILE
   return hipGetLastError();
 }
 
-hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+hipError_t launch_f8_linear(bool bf16, bool precise, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                             const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const void* bias, void* Y,
                             hipStream_t s) {
-  const uint16_t* b = static_cast<const uint16_t*>(bias);
-  uint8_t* y = static_cast<uint8_t*>(Y);
-  return bf16 ? linear_launch<true>(xcodes, xscales, M, K, wcodes, wscales, N, b, y, s)
-              : linear_launch<false>(xcodes, xscales, M, K, wcodes, wscales, N, b, y, s);
+  const auto go = bf16 ? precise ? linear_launch<true, true> : linear_launch<true, false>
+                       : precise ? linear_launch<false, true> : linear_launch<false, false>;
+  return go(xcodes, xscales, M, K, wcodes, wscales, N, static_cast<const uint16_t*>(bias), static_cast<uint8_t*>(Y), s);
 }
 
 size_t f8_gated_workspace_bytes(int64_t M, int64_t F, int64_t) { return gated_rows(M, F) ? (size_t)M * F * 4 : 0; }
 
-template <int ACT>
+template <int ACT, bool WIDE>
 static hipError_t gated_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                                const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,
                                uint8_t* scales, void* workspace, hipStream_t s) {
   if (gated_rows(M, F)) {
     // a workgroup's 16 columns are an eighth of a scale group: the outputs go through the
     // workspace in float32 and the quantizer
-    const hipError_t e = rows_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, workspace, s);
+    const hipError_t e = rows_launch<ACT, false>(WIDE, xcodes, xscales, M, K, wcodes, wscales, F, nullptr, workspace, s);
     if (e != hipSuccess) return e;
     return launch_f8_quantize_f32(static_cast<const float*>(workspace), M, F, codes, scales, s);
   }
@@ -993,22 +1032,21 @@ static hipError_t gated_launch(const uint8_t* xcodes, const uint8_t* xscales, in
   // / 256 tokens: 128 tokens, 11008 x 4096 26.6 / 30.9 / 37; 203 tokens 45 / 30 / 37; 203 tokens, 5600 x
   // 2240 15.2 / 18.7 / 21
   const int64_t tiles = (F + 127) / 128 * ((M + F8Low::BM - 1) / F8Low::BM);
-  if (tiles <= device_cu_count()) {
-    hipLaunchKernelGGL((f8_low_kernel<ACT>), dim3((unsigned)tiles), dim3(256), 0, s, wcodes, wscales, xcodes, xscales, M,
-                       (int)F, (int)K, codes, scales);
-    return hipGetLastError();
-  }
-  return gemm_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
+  if (tiles <= device_cu_count())
+    return tiles_launch<ACT, false, WIDE, F8Low>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
+  if constexpr (WIDE)
+    return tiles_launch<ACT, false, true, F8Half>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
+  else
+    return gemm_launch<ACT, false>(xcodes, xscales, M, K, wcodes, wscales, F, nullptr, codes, scales, s);
 }
 
-hipError_t launch_f8_gated(int act, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+hipError_t launch_f8_gated(int act, bool precise, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                            const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes, uint8_t* scales,
                            void* workspace, hipStream_t s) {
-  switch (act) {
-    case 0: return gated_launch<0>(xcodes, xscales, M, K, wcodes, wscales, F, codes, scales, workspace, s);
-    case 1: return gated_launch<1>(xcodes, xscales, M, K, wcodes, wscales, F, codes, scales, workspace, s);
-    default: return gated_launch<2>(xcodes, xscales, M, K, wcodes, wscales, F, codes, scales, workspace, s);
-  }
+  const auto go = act == 0   ? precise ? gated_launch<0, true> : gated_launch<0, false>
+                  : act == 1 ? precise ? gated_launch<1, true> : gated_launch<1, false>
+                             : precise ? gated_launch<2, true> : gated_launch<2, false>;
+  return go(xcodes, xscales, M, K, wcodes, wscales, F, codes, scales, workspace, s);
 }
 
 }  // namespace kq

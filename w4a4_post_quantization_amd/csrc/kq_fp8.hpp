@@ -110,12 +110,13 @@ hipError_t launch_f8_quantize_f32(const float* X, int64_t M, int64_t K, uint8_t*
 hipError_t launch_f8_rmsnorm(bool bf16, const void* X, const void* residual, const void* gamma, float eps, int64_t M,
                              int64_t K, uint8_t* codes, uint8_t* scales, void* residual_out, hipStream_t s);
 
-hipError_t launch_f8_linear(bool bf16, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+// precise: products of the exact codes summed in float32 whatever the number of tokens
+hipError_t launch_f8_linear(bool bf16, bool precise, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                             const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const void* bias, void* Y,
                             hipStream_t s);
 size_t f8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K);
 // act: 0 SiLU, 1 GELU (erf), 2 GELU (tanh)
-hipError_t launch_f8_gated(int act, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
+hipError_t launch_f8_gated(int act, bool precise, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                            const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes, uint8_t* scales,
                            void* workspace, hipStream_t s);
 

@@ -57,6 +57,8 @@ kq_status kq_rmsnorm_quantize_fp8(int32_t dtype, const void* X, const void* resi
 kq_status kq_fp8_linear(int32_t dtype, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                         const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const void* bias, void* Y,
                         hipStream_t stream) {
+  const bool precise = dtype & KQ_FP8_PRECISE;
+  dtype &= ~KQ_FP8_PRECISE;
   if (!xcodes || !xscales || !wcodes || !wscales || !Y) return KQ_ERR_NULL;
   if (!dtype_ok(dtype)) return KQ_ERR_UNSUPPORTED;
   kq_status st = check_rows(M, K);
@@ -64,7 +66,8 @@ kq_status kq_fp8_linear(int32_t dtype, const uint8_t* xcodes, const uint8_t* xsc
   if (st != KQ_OK) return st;
   if (!aligned(xcodes, 16) || !aligned(wcodes, 16) || !aligned(Y, 16) || !aligned(bias, 16)) return KQ_ERR_ALIGN;
   if (!aligned(xscales, 4) || !aligned(wscales, 4)) return KQ_ERR_ALIGN;
-  return hip_status(launch_f8_linear(dtype == KQ_DT_BF16, xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, stream));
+  return hip_status(launch_f8_linear(dtype == KQ_DT_BF16, precise, xcodes, xscales, M, K, wcodes, wscales, N, bias, Y,
+                                     stream));
 }
 
 size_t kq_fp8_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) {
@@ -75,6 +78,8 @@ size_t kq_fp8_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) {
 kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                               const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,
                               uint8_t* scales, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const bool precise = act & KQ_FP8_PRECISE;
+  act &= ~KQ_FP8_PRECISE;
   if (!xcodes || !xscales || !wcodes || !wscales || !codes || !scales) return KQ_ERR_NULL;
   if (act < KQ_ACT_SILU || act > KQ_ACT_GELU_TANH) return KQ_ERR_UNSUPPORTED;
   kq_status st = check_rows(M, K);
@@ -86,7 +91,8 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
   const size_t need = f8_gated_workspace_bytes(M, F, K);
   if (need && (!workspace || workspace_bytes < need)) return KQ_ERR_WORKSPACE;
   if (need && !aligned(workspace, 256)) return KQ_ERR_ALIGN;
-  return hip_status(launch_f8_gated(act, xcodes, xscales, M, K, wcodes, wscales, F, codes, scales, workspace, stream));
+  return hip_status(launch_f8_gated(act, precise, xcodes, xscales, M, K, wcodes, wscales, F, codes, scales, workspace,
+                                    stream));
 }
 
 }  // extern "C"
