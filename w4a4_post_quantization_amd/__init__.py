@@ -19,9 +19,11 @@ library is missing: there is no fallback.
     codes, scales = kq.fp8_gated_linear(codes, scales, gate_up_codes, gate_up_scales, act="silu")
     X = kq.fp8_linear(codes, scales, down_codes, down_scales, dtype=X.dtype)
 
-Outputs and workspaces that the binding allocates itself are marked as used on the stream
-the call runs on (``record_stream``), so torch's allocator does not hand their memory to
-another stream's work before the call has finished there.
+With ``stream`` a call runs with that stream as torch's current one: outputs and workspaces that
+the binding allocates itself are then that stream's memory, so no work still pending on another
+stream writes into them.  Outputs are also marked as used on the stream that was current before
+the call (``record_stream``), where their user may drop them while its own work on them is pending.
+Given tensors are the caller's to order.
 """
 
 import ctypes
@@ -137,12 +139,13 @@ def status_str(s):
 def clock_probe(spin_us, out=None, stream=None):
     """Launch the shader-clock probe on `stream` (see kq_clock_probe): returns the device
     uint64 [2] tensor that will hold (shader cycles, 100 MHz reference ticks)."""
+    if stream is not None:
+        return _on(stream, clock_probe, spin_us, out)
     torch = _torch()
     if out is None:
         out = torch.empty((2,), dtype=torch.int64, device="cuda")      # no fill kernel to race with
-        _on_stream(stream, out)
     _check(out, "out", torch.int64, (2,))
-    s = load().kq_clock_probe(int(spin_us), _ptr(out), _stream(stream))
+    s = load().kq_clock_probe(int(spin_us), _ptr(out), _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_clock_probe")
     return out
@@ -153,14 +156,15 @@ def mfma_fp4_probe(iters, workgroups, codes, out=None, stream=None):
     device uint8 tensor of at least 2048 bytes (its first 2048 are the operands); returns the
     float32 [4 * workgroups] tensor of per-wavefront sums.  The caller times the launch; the
     work is 64 * iters * workgroups products of 2 * 32 * 32 * 64 flops."""
+    if stream is not None:
+        return _on(stream, mfma_fp4_probe, iters, workgroups, codes, out)
     torch = _torch()
     if codes.dtype != torch.uint8 or not codes.is_cuda or not codes.is_contiguous() or codes.numel() < 2048:
         raise ValueError("codes must be a contiguous device uint8 tensor of at least 2048 bytes")
     if out is None:
         out = torch.empty((4 * int(workgroups),), dtype=torch.float32, device=codes.device)
-        _on_stream(stream, out)
     _check(out, "out", torch.float32, (4 * int(workgroups),))
-    s = load().kq_mfma_fp4_probe(int(iters), int(workgroups), _ptr(codes), _ptr(out), _stream(stream))
+    s = load().kq_mfma_fp4_probe(int(iters), int(workgroups), _ptr(codes), _ptr(out), _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_mfma_fp4_probe")
     return out
@@ -192,25 +196,31 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream():
+    return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
 
 
-def _on_stream(stream, *made):
-    """Tensors this binding allocated on torch's current stream but handed to a call on
-    another stream: record that stream on them, so their memory is not reused before the
-    call has finished there (torch's caching allocator otherwise only waits for the
-    stream they were allocated on)."""
-    if stream is None:
-        return
+def _on(stream, f, *args, **kw):
+    """f(*args, **kw) with `stream` as the current stream.  Memory of the allocator belongs to the
+    stream it was allocated for: taken for another one, its last owner's kernels may still be
+    writing to it.  Outputs made here are recorded on the caller's stream as well."""
     torch = _torch()
-    if stream == torch.cuda.current_stream():
-        return
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
+    here = torch.cuda.current_stream(stream.device)
+    device = torch.cuda.current_device()
+    if stream == here and stream.device.index == device:
+        return f(*args, **kw)
+    torch.cuda.set_stream(stream)                            # and its device; 5 us less than the context manager
+    try:
+        out = f(*args, **kw)
+    finally:
+        torch.cuda.set_stream(here)
+        if stream.device.index != device:
+            torch.cuda.set_device(device)
+    given = [id(t) for t in (*args, *kw.values())]
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and id(t) not in given:
+            t.record_stream(here)
+    return out
 
 
 def _check(t, name, dtype, shape=None):
@@ -313,6 +323,8 @@ def _flat(a):
 
 def transform_quantize(X, xform, fmt="mxfp4", center=False, codes=None, scales=None, mu=None, stream=None):
     """[centre] -> block transform -> 4-bit quantize + pack.  Returns (codes, scales, mu)."""
+    if stream is not None:
+        return _on(stream, transform_quantize, X, xform, fmt, center, codes, scales, mu)
     torch = _torch()
     _check(X, "X", torch.float16)
     if X.dim() != 2:
@@ -322,15 +334,12 @@ def transform_quantize(X, xform, fmt="mxfp4", center=False, codes=None, scales=N
     if f not in (FMT_MXFP4, FMT_LM4):
         raise ValueError("fmt must be 'mxfp4' or 'lm4'")
     dev = X.device
-    made = []
     if codes is None:
         codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
-        made.append(codes)
     _check(codes, "codes", torch.uint8, (M, K // 2))
     if scales is None:
         scales = torch.empty((M, K // 32) if f == FMT_MXFP4 else (M,),
                              dtype=torch.uint8 if f == FMT_MXFP4 else torch.float32, device=dev)
-        made.append(scales)
     if f == FMT_MXFP4:
         _check(scales, "scales", torch.uint8, (M, K // 32))
     else:
@@ -338,19 +347,17 @@ def transform_quantize(X, xform, fmt="mxfp4", center=False, codes=None, scales=N
     if center:
         if mu is None:
             mu = torch.empty((M,), dtype=torch.float16, device=dev)
-            made.append(mu)
         _check(mu, "mu", torch.float16, (M,))
     else:
         mu = None
-    _on_stream(stream, *made)
     s = load().kq_transform_quantize(xform.c(), f, int(bool(center)), _ptr(X), M, K, _ptr(codes), _ptr(scales),
-                                     _ptr(mu), _stream(stream))
+                                     _ptr(mu), _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_transform_quantize")
     return codes, scales, mu
 
 
-def _fold(name, W, N, K, xform, fmt, with_wbar, stream):
+def _fold(name, W, N, K, xform, fmt, with_wbar):
     torch = _torch()
     f = _FMT[fmt]
     dev = W.device
@@ -363,12 +370,11 @@ def _fold(name, W, N, K, xform, fmt, with_wbar, stream):
     else:
         raise ValueError("fmt must be 'mxfp4' or 'lm2'")
     wbar = torch.empty((N,), dtype=torch.float16, device=dev) if with_wbar else None
-    _on_stream(stream, wcodes, wscales, wbar)
     fn = getattr(load(), name)
     if name == "kq_fold_inverse_into_weights":
-        s = fn(xform.c(), f, _ptr(W), K, N, _ptr(wcodes), _ptr(wscales), _ptr(wbar), _stream(stream))
+        s = fn(xform.c(), f, _ptr(W), K, N, _ptr(wcodes), _ptr(wscales), _ptr(wbar), _stream())
     else:
-        s = fn(xform.c(), f, _ptr(W), N, K, _ptr(wcodes), _ptr(wscales), _ptr(wbar), _stream(stream))
+        s = fn(xform.c(), f, _ptr(W), N, K, _ptr(wcodes), _ptr(wscales), _ptr(wbar), _stream())
     if s != KQ_OK:
         raise KQError(s, name)
     return wcodes, wscales, wbar
@@ -377,22 +383,26 @@ def _fold(name, W, N, K, xform, fmt, with_wbar, stream):
 def fold_inverse_into_weights(W, xform, fmt="mxfp4", with_wbar=True, stream=None):
     """Offline: W' = P^-1 W, quantized along K.  W is fp16 [K][N] (Y = X W).
     Returns (wcodes [N][K/2], wscales [N][K/32], wbar [N] or None)."""
+    if stream is not None:
+        return _on(stream, fold_inverse_into_weights, W, xform, fmt, with_wbar)
     torch = _torch()
     _check(W, "W", torch.float16)
     if W.dim() != 2:
         raise ValueError("W must be 2-D [K, N]")
     K, N = W.shape
-    return _fold("kq_fold_inverse_into_weights", W, N, K, xform, fmt, with_wbar, stream)
+    return _fold("kq_fold_inverse_into_weights", W, N, K, xform, fmt, with_wbar)
 
 
 def fold_inverse_into_weights_nk(Wt, xform, fmt="mxfp4", with_wbar=True, stream=None):
     """The same fold for weights in the [out][in] layout: Wt is fp16 [N][K]."""
+    if stream is not None:
+        return _on(stream, fold_inverse_into_weights_nk, Wt, xform, fmt, with_wbar)
     torch = _torch()
     _check(Wt, "Wt", torch.float16)
     if Wt.dim() != 2:
         raise ValueError("Wt must be 2-D [N, K]")
     N, K = Wt.shape
-    return _fold("kq_fold_inverse_into_weights_nk", Wt, N, K, xform, fmt, with_wbar, stream)
+    return _fold("kq_fold_inverse_into_weights_nk", Wt, N, K, xform, fmt, with_wbar)
 
 
 def lowrank_down_workspace_bytes(M, K, r):
@@ -404,25 +414,23 @@ def lowrank_down(X, L1, T=None, workspace=None, stream=None):
     """T = fp16(X L1^T): the low-rank branch's down-projection (fp16 [M][r]).  workspace:
     a uint8 device tensor for the split-K partials; by default one of the size
     lowrank_down_workspace_bytes is taken from torch's allocator."""
+    if stream is not None:
+        return _on(stream, lowrank_down, X, L1, T, workspace)
     torch = _torch()
     _check(X, "X", torch.float16)
     M, K = X.shape
     r = L1.shape[0]
     _check(L1, "L1", torch.float16, (r, K))
-    made = []
     if T is None:
         T = torch.empty((M, r), dtype=torch.float16, device=X.device)
-        made.append(T)
     _check(T, "T", torch.float16, (M, r))
     if workspace is None:
         nb = lowrank_down_workspace_bytes(M, K, r)
         workspace = torch.empty((nb,), dtype=torch.uint8, device=X.device) if nb else None
-        made.append(workspace)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8)
-    _on_stream(stream, *made)
     wp, wn = (_ptr(workspace), workspace.numel()) if workspace is not None else (None, 0)
-    s = load().kq_lowrank_down(_ptr(X), _ptr(L1), M, K, r, _ptr(T), wp, wn, _stream(stream))
+    s = load().kq_lowrank_down(_ptr(X), _ptr(L1), M, K, r, _ptr(T), wp, wn, _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_lowrank_down")
     return T
@@ -433,6 +441,8 @@ def transform_quantize_lowrank(X, xform, L1, center=False, codes=None, scales=No
     """One pass over X: MXFP4 codes and scales of the (optionally centred, RPBH only)
     block-transformed X and the low-rank down-projection T = fp16(X L1^T).
     Returns (codes, scales, mu or None, T)."""
+    if stream is not None:
+        return _on(stream, transform_quantize_lowrank, X, xform, L1, center, codes, scales, mu, T, workspace)
     torch = _torch()
     _check(X, "X", torch.float16)
     if X.dim() != 2:
@@ -441,36 +451,29 @@ def transform_quantize_lowrank(X, xform, L1, center=False, codes=None, scales=No
     r = L1.shape[0]
     _check(L1, "L1", torch.float16, (r, K))
     dev = X.device
-    made = []
     if codes is None:
         codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
-        made.append(codes)
     _check(codes, "codes", torch.uint8, (M, K // 2))
     if scales is None:
         scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
-        made.append(scales)
     _check(scales, "scales", torch.uint8, (M, K // 32))
     if center:
         if mu is None:
             mu = torch.empty((M,), dtype=torch.float16, device=dev)
-            made.append(mu)
         _check(mu, "mu", torch.float16, (M,))
     else:
         mu = None
     if T is None:
         T = torch.empty((M, r), dtype=torch.float16, device=dev)
-        made.append(T)
     _check(T, "T", torch.float16, (M, r))
     if workspace is None:
         nb = lowrank_down_workspace_bytes(M, K, r)
         workspace = torch.empty((nb,), dtype=torch.uint8, device=dev) if nb else None
-        made.append(workspace)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8)
-    _on_stream(stream, *made)
     wp, wn = (_ptr(workspace), workspace.numel()) if workspace is not None else (None, 0)
     s = load().kq_transform_quantize_lowrank(xform.c(), int(bool(center)), _ptr(X), M, K, _ptr(codes), _ptr(scales),
-                                             _ptr(mu), _ptr(L1), r, _ptr(T), wp, wn, _stream(stream))
+                                             _ptr(mu), _ptr(L1), r, _ptr(T), wp, wn, _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_transform_quantize_lowrank")
     return codes, scales, mu, T
@@ -483,6 +486,8 @@ def svd_lowrank_workspace_bytes(N, K, r, l):
 def svd_lowrank(W, r, omega, iters=4, L1=None, L2=None, R=None, sigma=None, workspace=None, stream=None):
     """Offline rank-r extraction: W (fp16 [N][K]) ~ L2 L1 + R.  omega: float32 [K][l]
     device starting block (l > r).  Returns (L1 [r][K], L2 [N][r], R [N][K], sigma [r])."""
+    if stream is not None:
+        return _on(stream, svd_lowrank, W, r, omega, iters, L1, L2, R, sigma, workspace)
     torch = _torch()
     _check(W, "W", torch.float16)
     N, K = W.shape
@@ -491,12 +496,9 @@ def svd_lowrank(W, r, omega, iters=4, L1=None, L2=None, R=None, sigma=None, work
         raise ValueError("omega must be [K, l]")
     l = omega.shape[1]
     dev = W.device
-    made = []
 
     def _new(shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-        made.append(t)
-        return t
+        return torch.empty(shape, dtype=dtype, device=dev)
     L1 = _new((r, K), torch.float16) if L1 is None else L1
     L2 = _new((N, r), torch.float16) if L2 is None else L2
     R = _new((N, K), torch.float16) if R is None else R
@@ -509,9 +511,8 @@ def svd_lowrank(W, r, omega, iters=4, L1=None, L2=None, R=None, sigma=None, work
     if workspace is None:
         workspace = _new((max(nb, 256),), torch.uint8)
     _check(workspace, "workspace", torch.uint8)
-    _on_stream(stream, *made)
     s = load().kq_svd_lowrank(_ptr(W), N, K, r, _ptr(omega), l, int(iters), _ptr(L1), _ptr(L2), _ptr(R),
-                              _ptr(sigma), _ptr(workspace), workspace.numel(), _stream(stream))
+                              _ptr(sigma), _ptr(workspace), workspace.numel(), _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_svd_lowrank")
     return L1, L2, R, sigma
@@ -539,10 +540,8 @@ def _linear_tail(M, N, mu, wbar, Y, dev):
     if mu is not None:
         _check(mu, "mu", torch.float16, (M,))
         _check(wbar, "wbar", torch.float16, (N,))
-    made = Y is None
     Y = torch.empty((M, N), dtype=torch.float16, device=dev) if Y is None else Y
-    _check(Y, "Y", torch.float16, (M, N))
-    return Y, made
+    return _check(Y, "Y", torch.float16, (M, N))
 
 
 def w4a4_linear_workspace_bytes(M, r):
@@ -557,6 +556,8 @@ def w4a4_linear(xcodes, xscales, wcodes, wscales, X=None, L1=None, L2=None, mu=N
     [M][K], L1 fp16 [r][K], L2 fp16 [N][r].  workspace: a uint8 device tensor of at least
     w4a4_linear_workspace_bytes(M, r) bytes (256-byte aligned); by default one is taken
     from torch's allocator.  fmt 'mxfp4' (W4A4) or 'lm2' (W2A4, no branches)."""
+    if stream is not None:
+        return _on(stream, w4a4_linear, xcodes, xscales, wcodes, wscales, X, L1, L2, mu, wbar, fmt, Y, workspace)
     torch = _torch()
     f, M, K, N = _linear_operands(xcodes, xscales, wcodes, wscales, fmt)
     r = 0
@@ -565,18 +566,15 @@ def w4a4_linear(xcodes, xscales, wcodes, wscales, X=None, L1=None, L2=None, mu=N
         _check(X, "X", torch.float16, (M, K))
         _check(L1, "L1", torch.float16, (r, K))
         _check(L2, "L2", torch.float16, (N, r))
-    Y, made_y = _linear_tail(M, N, mu, wbar, Y, xcodes.device)
-    made = [Y] if made_y else []
+    Y = _linear_tail(M, N, mu, wbar, Y, xcodes.device)
     if r and workspace is None:
         workspace = torch.empty((w4a4_linear_workspace_bytes(M, r),), dtype=torch.uint8, device=xcodes.device)
-        made.append(workspace)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8)
-    _on_stream(stream, *made)
     wp, wn = (_ptr(workspace), workspace.numel()) if workspace is not None else (None, 0)
     s = load().kq_w4a4_linear(f, _ptr(xcodes), _ptr(xscales), M, K, _ptr(wcodes), _ptr(wscales), N,
                               _ptr(X if r else None), _ptr(L1 if r else None), _ptr(L2 if r else None), r,
-                              _ptr(mu), _ptr(wbar), _ptr(Y), wp, wn, _stream(stream))
+                              _ptr(mu), _ptr(wbar), _ptr(Y), wp, wn, _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_w4a4_linear")
     return Y
@@ -586,6 +584,8 @@ def w4a4_linear_t(xcodes, xscales, wcodes, wscales, T=None, L2=None, mu=None, wb
                   fmt="mxfp4", Y=None, stream=None):
     """Y = Xq Wq^T + T L2^T + mu wbar^T (fp16 [M][N]) with the down-projection T (fp16
     [M][r]) already computed.  fmt 'mxfp4' (W4A4) or 'lm2' (W2A4)."""
+    if stream is not None:
+        return _on(stream, w4a4_linear_t, xcodes, xscales, wcodes, wscales, T, L2, mu, wbar, fmt, Y)
     torch = _torch()
     f, M, K, N = _linear_operands(xcodes, xscales, wcodes, wscales, fmt)
     r = 0
@@ -593,12 +593,10 @@ def w4a4_linear_t(xcodes, xscales, wcodes, wscales, T=None, L2=None, mu=None, wb
         r = T.shape[1]
         _check(T, "T", torch.float16, (M, r))
         _check(L2, "L2", torch.float16, (N, r))
-    Y, made_y = _linear_tail(M, N, mu, wbar, Y, xcodes.device)
-    if made_y:
-        _on_stream(stream, Y)
+    Y = _linear_tail(M, N, mu, wbar, Y, xcodes.device)
     s = load().kq_w4a4_linear_t(f, _ptr(xcodes), _ptr(xscales), M, K, _ptr(wcodes), _ptr(wscales), N,
                                 _ptr(T), _ptr(L2 if r else None), r, _ptr(mu), _ptr(wbar), _ptr(Y),
-                                _stream(stream))
+                                _stream())
     if s != KQ_OK:
         raise KQError(s, "kq_w4a4_linear_t")
     return Y
@@ -634,18 +632,10 @@ def _same(t, name, dtype, shape, index):
     raise ValueError(f"{name} is on {t.device}, the first tensor on GPU {index}")
 
 
-def _call(torch, name, index, stream, made, args):
-    """One library call on `stream` (default: the current stream of the tensors' GPU, which is
-    made the current device for the call if it is not)."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        if stream.device.index != index:
-            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on GPU {index}")
-        raw = stream.cuda_stream
-        if stream != torch.cuda.current_stream(index):
-            for t in made:
-                t.record_stream(stream)
+def _call(torch, name, index, args):
+    """One library call on the current stream of the tensors' GPU, which is made the current device
+    for the call if it is not."""
+    raw = torch._C._cuda_getCurrentRawStream(index)
     fn = getattr(_LIB or load(), name)
     if torch._C._cuda_getDevice() == index:
         s = fn(*args, raw)
@@ -656,12 +646,19 @@ def _call(torch, name, index, stream, made, args):
         raise KQError(s, name)
 
 
+def _on_fp8(stream, first, f, *args, **kw):
+    """_on for a call whose first tensor is `first`: its GPU must be the stream's."""
+    if isinstance(first, _torch().Tensor) and first.is_cuda and stream.device.index != first.get_device():
+        raise ValueError(f"{f.__name__}: the stream is on {stream.device}, the tensors on GPU {first.get_device()}")
+    return _on(stream, f, first, *args, **kw)
+
+
 def fp8_scale_cols(K):
     """Scale bytes of a row of K values: one per 128, padded to a multiple of four."""
     return (K + 511) // 512 * 4
 
 
-def _fp8_out(torch, rows, K, codes, scales, index, made, like=None):
+def _fp8_out(torch, rows, K, codes, scales, index, like=None):
     """codes and scales (made here where not given) and their addresses; like: a checked tensor of
     codes' shape.  torch makes a tensor in 1.2 us like another, 1.3 from shape and strides, 1.7 from
     a shape alone."""
@@ -670,14 +667,12 @@ def _fp8_out(torch, rows, K, codes, scales, index, made, like=None):
             codes = torch.empty_strided((rows, K), (K, 1), dtype=torch.float8_e4m3fn, device=index)
         else:
             codes = torch.empty_like(like, dtype=torch.float8_e4m3fn)
-        made.append(codes)
         c = codes.data_ptr()
     else:
         c = _same(codes, "codes", torch.float8_e4m3fn, (rows, K), index)
     cols = (K + 511) // 512 * 4
     if scales is None:
         scales = torch.empty_strided((rows, cols), (cols, 1), dtype=torch.uint8, device=index)
-        made.append(scales)
         return codes, scales, c, scales.data_ptr()
     return codes, scales, c, _same(scales, "scales", torch.uint8, (rows, cols), index)
 
@@ -686,13 +681,15 @@ def quantize_fp8(X, codes=None, scales=None, stream=None):
     """E4M3 codes (float8_e4m3fn [M][K]) and E8M0 scale bytes (uint8 [M][fp8_scale_cols(K)],
     one per 128 values) of X (fp16 or bf16 [M][K], K a multiple of 16).  Also for weights
     [N][K], offline."""
+    if stream is not None:
+        return _on_fp8(stream, X, quantize_fp8, codes, scales)
     torch = _torch()
     shape = M, K = _matrix(X, "X")
-    dtype, index, made = X.dtype, X.get_device(), []
+    dtype, index = X.dtype, X.get_device()
     dt = _dtype16(torch, dtype, "X")
     x = _same(X, "X", dtype, shape, index)
-    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, index, made, X)
-    _call(torch, "kq_quantize_fp8", index, stream, made, (dt, x, M, K, c, s))
+    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, index, X)
+    _call(torch, "kq_quantize_fp8", index, (dt, x, M, K, c, s))
     return codes, scales
 
 
@@ -701,9 +698,11 @@ def rmsnorm_quantize_fp8(X, gamma, eps=1e-6, residual=None, codes=None, scales=N
     X, residual fp16 or bf16 [M][K], gamma [K] of the same dtype, K <= 16384.  Returns (codes,
     scales, h rounded to the dtype); the last is None without a residual.  residual_out may be
     residual itself (updated in place)."""
+    if stream is not None:
+        return _on_fp8(stream, X, rmsnorm_quantize_fp8, gamma, eps, residual, codes, scales, residual_out)
     torch = _torch()
     shape = M, K = _matrix(X, "X")
-    dtype, index, made = X.dtype, X.get_device(), []
+    dtype, index = X.dtype, X.get_device()
     dt = _dtype16(torch, dtype, "X")
     x = _same(X, "X", dtype, shape, index)
     g = _same(gamma, "gamma", dtype, (K,), index)
@@ -714,12 +713,11 @@ def rmsnorm_quantize_fp8(X, gamma, eps=1e-6, residual=None, codes=None, scales=N
         r = _same(residual, "residual", dtype, shape, index)
         if residual_out is None:
             residual_out = torch.empty_like(X)
-            made.append(residual_out)
             o = residual_out.data_ptr()
         else:
             o = _same(residual_out, "residual_out", dtype, shape, index)
-    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, index, made, X)
-    _call(torch, "kq_rmsnorm_quantize_fp8", index, stream, made, (dt, x, r, g, eps, M, K, c, s, o))
+    codes, scales, c, s = _fp8_out(torch, M, K, codes, scales, index, X)
+    _call(torch, "kq_rmsnorm_quantize_fp8", index, (dt, x, r, g, eps, M, K, c, s, o))
     return codes, scales, residual_out
 
 
@@ -740,20 +738,20 @@ def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, 
     product exact and added in float32, as up to 16 tokens always; else calls of more tokens take
     the 8-bit matrix instructions, which cut products off at 2^-13 of the largest of each eight and
     are up to twice as fast (KQ_FP8_PRECISE in kq.h)."""
+    if stream is not None:
+        return _on_fp8(stream, xcodes, fp8_linear, xscales, wcodes, wscales, bias, dtype, Y, precise=precise)
     torch = _torch()
     M, N, K, index, x, xs, w, ws = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if dtype is None:
         dtype = Y.dtype if Y is not None else bias.dtype if bias is not None else torch.float16
     dt = _dtype16(torch, dtype, "dtype")
-    made = []
     b = None if bias is None else _same(bias, "bias", dtype, (N,), index)
     if Y is None:
         Y = torch.empty_strided((M, N), (N, 1), dtype=dtype, device=index)
-        made.append(Y)
         y = Y.data_ptr()
     else:
         y = _same(Y, "Y", dtype, (M, N), index)
-    _call(torch, "kq_fp8_linear", index, stream, made, (dt | _PRECISE if precise else dt, x, xs, M, K, w, ws, N, b, y))
+    _call(torch, "kq_fp8_linear", index, (dt | _PRECISE if precise else dt, x, xs, M, K, w, ws, N, b, y))
     return Y
 
 
@@ -769,6 +767,9 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
     'gelu_tanh'.  The result feeds fp8_linear with the down-projection's weights.  workspace: a
     uint8 device tensor of fp8_gated_linear_workspace_bytes(M, F, K) bytes (256-byte aligned); by
     default one is taken from torch's allocator.  precise: as in fp8_linear."""
+    if stream is not None:
+        return _on_fp8(stream, xcodes, fp8_gated_linear, xscales, wcodes, wscales, act, codes, scales, workspace,
+                       precise=precise)
     torch = _torch()
     if act not in _ACT:
         raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
@@ -776,8 +777,7 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
     if N % 2:
         raise ValueError("wcodes must hold as many gate rows as up rows")
     F = N // 2
-    made = []
-    codes, scales, c, s = _fp8_out(torch, M, F, codes, scales, index, made)
+    codes, scales, c, s = _fp8_out(torch, M, F, codes, scales, index)
     wk = nb = 0
     if workspace is not None:
         wk, nb = _same(workspace, "workspace", torch.uint8, workspace.shape, index), workspace.numel()
@@ -785,7 +785,6 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
         nb = fp8_gated_linear_workspace_bytes(M, F, K)
         if nb:
             workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
-            made.append(workspace)
             wk = workspace.data_ptr()
-    _call(torch, "kq_fp8_gated_linear", index, stream, made, (_ACT[act] | _PRECISE if precise else _ACT[act], x, xs, M, K, w, ws, F, c, s, wk or None, nb))
+    _call(torch, "kq_fp8_gated_linear", index, (_ACT[act] | _PRECISE if precise else _ACT[act], x, xs, M, K, w, ws, F, c, s, wk or None, nb))
     return codes, scales
