@@ -360,9 +360,8 @@ kq_status kq_quantize_fp8(int32_t dtype, const void* X, int64_t M, int64_t K, ui
  *   codes, scales of y = h / sqrt(mean_k h^2 + eps) * gamma.
  * y is formed from the float32 h, not from its rounded copy.  All 16-bit arrays have the one
  * dtype: X, residual, residual_out [M][K], gamma [K].  residual_out may be residual itself.
- * K <= 16384 (a row stays in registers); eps finite and >= 0 (else KQ_ERR_VALUE).  Squares
- * are float32: a bf16 row with values beyond about 1e18 overflows their sum and gives zeros (and
- * one below 1e-18 with eps = 0 underflows it and gives NaN). */
+ * K <= 16384 (a row stays in registers); eps finite and >= 0 (else KQ_ERR_VALUE).  Rows
+ * of any finite size are normalized, to float32's ends; a row of zeros with eps = 0 gives NaN. */
 kq_status kq_rmsnorm_quantize_fp8(int32_t dtype, const void* X, const void* residual, const void* gamma, float eps,
                                   int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, void* residual_out,
                                   hipStream_t stream);

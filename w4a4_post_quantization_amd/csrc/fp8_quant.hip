@@ -86,15 +86,28 @@ hipError_t launch_f8_quantize_f32(const float* X, int64_t M, int64_t K, uint8_t*
 // 1 / sqrt(x) from the hardware's estimate (good to a step) by one Newton step in float64: with the
 // sum joined in float64 too, the factor of a whole row is off by its own rounding alone.
 __device__ __forceinline__ float f8_rsqrt(double x) {
-  const float r0 = __builtin_amdgcn_rsqf((float)x);
-  if (!(r0 > 0.0f && r0 < INFINITY)) return r0;                // of infinity, zero or NaN
-  const double r = (double)r0;
+  const double r = (double)__builtin_amdgcn_rsqf((float)x);
   return (float)fma(0.5 * r, fma(-x * r, r, 1.0), r);
+}
+
+// The sum over a workgroup's threads, the same bits in each.
+template <int NT>
+__device__ __forceinline__ double f8_block_sum(double sum, double* part, int t) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if ((t & 63) == 0) part[t >> 6] = sum;
+  __syncthreads();
+  sum = part[0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) sum += part[w];
+  return sum;
 }
 
 // One row per NT threads at a time; thread t holds columns 8 (v NT + t) .. + 7 for v < VPT in
 // float32.  h is normalized as summed in float32; only the stored residual is rounded to 16 bits.
-// A lane's squares are a float32 chain, the lanes' sums are joined in float64.
+// A lane's squares are a float32 chain, the lanes' sums are joined in float64.  Rows whose squares may
+// have left float32's range (bf16 reaches 3e38) take them again in float64, and their factor, which
+// may itself be out of float32's range, in two parts.
 template <bool BF16, bool RES, int NT, int VPT>
 __global__ __launch_bounds__(NT) void f8_rmsnorm_kernel(const uint8_t* __restrict__ X,
                                                         const uint8_t* residual,
@@ -124,15 +137,25 @@ __global__ __launch_bounds__(NT) void f8_rmsnorm_kernel(const uint8_t* __restric
 #pragma unroll
       for (int i = 0; i < 8; ++i) sq = fmaf(h[v][i], h[v][i], sq);
     }
-    double sum = (double)sq;
+    double mean = f8_block_sum<NT>((double)sq, part, t) / (double)K + (double)eps;
+    float rinv;
+    int ex = 0;                                                // h 2^ex rinv is the normalized row
+    // squares below 2^-126 count for nothing beside 2^-100; NaN comes here too
+    if (__builtin_expect(mean >= 0x1p-100 && mean <= 0x1p100, 1)) {
+      rinv = f8_rsqrt(mean);
+    } else {
+      double sq64 = 0.0;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if (lane == 0) part[t >> 6] = sum;
-    __syncthreads();
-    sum = part[0];
+      for (int v = 0; v < VPT; ++v)
 #pragma unroll
-    for (int w = 1; w < NT / 64; ++w) sum += part[w];
-    const float rinv = f8_rsqrt(sum / (double)K + (double)eps);
+        for (int i = 0; i < 8; ++i) sq64 = fma((double)h[v][i], (double)h[v][i], sq64);
+      __syncthreads();                                         // part has been read
+      mean = f8_block_sum<NT>(sq64, part, t) / (double)K + (double)eps;
+      const double r = 1.0 / sqrt(mean);
+      rinv = (float)r;
+      if (r > 0.0 && r < INFINITY) rinv = (float)frexp(r, &ex);
+    }
+    ex = __builtin_amdgcn_readfirstlane(ex);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int col = 8 * (v * NT + t);
@@ -150,7 +173,13 @@ __global__ __launch_bounds__(NT) void f8_rmsnorm_kernel(const uint8_t* __restric
       unpack8_16<BF16>(gw, g);
       // lanes past K: 0 times a possibly infinite rinv is not to reach the group's maximum
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = col < K ? h[v][i] * rinv * g[i] : 0.0f;
+      for (int i = 0; i < 8; ++i) y[i] = h[v][i];
+      if (__builtin_expect(ex != 0, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = ldexpf(y[i], ex);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = col < K ? y[i] * rinv * g[i] : 0.0f;
       f8_store_512(y, row, col, K, lane, codes, scales);
     }
     __syncthreads();                                           // part is read before the next row's
