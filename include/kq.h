@@ -379,7 +379,8 @@ kq_status kq_fp8_linear(int32_t dtype, const uint8_t* xcodes, const uint8_t* xsc
  * and the product stay in float32; the result is rounded once, to E4M3.  kq_fp8_linear with
  * the down-projection's weights takes codes and scales as they are.  workspace: at least
  * kq_fp8_gated_linear_workspace_bytes(M, F, K) bytes (0: none needed), which holds the float32
- * outputs of a few tokens.  Calls that share a workspace must not overlap, replays of captured
+ * outputs of a few tokens (up to 32, and up to 64 as far as the device's compute units hold the workgroups:
+ * ask on the device that runs the call).  Calls that share a workspace must not overlap, replays of captured
  * graphs that hold it included. */
 size_t kq_fp8_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K);
 kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,

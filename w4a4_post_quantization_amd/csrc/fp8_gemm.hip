@@ -237,11 +237,17 @@ static hipError_t rows_go(const uint8_t* xcodes, const uint8_t* xscales, int64_t
 // against 11.1 in tiles, 128 tokens 13.1 against 12.3.
 constexpr int64_t ROWS_LINEAR = 64;
 
-// The gated pair, where a second launch and the float32 outputs between them count too: to 32 tokens, and to 48
-// and 64 while its workgroups of 16 columns all run at once, three and two on each of 256 compute units.
-// Measured (us) in rows and in tiles, K = 4096: 40 tokens, F = 2816 12.7 and 18.6, 11008 23.3 and 25.9, 14336 36.7
-// and 33.0; 64 tokens, 2816 13.4 and 19.0, 8192 17.2 and 19.3, 11008 32.2 and 26.5; 32 tokens, 14336 33.2 and 33.0.
-static bool gated_rows(int64_t M, int64_t F) { return M <= 32 || (M <= 48 && F <= 12288) || (M <= 64 && F <= 8192); }
+// Tokens the rows kernel takes with this many workgroups of 32 weight rows: to 32, and to 48 and 64 while the
+// workgroups all run at once, three and two on a compute unit.
+static bool rows_fit(int64_t M, int64_t wgs) {
+  const int64_t cus = device_cu_count();
+  return M <= 32 || (M <= 48 && wgs <= 3 * cus) || (M <= 64 && wgs <= 2 * cus);
+}
+
+// The gated pair, whose second launch and float32 outputs between them count too.  Measured (us) in rows and in
+// tiles, 256 compute units, K = 4096: 40 tokens, F = 2816 12.7 and 18.6, 11008 23.3 and 25.9, 14336 36.7 and 33.0; 64
+// tokens, 2816 13.4 and 19.0, 8192 17.2 and 19.3, 11008 32.2 and 26.5; 32 tokens, 14336 33.2 and 33.0.
+static bool gated_rows(int64_t M, int64_t F) { return rows_fit(M, F / 16); }
 
 template <int ACT, bool BF16>
 static hipError_t rows_launch(bool precise, const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
