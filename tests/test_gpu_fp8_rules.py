@@ -51,3 +51,18 @@ def test_gated_to_each_side(kq, M):
     # group's largest), and 1e-5 for the float32 activation
     for v in h:
         assert bool(((v - exact).abs() <= torch.maximum(exact.abs() * 2.0 ** -4, top * 2.0 ** -17) + 1e-5 * exact.abs()).all())
+
+
+@pytest.mark.parametrize("M", [32, 33, 48, 49, 64])
+@pytest.mark.parametrize("K", [144, 656])
+@pytest.mark.parametrize("precise", [False, True])
+def test_linear_to_each_side(kq, M, K, precise):
+    """Every bit, with as many workgroups of 32 weight rows as the rule allows and one more."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    N = 32 * (3 if M <= 48 else 2) * cus
+    x, xs, xv = _whole(M, K, M)
+    w, ws, wv = _whole(N + 16, K, N)
+    ref = (xv @ wv.t()).to(torch.float16)                    # sums exact in float32
+    for n in (N, N + 16):
+        y = kq.fp8_linear(x, xs, w[:n], ws[:n], precise=precise)
+        assert torch.equal(y, ref[:, :n])

@@ -233,12 +233,12 @@ static hipError_t rows_go(const uint8_t* xcodes, const uint8_t* xscales, int64_t
   return hipGetLastError();
 }
 
-// Tokens the rows kernel takes; above, tiles.  Measured (us): linear 6144 x 4096, 64 tokens 9.0
-// against 11.1 in tiles, 128 tokens 13.1 against 12.3.
-constexpr int64_t ROWS_LINEAR = 64;
-
 // Tokens the rows kernel takes with this many workgroups of 32 weight rows: to 32, and to 48 and 64 while the
-// workgroups all run at once, three and two on a compute unit.
+// workgroups all run at once, three and two on a compute unit; else, and above, tiles.  The linear, measured (us)
+// in rows and in tiles on 256 compute units: 4096 k, 64 tokens, 6144 rows 9.0 and 11.1, 16384 14.7 and 14.0, 18432 23.8
+// and 17.3, 28672 37.0 and 34.2; 40 tokens, 16384 14.4 and 13.5, 22016 21.3 and 23.7, 24576 26.9 and 30.6, 28672 35.1
+// and 33.4; 32 tokens, 22016 22.7 and 24.3, 57344 52.5 and 58.1; 8192 k, 64 tokens, 18432 59.7 and 52.7, 40 tokens, 24576
+// 47.4 and 56.1, 28672 60.7 and 56.0; 128 tokens of 6144 rows, 4096 k, 13.1 and 12.3.
 static bool rows_fit(int64_t M, int64_t wgs) {
   const int64_t cus = device_cu_count();
   return M <= 32 || (M <= 48 && wgs <= 3 * cus) || (M <= 64 && wgs <= 2 * cus);
@@ -994,7 +994,7 @@ template <bool BF16, bool WIDE>
 static hipError_t linear_launch(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, int64_t K,
                                 const uint8_t* wcodes, const uint8_t* wscales, int64_t N, const uint16_t* bias,
                                 uint8_t* Y, hipStream_t s) {
-  if (M <= ROWS_LINEAR) return rows_launch<-1, BF16>(WIDE, xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
+  if (rows_fit(M, (N + 31) / 32)) return rows_launch<-1, BF16>(WIDE, xcodes, xscales, M, K, wcodes, wscales, N, bias, Y, s);
   const int64_t cus = device_cu_count();
   auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
 #define KQ_TILE(...)                                                                                                \
