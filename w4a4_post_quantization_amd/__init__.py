@@ -696,8 +696,10 @@ def quantize_fp8(X, codes=None, scales=None, stream=None):
 def rmsnorm_quantize_fp8(X, gamma, eps=1e-6, residual=None, codes=None, scales=None, residual_out=None, stream=None):
     """h = X + residual; codes and scales (as quantize_fp8) of h / sqrt(mean h^2 + eps) * gamma.
     X, residual fp16 or bf16 [M][K], gamma [K] of the same dtype, K <= 16384.  Returns (codes,
-    scales, h rounded to the dtype); the last is None without a residual.  residual_out may be
-    residual itself (updated in place)."""
+    scales, h rounded to the dtype); the last is None without a residual, and residual_out (where h
+    is to go) is then refused.  residual_out may be residual itself (updated in place)."""
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out is given without a residual: h is X itself")
     if stream is not None:
         return _on_fp8(stream, X, rmsnorm_quantize_fp8, gamma, eps, residual, codes, scales, residual_out)
     torch = _torch()
@@ -707,9 +709,7 @@ def rmsnorm_quantize_fp8(X, gamma, eps=1e-6, residual=None, codes=None, scales=N
     x = _same(X, "X", dtype, shape, index)
     g = _same(gamma, "gamma", dtype, (K,), index)
     r = o = None
-    if residual is None:
-        residual_out = None
-    else:
+    if residual is not None:
         r = _same(residual, "residual", dtype, shape, index)
         if residual_out is None:
             residual_out = torch.empty_like(X)
