@@ -743,7 +743,8 @@ def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, 
     torch = _torch()
     M, N, K, index, x, xs, w, ws = _fp8_operands(torch, xcodes, xscales, wcodes, wscales)
     if dtype is None:
-        dtype = Y.dtype if Y is not None else bias.dtype if bias is not None else torch.float16
+        like = Y if Y is not None else bias
+        dtype = torch.float16 if like is None else getattr(like, "dtype", type(like))
     dt = _dtype16(torch, dtype, "dtype")
     b = None if bias is None else _same(bias, "bias", dtype, (N,), index)
     if Y is None:
@@ -780,7 +781,8 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
     codes, scales, c, s = _fp8_out(torch, M, F, codes, scales, index)
     wk = nb = 0
     if workspace is not None:
-        wk, nb = _same(workspace, "workspace", torch.uint8, workspace.shape, index), workspace.numel()
+        wk = _same(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), index)
+        nb = workspace.numel()
     else:
         nb = fp8_gated_linear_workspace_bytes(M, F, K)
         if nb:
