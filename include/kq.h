@@ -337,7 +337,7 @@ enum { KQ_DT_F16 = 0, KQ_DT_BF16 = 1 };
 enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1, KQ_ACT_GELU_TANH = 2 };
 /* Or'ed into the dtype of kq_fp8_linear or the act of kq_fp8_gated_linear: every product of two codes
  * exact and added in float32, as calls of up to 16 tokens always do, and a gated call's activation by
- * the correctly rounded quotient and exponential.  Without it, calls of more tokens use the 8-bit matrix
+ * the library's exponential and a rounded quotient.  Without it, calls of more tokens use the 8-bit matrix
  * instructions, which cut off (towards zero) each of eight consecutive products at 2^(E - 13), E the largest
  * of the eight's sums of two exponents (a subnormal code's exponent is that of the smallest normal one).
  * So a sum is off by at most 7 * 2^(E - 13) added over the eights; relative to the sum itself there is no

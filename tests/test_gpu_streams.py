@@ -121,3 +121,35 @@ def test_current_stream_stays(kq):
             kq.quantize_fp8(x[:, :40].contiguous(), stream=side)
         assert torch.cuda.current_stream() == mine
     torch.cuda.synchronize()
+
+
+def test_captured_on_a_forked_stream(kq):
+    """A graph whose capture forks to another stream for a gated pair (a workspace and two launches) and a
+    linear, replayed on new inputs with eager work and waits between."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    gu = kq.quantize_fp8(torch.randn(512, 512, device="cuda", generator=g).to(torch.bfloat16))
+    dn = kq.quantize_fp8(torch.randn(512, 256, device="cuda", generator=g).to(torch.bfloat16))
+    x = torch.randn(9, 512, device="cuda", generator=g).to(torch.bfloat16)
+
+    def block(stream):
+        codes, scales = kq.quantize_fp8(x)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        codes, scales = kq.fp8_gated_linear(codes, scales, *gu, stream=stream)
+        y = kq.fp8_linear(codes, scales, *dn, dtype=torch.bfloat16, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        return y + 1
+    side = torch.cuda.Stream()
+    block(None), block(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = block(side)
+    for k in range(3):
+        x.copy_(torch.randn(9, 512, device="cuda", generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, block(None)), k
+        assert torch.equal(y, block(side)), k
+        torch.cuda.synchronize()

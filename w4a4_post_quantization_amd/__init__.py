@@ -734,7 +734,8 @@ def _fp8_operands(torch, xcodes, xscales, wcodes, wscales):
 def fp8_linear(xcodes, xscales, wcodes, wscales, bias=None, dtype=None, Y=None, stream=None, precise=False):
     """Y = Xq Wq^T (+ bias), fp16 or bf16 [M][N], float32 accumulation.  xcodes [M][K] and
     wcodes [N][K] float8_e4m3fn with their scale bytes (quantize_fp8); N a multiple of 16; bias
-    [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16).  precise: every
+    [N] of Y's dtype.  dtype: Y's (default: Y's own, the bias's, or float16, where sums past 65504
+    turn infinite).  precise: every
     product exact and added in float32, as up to 16 tokens always; else calls of more tokens take
     the 8-bit matrix instructions, which cut products off at 2^-13 of the largest of each eight and
     are up to twice as fast (KQ_FP8_PRECISE in kq.h)."""
