@@ -343,7 +343,7 @@ enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1, KQ_ACT_GELU_TANH = 2 };
  * So a sum is off by at most 7 * 2^(E - 13) added over the eights; relative to the sum itself there is no
  * bound (p, -p and a much smaller q in one eight lose q).  Norm of the errors over norm of the sums, measured:
  * 1.0e-5 to 1.6e-5 on Gaussian values, 2e-5 to 7e-5 with 12 channels of 20 times the size (K = 16 to
- * 11008), 1e-8 to 2e-7 with the flag.  It costs 1 to 8% up to 32 tokens and, for long prompts, as much
+ * 11008), 1e-8 to 2e-7 with the flag.  It costs 1 to 10% up to 32 tokens and, for long prompts, as much
  * time again. */
 enum { KQ_FP8_PRECISE = 0x100 };
 
