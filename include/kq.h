@@ -387,6 +387,67 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
                               const uint8_t* wcodes, const uint8_t* wscales, int64_t F, uint8_t* codes,
                               uint8_t* scales, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- Attention of the 8-bit path: between the projection of queries, keys and values and the output
+ * projection.  16-bit types are fp16 or bf16 (KQ_DT_*), one in all 16-bit arrays of a call.  Hq query heads
+ * share Hkv key heads, Hq / Hkv at a time (head h reads key head h Hkv / Hq); D values a head, a multiple of
+ * 8, 8 to 128.
+ *
+ *   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j - max),  over the keys j that the query sees;
+ *
+ * a query that sees no key gets zeros, and what is at keys that it does not see (NaN and infinities
+ * included) does not reach it.  Scores, maxima and sums are float32; the weights are rounded to the
+ * 16-bit type for the product with the values (in an 8-bit cache: to bf16, for fp16 outputs to the sum of
+ * two bf16 numbers).  They are divided by their sum at the end, so values beyond 10^30 may overflow.  The
+ * order of additions is fixed for one device: equal inputs of equal shape give equal bits.
+ *
+ * Outputs: O [rows][Hq][D] in the 16-bit type, or, where codes and scales are given instead (O NULL; D = 128
+ * only), E4M3 codes [rows][Hq 128] with one E8M0 byte for each head, [rows][kq_fp8_scale_cols(Hq 128)],
+ * rounded once from float32: what kq_fp8_linear takes.  Contiguous.  Pointers 16-byte aligned, integers,
+ * table and scales 4.  Entries of device arrays (cu, table, lengths) are not checked on the host; kernels hold
+ * them to what the arrays can hold, as each call says, so none leads out of them. */
+
+/* Packed sequences: sequence s has queries cu_q[s] .. cu_q[s + 1] - 1 of Q and keys cu_k[s] .. cu_k[s + 1] - 1 of
+ * K and V (cu_q, cu_k: int32 [B + 1], ascending, device memory; both NULL: one sequence of T queries and Tk keys,
+ * B = 1).  causal: query i of a sequence sees the keys j <= i + Lk - Lq, so the last query sees all.  Rows of Q
+ * outside all sequences get no output: theirs is left as it was.  Entries of cu are held to 0 .. T (Tk)
+ * and to their order.
+ * Q, K, V: element (token, head, d) at token * token stride + head * head stride + d, strides in elements,
+ * multiples of 8; token strides D to 2^21, head strides 0 to 2^40.  Views of one projection's output
+ * [T][(Hq + 2 Hkv) D] are the usual case.  T, Tk <= 2^30, T Hq <= 2^29, B Hq <= 2^22.  scale finite, above 0. */
+kq_status kq_attention(int32_t dtype, const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token,
+                       int64_t k_head, const void* V, int64_t v_token, int64_t v_head, const int32_t* cu_q,
+                       const int32_t* cu_k, int64_t B, int64_t T, int64_t Tk, int32_t Hq, int32_t Hkv, int32_t D,
+                       int32_t causal, float scale, void* O, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* A cache of keys and values in pages of `page` tokens (a multiple of 16, to 65536): kcache, vcache
+ * [pages][Hkv][page][D], in the 16-bit type; or, with kscales and vscales (both or neither; [pages][Hkv][page]),
+ * E4M3 codes with one E8M0 byte for each token and head, as kq_quantize_fp8 would give for a row of D
+ * values (D a multiple of 16 then).  table int32 [B][width] names each sequence's pages in order, lengths
+ * int32 [B] its tokens; lengths are held to 0 .. width * page, and entries of the table outside 0 .. pages - 1
+ * are pages that are not there: their tokens are neither written nor seen.  Entries behind a sequence's last
+ * page are not read.  A page may be in several sequences' tables (a common beginning); one that receives
+ * tokens must be in one.  B <= 2^20, width * page <= 2^30, B width page <= 2^37, pages < 2^31. */
+
+/* Writes new tokens' keys and values: lengths already count them.  Sequence s's new tokens are rows cu[s] ..
+ * cu[s + 1] - 1 of K and V (int32 [B + 1], ascending; NULL: one token each, T = B), the last of them at
+ * position lengths[s] - 1.  K, V: as kq_attention, head strides to 2^40.  Tokens whose position is
+ * outside the table, and rows outside all sequences, are not written.  T <= 2^30. */
+kq_status kq_cache_append(int32_t dtype, const void* K, int64_t k_token, int64_t k_head, const void* V, int64_t v_token,
+                          int64_t v_head, const int32_t* cu, int64_t B, int64_t T, int32_t Hkv, int32_t D,
+                          const int32_t* table, int64_t width, const int32_t* lengths, void* kcache, void* vcache,
+                          uint8_t* kscales, uint8_t* vscales, int64_t pages, int32_t page, hipStream_t stream);
+
+/* One new token a sequence: query b of Q [B][Hq][D] (strides as above, both D to 2^21) sees the lengths[b]
+ * tokens of its sequence.  workspace: at least kq_paged_attention_workspace_bytes bytes, 256-byte aligned (it
+ * depends on the device's compute units: ask on the device that runs the call).  Calls that share a workspace
+ * must not overlap, replays of captured graphs that hold it included.  B Hq <= 2^23.  scale finite, above 0. */
+size_t kq_paged_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t width, int32_t page);
+kq_status kq_paged_attention(int32_t dtype, const void* Q, int64_t q_seq, int64_t q_head, const void* kcache,
+                             const void* vcache, const uint8_t* kscales, const uint8_t* vscales, int64_t pages,
+                             int32_t page, const int32_t* table, int64_t width, const int32_t* lengths, int64_t B,
+                             int32_t Hq, int32_t Hkv, int32_t D, float scale, void* O, uint8_t* codes, uint8_t* scales,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

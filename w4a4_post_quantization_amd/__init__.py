@@ -19,6 +19,14 @@ library is missing: there is no fallback.
     codes, scales = kq.fp8_gated_linear(codes, scales, gate_up_codes, gate_up_scales, act="silu")
     X = kq.fp8_linear(codes, scales, down_codes, down_scales, dtype=X.dtype)
 
+    # and its attention: prompts (packed sequences), then one token at a time from a paged cache
+    qkv = kq.fp8_linear(codes, scales, qkv_codes, qkv_scales, dtype=X.dtype).view(T, Hq + 2 * Hkv, 128)
+    Q, K, V = qkv.split((Hq, Hkv, Hkv), dim=1)
+    kq.cache_append(K, V, kcache, vcache, table, lengths, cu)
+    codes, scales = kq.attention(Q, K, V, cu, fp8=True)                       # a prompt
+    codes, scales = kq.paged_attention(Q, kcache, vcache, table, lengths, fp8=True)     # later tokens
+    X = kq.fp8_linear(codes, scales, out_codes, out_scales, dtype=X.dtype)
+
 With ``stream`` a call runs with that stream as torch's current one: outputs and workspaces that
 the binding allocates itself are then that stream's memory, so no work still pending on another
 stream writes into them.  Outputs are also marked as used on the stream that was current before
@@ -35,6 +43,7 @@ __all__ = ["mfma_fp4_probe", "load", "lib_path", "abi_version", "status_str", "l
            "lowrank_down", "lowrank_down_workspace_bytes", "transform_quantize_lowrank",
            "svd_lowrank", "svd_lowrank_workspace_bytes", "fp8_scale_cols", "quantize_fp8", "rmsnorm_quantize_fp8",
            "fp8_linear", "fp8_gated_linear", "fp8_gated_linear_workspace_bytes",
+           "attention", "cache_append", "paged_attention", "paged_attention_workspace_bytes",
            "KQError"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -124,6 +133,18 @@ def load():
     lib.kq_fp8_gated_linear_workspace_bytes.argtypes = [i64, i64, i64]
     lib.kq_fp8_gated_linear.restype = i32
     lib.kq_fp8_gated_linear.argtypes = [i32, vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, sz, vp]
+    f32 = ctypes.c_float
+    lib.kq_attention.restype = i32
+    lib.kq_attention.argtypes = [i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, i32, i32, i32, i32,
+                                 f32, vp, vp, vp, vp]
+    lib.kq_cache_append.restype = i32
+    lib.kq_cache_append.argtypes = [i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp,
+                                    i64, i32, vp]
+    lib.kq_paged_attention_workspace_bytes.restype = sz
+    lib.kq_paged_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i32]
+    lib.kq_paged_attention.restype = i32
+    lib.kq_paged_attention.argtypes = [i32, vp, i64, i64, vp, vp, vp, vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, f32,
+                                       vp, vp, vp, vp, sz, vp]
     _LIB = lib
     return lib
 
@@ -791,3 +812,179 @@ def fp8_gated_linear(xcodes, xscales, wcodes, wscales, act="silu", codes=None, s
             wk = workspace.data_ptr()
     _call(torch, "kq_fp8_gated_linear", index, (_ACT[act] | _PRECISE if precise else _ACT[act], x, xs, M, K, w, ws, F, c, s, wk or None, nb))
     return codes, scales
+
+
+# ------------------------------------------------------------------------- attention of the 8-bit path
+
+def _rows3(t, name, dtype, shape, index):
+    """t: heads' rows [tokens][heads][D] of the dtype on GPU `index`, values of a row next to each other;
+    its address, token stride and head stride."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0:
+            token, head, one = t.stride()
+            if one == 1 or shape[2] == 1:
+                # strides of axes of one element are arbitrary
+                return t.data_ptr(), token if shape[0] > 1 else shape[2], head if shape[1] > 1 else 0
+            raise ValueError(f"{name}'s values of a row must lie next to each other (stride 1, got {one})")
+    except AttributeError:
+        pass
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU (got {t.device})")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    raise ValueError(f"{name} is on {t.device}, the first tensor on GPU {index}")
+
+
+def _heads3(t, name):
+    if not isinstance(t, _torch().Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D torch.Tensor [tokens, heads, D]")
+    return t.shape
+
+
+def _ints(torch, t, name, shape, index):
+    return None if t is None else _same(t, name, torch.int32, shape, index)
+
+
+def _attn_out(torch, rows, H, D, dtype, fp8, O, codes, scales, index):
+    """Outputs of an attention (made here where not given) and their addresses."""
+    if fp8:
+        if O is not None:
+            raise ValueError("O is given with fp8: the outputs are codes and scales")
+        if D != 128:
+            raise ValueError(f"fp8 outputs need heads of 128 values (got {D}): quantize_fp8 takes the 16-bit ones")
+        codes, scales, c, s = _fp8_out(torch, rows, 128 * H, codes, scales, index)
+        return (codes, scales), None, c, s
+    if codes is not None or scales is not None:
+        raise ValueError("codes or scales are given without fp8: the output is O")
+    if O is None:
+        O = torch.empty_strided((rows, H, D), (H * D, D, 1), dtype=dtype, device=index)
+        return O, O.data_ptr(), None, None
+    return O, _same(O, "O", dtype, (rows, H, D), index), None, None
+
+
+def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False, O=None, codes=None, scales=None,
+              stream=None):
+    """Attention of packed sequences.  Q [T][Hq][D], K and V [Tk][Hkv][D], fp16 or bf16, Hq a multiple of Hkv (head h
+    reads key head h Hkv // Hq), D a multiple of 8 up to 128; any strides that are multiples of 8 (the values
+    of a row next to each other), so views of a projection's output serve.  cu_q, cu_k (int32 [B + 1]): where each
+    sequence's queries and keys begin and the last one's end; cu_k defaults to cu_q, and without either all is
+    one sequence.  causal: query i of Lq sees the keys j <= i + Lk - Lq of Lk.  scale (above 0) defaults to
+    D ** -0.5.  A query that sees no key gets zeros; rows outside all sequences are left as they were.  Returns O
+    [T][Hq][D] in the inputs' dtype, or with fp8 (D 128) codes [T][Hq * 128] and scales as quantize_fp8 gives them,
+    which fp8_linear takes."""
+    if stream is not None:
+        return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales)
+    torch = _torch()
+    shape = T, Hq, D = _heads3(Q, "Q")
+    Tk, Hkv, _ = _heads3(K, "K")
+    dtype, index = Q.dtype, Q.get_device()
+    dt = _dtype16(torch, dtype, "Q")
+    q = _rows3(Q, "Q", dtype, shape, index)
+    kv = (Tk, Hkv, D)
+    k, v = _rows3(K, "K", dtype, kv, index), _rows3(V, "V", dtype, kv, index)
+    B = 1
+    cq = ck = None
+    if cu_q is not None:
+        B = _vector(cu_q, "cu_q") - 1
+        cq = _ints(torch, cu_q, "cu_q", (B + 1,), index)
+        if cu_k is None and Tk != T:
+            raise ValueError(f"cu_k must be given where there are {Tk} keys for {T} queries")
+        ck = cq if cu_k is None else _ints(torch, cu_k, "cu_k", (B + 1,), index)
+    elif cu_k is not None:
+        raise ValueError("cu_k is given without cu_q")
+    out, o, c, s = _attn_out(torch, T, Hq, D, dtype, fp8, O, codes, scales, index)
+    _call(torch, "kq_attention", index, (dt, *q, *k, *v, cq, ck, B, T, Tk, Hq, Hkv, D, 1 if causal else 0,
+                                         D ** -0.5 if scale is None else scale, o, c, s))
+    return out
+
+
+def _vector(t, name):
+    if not isinstance(t, _torch().Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D torch.Tensor")
+    return t.shape[0]
+
+
+def _cache(torch, kcache, vcache, kscales, vscales, table, lengths, dtype, B, Hkv, D, index):
+    """Addresses and sizes of a paged cache: (k, v, ks, vs), pages, page, table, width, lengths."""
+    if not isinstance(kcache, torch.Tensor) or kcache.dim() != 4:
+        raise ValueError("kcache must be a 4-D torch.Tensor [pages, heads, page, D]")
+    pages, _, page, _ = kcache.shape
+    shape = (pages, Hkv, page, D)
+    ks = vs = None
+    if (kscales is None) != (vscales is None):
+        raise ValueError("kscales and vscales go together")
+    if kscales is not None:
+        dtype = torch.float8_e4m3fn
+        ks = _same(kscales, "kscales", torch.uint8, shape[:3], index)
+        vs = _same(vscales, "vscales", torch.uint8, shape[:3], index)
+    k, v = _same(kcache, "kcache", dtype, shape, index), _same(vcache, "vcache", dtype, shape, index)
+    width = _matrix(table, "table")[1]
+    return (k, v, ks, vs, pages, page, _same(table, "table", torch.int32, (B, width), index), width,
+            _same(lengths, "lengths", torch.int32, (B,), index))
+
+
+def cache_append(K, V, kcache, vcache, table, lengths, cu=None, kscales=None, vscales=None, stream=None):
+    """Writes new tokens' keys and values (K, V [T][Hkv][D], fp16 or bf16, strides as in attention) into the pages of
+    a cache, in place.  kcache, vcache [pages][Hkv][page][D] of the same dtype, page a multiple of 16; or, with
+    kscales and vscales (uint8 [pages][Hkv][page]), float8_e4m3fn, quantized as quantize_fp8 does, one scale for each
+    token and head.  table (int32 [B][width]) names each sequence's pages, lengths (int32 [B]) its tokens WITH the
+    new ones.  Sequence b's new tokens are rows cu[b] .. cu[b + 1] - 1 (int32 [B + 1]; default: one token each), the
+    last of them at position lengths[b] - 1.  Tokens that the table has no page for are not written.  Returns
+    kcache and vcache."""
+    if stream is not None:
+        return _on_fp8(stream, K, cache_append, V, kcache, vcache, table, lengths, cu, kscales, vscales)
+    torch = _torch()
+    shape = T, Hkv, D = _heads3(K, "K")
+    dtype, index = K.dtype, K.get_device()
+    dt = _dtype16(torch, dtype, "K")
+    k, v = _rows3(K, "K", dtype, shape, index), _rows3(V, "V", dtype, shape, index)
+    B = _vector(lengths, "lengths")
+    at = _ints(torch, cu, "cu", (B + 1,), index)
+    kc, vc, ks, vs, pages, page, tb, width, ln = _cache(torch, kcache, vcache, kscales, vscales, table, lengths, dtype, B,
+                                                        Hkv, D, index)
+    _call(torch, "kq_cache_append", index, (dt, *k, *v, at, B, T, Hkv, D, tb, width, ln, kc, vc, ks, vs, pages, page))
+    return kcache, vcache
+
+
+def paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page):
+    """Workspace bytes kq_paged_attention needs on the current device."""
+    return load().kq_paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page)
+
+
+def paged_attention(Q, kcache, vcache, table, lengths, kscales=None, vscales=None, scale=None, fp8=False, O=None, codes=None,
+                    scales=None, workspace=None, stream=None):
+    """Attention of one new token a sequence over a paged cache (cache_append has the cache's layout).  Q [B][Hq][D],
+    fp16 or bf16; sequence b's query sees its lengths[b] tokens.  Outputs as attention's, [B][Hq][D] or codes and
+    scales; a sequence of no tokens gets zeros.  workspace: a uint8 device tensor of
+    paged_attention_workspace_bytes bytes (256-byte aligned); by default one is taken from torch's allocator."""
+    if stream is not None:
+        return _on_fp8(stream, Q, paged_attention, kcache, vcache, table, lengths, kscales, vscales, scale, fp8, O, codes,
+                       scales, workspace)
+    torch = _torch()
+    shape = B, Hq, D = _heads3(Q, "Q")
+    dtype, index = Q.dtype, Q.get_device()
+    dt = _dtype16(torch, dtype, "Q")
+    q = _rows3(Q, "Q", dtype, shape, index)
+    Hkv = kcache.shape[1] if isinstance(kcache, torch.Tensor) and kcache.dim() == 4 else 0
+    kc, vc, ks, vs, pages, page, tb, width, ln = _cache(torch, kcache, vcache, kscales, vscales, table, lengths, dtype, B,
+                                                        Hkv, D, index)
+    out, o, c, s = _attn_out(torch, B, Hq, D, dtype, fp8, O, codes, scales, index)
+    if workspace is not None:
+        wk = _same(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), index)
+        nb = workspace.numel()
+    else:
+        if torch._C._cuda_getDevice() == index:
+            nb = paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page)
+        else:
+            with torch.cuda.device(index):
+                nb = paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page)
+        workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
+        wk = workspace.data_ptr()
+    _call(torch, "kq_paged_attention", index, (dt, *q, kc, vc, ks, vs, pages, page, tb, width, ln, B, Hq, Hkv, D,
+                                               D ** -0.5 if scale is None else scale, o, c, s, wk or None, nb))
+    return out

@@ -1,0 +1,582 @@
+// Attention of one new token a sequence over pages of cached keys and values, and the pages' filling.
+//
+// The cache's bytes bound it.  The batch's keys are cut into blocks of 128 (a key head's blocks after one
+// another, then the next head's, then the next sequence's) and the blocks are dealt to a fixed number of
+// workgroups in equal runs, whatever the lengths: a run may end inside a head's keys and begin inside
+// another's.  A run's whole heads go out at once; of a head that several runs share, each leaves its
+// unnormalized sum, maximum and sum of weights in the workspace (a run has two such at most), and a second
+// kernel joins them in a fixed order.
+//
+// Within a run, each of four wavefronts takes 32 keys of a block, through a ring of its own in LDS that is
+// filled two blocks ahead, so there is no barrier in the loop.  As for prompts everything is transposed:
+// S^T = K Q^T with the key head's queries as 16 columns, O^T += V^T P^T in the order of keys in which the
+// scores came out, V^T by transposing reads.  8-bit rows are widened exactly; their scales go to the scores
+// (keys) and to the weights (values).
+#include "kq_attn.hpp"
+#include "kq_launch.hpp"
+
+namespace kq {
+
+namespace {
+
+constexpr int NW = 4, BLOCK = 32 * NW;
+
+// Lengths are held to what the table's rows can hold.
+__device__ __forceinline__ int held(const Pages& c, int32_t len) {
+  return (int)min((int64_t)max(len, 0), (int64_t)c.width * c.page);
+}
+__device__ __forceinline__ int blocks_in(int len) { return (int)(((int64_t)len + BLOCK - 1) / BLOCK); }
+
+// An entry at an index that the whole wavefront shares, as a scalar load: a vector load would have to be
+// waited for together with the rings'.
+__device__ __forceinline__ int32_t scalar_at(const int32_t* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) int32_t*)p)[i];
+}
+__device__ __forceinline__ int length_of(const Pages& c, int b) { return held(c, scalar_at(c.lengths, b)); }
+__device__ __forceinline__ int blocks_of(const Pages& c, int b) { return blocks_in(length_of(c, b)); }
+__device__ __forceinline__ int lane_blocks_of(const Pages& c, int b) { return blocks_in(held(c, c.lengths[b])); }
+
+// Sum over a wavefront, the same in each lane.
+__device__ __forceinline__ int wave_isum(int v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// Blocks of all sequences (one head's).
+__device__ int all_blocks(const Pages& c) {
+  int n = 0;
+  for (int b = threadIdx.x & 63; b < c.B; b += 64) n += lane_blocks_of(c, b);
+  return __builtin_amdgcn_readfirstlane(wave_isum(n));
+}
+
+// The sequence that holds block y of them all, and the blocks before that sequence.
+__device__ int find_sequence(const Pages& c, int y, int& before) {
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 64) {
+    const int n = b0 + lane < c.B ? lane_blocks_of(c, b0 + lane) : 0;
+    int upto = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(upto, off, 64);
+      upto += lane >= off ? o : 0;
+    }
+    const uint64_t hit = __ballot(y < base + upto);
+    if (hit) {
+      const int i = __builtin_ctzll(hit);
+      before = __builtin_amdgcn_readfirstlane(base + __shfl(upto - n, i, 64));
+      return b0 + i;
+    }
+    base += __builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64));
+  }
+  before = base;
+  return c.B;
+}
+
+// What the runs share of a head's keys.  Block x of them all belongs to run ((x + 1) W - 1) / N.
+__device__ __forceinline__ int run_of(int64_t x, int64_t N, int W) { return (int)(((x + 1) * W - 1) / N); }
+__device__ __forceinline__ int64_t run_start(int64_t w, int64_t N, int W) { return w * N / W; }
+
+__device__ __forceinline__ float row_pair_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float row_pair_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// 16 bytes from each active lane's own address into LDS at lds + 16 x lane.
+__device__ __forceinline__ void lds_load16_at(uint32_t lds, const void* p) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
+}
+
+// 2^(byte - 127)
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// Eight E4M3 codes as 16-bit values (exact).
+template <bool BF16>
+__device__ __forceinline__ v4u widen8(uint32_t lo, uint32_t hi) {
+  v4u r;
+  if constexpr (BF16) {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+  } else {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+  }
+  return r;
+}
+
+// One row's eight values d = 8 i .. + 7 (i = lane % 16, the row's 16 lanes hold it all) into the output.
+template <bool BF16>
+__device__ __forceinline__ void store_row(const float* o, const PagedArgs& a, int b, int head, int i) {
+  const int D = a.c.D;
+  const int64_t row = (int64_t)b * a.Hq + head;
+  if (a.scales) {                                            // D is 128
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = umax32(top, abs_bits(o[e]));
+    const uint32_t byte = f8_scale_byte(row16_umax(top));
+    const bool bad = byte == 255u;
+    const float inv = bad ? 1.0f : f8_inv_scale(byte);
+    const uint2 w = {bad ? 0x7F7F7F7Fu : f8_pack4(o[0], o[1], o[2], o[3], inv),
+                     bad ? 0x7F7F7F7Fu : f8_pack4(o[4], o[5], o[6], o[7], inv)};
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * 128 + 8 * i) = w;
+    if (i == 0) {
+      const int SC = (int)f8_scale_cols((int64_t)a.Hq * 128);
+      uint8_t* const at = a.scales + (int64_t)b * SC;
+      at[head] = (uint8_t)byte;
+      if (head == a.Hq - 1)
+        for (int c = a.Hq; c < SC; ++c) at[c] = 0;
+    }
+  } else if (8 * i < D) {
+    *reinterpret_cast<v4u*>(static_cast<uint8_t*>(a.out) + (row * D + 8 * i) * 2) =
+        v4u{pack2_16<BF16>(o[0], o[1]), pack2_16<BF16>(o[2], o[3]), pack2_16<BF16>(o[4], o[5]), pack2_16<BF16>(o[6], o[7])};
+  }
+}
+
+// Floats of a partial result: 16 heads' sums, then their maxima and their sums of weights.
+template <int DP> constexpr int PART = 16 * DP + 32;
+
+// BF16: of queries and outputs.  WIDE: 16-bit rows of that type, else E4M3.  DP: D rounded up.
+template <bool BF16, bool WIDE, int DP, int S>
+__global__ __launch_bounds__(64 * NW) void paged_kernel(PagedArgs a, int W) {
+  constexpr int PITCH = WIDE ? 2 * DP : DP;                  // bytes of a row in LDS
+  constexpr int CH = PITCH / 16;                             // its 16-byte chunks
+  constexpr int LOADS = 16 * PITCH / 1024;                   // of 16 rows
+  constexpr int SLOT = 64 * PITCH + (WIDE ? 0 : 64);         // 32 keys, 32 values, scales
+  constexpr int NV = 4 * LOADS + (WIDE ? 0 : 1);             // vector loads of a step
+  constexpr int KS = DP / 32, DT = DP / 16;
+  constexpr int RING = S * SLOT;
+  constexpr int LIFT = BF16 || !WIDE ? 0 : 6;                // fp16 weights are held 2^6 larger: see below
+  constexpr bool SPLIT = !WIDE && !BF16;                     // weights as two bf16 numbers
+  constexpr int LDS = NW * RING > NW * 4 * PART<DP> ? NW * RING : NW * 4 * PART<DP>;
+  __shared__ __align__(1024) uint8_t lds[LDS];
+  const Pages& c = a.c;
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, r = lane & 15;
+  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16, HH = c.Hkv * HC;
+  const int RB = WIDE ? 2 * c.D : c.D;                       // bytes of a row
+  const int64_t N = (int64_t)all_blocks(c) * HH;
+  W = (int)min((int64_t)W, N);                               // no run is empty
+  const int w = blockIdx.x;
+  if (w >= W) return;
+  int64_t x = run_start(w, N, W);
+  const int64_t end = run_start(w + 1, N, W);
+
+  int before;
+  int b = find_sequence(c, (int)(x / HH), before);
+  if (b >= c.B) return;
+  int nb = blocks_of(c, b);
+  int unit = (int)((x - (int64_t)before * HH) / nb), j0 = (int)((x - (int64_t)before * HH) % nb);
+
+  auto swizzle_k = [](int row) { return PITCH == 256 ? row & 15 : PITCH == 128 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  auto swizzle_v = [](int row) {
+    if (!WIDE) return PITCH == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+    return PITCH == 256 ? 2 * (row & 7) : PITCH == 128 ? 2 * ((row >> 1) & 3) : 2 * ((row >> 2) & 1);
+  };
+  // this lane's part of a 1024-byte load: offsets of its key and value chunks from the row of the load
+  int vk[LOADS], vv[LOADS];
+#pragma unroll
+  for (int n = 0; n < LOADS; ++n) {
+    const int row = n * (1024 / PITCH) + lane / CH, ch = lane % CH;
+    const int ck = ch ^ swizzle_k(row), cv = ch ^ swizzle_v(row);
+    vk[n] = 16 * ck < RB ? row * RB + 16 * ck : KQ_OOB;
+    vv[n] = 16 * cv < RB ? row * RB + 16 * cv : KQ_OOB;
+  }
+  const uint32_t ring0 = lds_addr(lds) + wid * RING;
+  const uint8_t* const ring = lds + wid * RING;
+
+  bool first_piece = true;
+  while (x < end) {
+    const int len = length_of(c, b);
+    const int h = unit / HC, hc = unit % HC;
+    const int j1 = (int)min((int64_t)nb, j0 + (end - x));
+    const int heads = min(16, G - 16 * hc), head0 = h * G + 16 * hc;
+
+    // page of 16 keys from key0 on, and how many of them there are
+    auto page_of = [&](int key0, int& n) {
+      n = max(0, min(16, len - key0));
+      int64_t p = 0;
+      if (n > 0) {
+        p = scalar_at(c.table, (int64_t)b * c.width + key0 / c.page);
+        if (p < 0 || p >= c.pages) n = 0, p = 0;
+      }
+      return (p * c.Hkv + h) * c.page + (n > 0 ? key0 % c.page : 0);         // row in the cache
+    };
+    auto load = [&](int slot, int j) {                       // block j's 32 keys of this wavefront
+      const int key = j < j1 ? BLOCK * j + 32 * wid : len;
+      const uint32_t at = ring0 + slot * SLOT;
+      int64_t row[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        int n;
+        row[s] = page_of(key + 16 * s, n);
+        const v4i rk = rsrc_words(c.k + row[s] * RB, (int64_t)n * RB), rv = rsrc_words(c.v + row[s] * RB, (int64_t)n * RB);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) lds_load16(rk, at + 16 * PITCH * s + 1024 * i, vk[i]);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) lds_load16(rv, at + 16 * PITCH * (2 + s) + 1024 * i, vv[i]);
+      }
+      if constexpr (!WIDE) {
+        if (lane < 4) lds_load16_at(at + 64 * PITCH, (lane < 2 ? c.ks : c.vs) + ((lane & 1) ? row[1] : row[0]));
+      }
+    };
+
+    // queries: this lane's column is head r of the unit
+    v4u q[KS];
+    {
+      const __amdgpu_buffer_rsrc_t rq =
+          make_rsrc(a.q + b * a.qs + head0 * a.qh, (heads - 1) * a.qh + 2 * c.D);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        // 8-bit rows give a lane 16 codes at a time, which are two products' worth
+        const int d = WIDE ? 32 * i + 8 * g : 64 * (i / 2) + 16 * g + 8 * (i % 2);
+        q[i] = __builtin_bit_cast(
+            v4u, __builtin_amdgcn_raw_buffer_load_b128(rq, r < heads && d < c.D ? r * (int)a.qh + 2 * d : KQ_OOB, 0, 0));
+      }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i]));
+    }
+    v4f acc[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.0f;
+
+    int slot = 0;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) load(i, j0 + i);
+    for (int j = j0; j < j1; ++j) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the slot that is filled next has been read
+      load(slot == 0 ? S - 1 : slot - 1, j + S - 1);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm((S - 1) * NV));
+      asm volatile("" ::: "memory");
+      const uint8_t* const sk = ring + slot * SLOT;
+      const uint8_t* const sv = sk + 32 * PITCH;
+      v4f t[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        t[s] = v4f{0.f, 0.f, 0.f, 0.f};
+        const uint8_t* const row = sk + PITCH * (16 * s + r);
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+            t[s] = mfma16<BF16>(*reinterpret_cast<const v4u*>(row + 16 * ((4 * i + g) ^ swizzle_k(r))), q[i], t[s]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < KS / 2; ++i) {
+            const v4u w16 = *reinterpret_cast<const v4u*>(row + 16 * ((4 * i + g) ^ swizzle_k(r)));
+            t[s] = mfma16<BF16>(widen8<BF16>(w16[0], w16[1]), q[2 * i], t[s]);
+            t[s] = mfma16<BF16>(widen8<BF16>(w16[2], w16[3]), q[2 * i + 1], t[s]);
+          }
+        }
+      }
+      float vscale[8];
+      if constexpr (!WIDE) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t kb = *reinterpret_cast<const uint32_t*>(sk + 64 * PITCH + 16 * s + 4 * g);
+          const uint32_t vb = *reinterpret_cast<const uint32_t*>(sk + 64 * PITCH + 32 + 16 * s + 4 * g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            t[s][e] *= e8m0_value((kb >> (8 * e)) & 255u);
+            vscale[4 * s + e] = e8m0_value((vb >> (8 * e)) & 255u);
+          }
+        }
+      }
+      const int key = BLOCK * j + 32 * wid;
+      int n0, n1;
+      page_of(key, n0);
+      page_of(key + 16, n1);
+      if (n0 + n1 < 32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool seen = 4 * g + (e & 3) < (e < 4 ? n0 : n1);
+          t[e / 4][e & 3] = seen ? t[e / 4][e & 3] : -INFINITY;
+          if constexpr (!WIDE) vscale[e] = seen ? vscale[e] : 0.0f;
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, t[e / 4][e & 3]);
+      top = half_max(row_pair_max(top)) * a.scale;
+      if (__any(top > m + 8.0f)) {
+        const float to = fmaxf(m, top);
+        const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+      }
+      const float base = (m == -INFINITY ? 0.0f : m) - LIFT;
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(fmaf(t[e / 4][e & 3], a.scale, -base));
+        l += p[e];
+        if constexpr (!WIDE) p[e] *= vscale[e];
+      }
+      constexpr bool PB = BF16 || !WIDE;                     // the weights' 16-bit type
+      v4u pw, pl;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        pw[e] = pack2_16<PB>(p[2 * e], p[2 * e + 1]);
+        if constexpr (SPLIT)
+          pl[e] = pack2_16<true>(p[2 * e] - __uint_as_float(pw[e] << 16), p[2 * e + 1] - __uint_as_float(pw[e] & 0xFFFF0000u));
+      }
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        v4u v;
+        if constexpr (WIDE) {
+          const int row = 4 * g + (r >> 2);
+          const uint8_t* const at = sv + PITCH * row + 16 * ((2 * i + ((r & 3) >> 1)) ^ swizzle_v(row)) + 8 * (r & 1);
+          const v2u lo = lds_tr16(at), hi = lds_tr16(at + 16 * PITCH);
+          v = v4u{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+          const int k = r >> 1, row = 4 * g + (k & 3) + 16 * (k >> 2);
+          const v2u w8 = lds_tr8(sv + PITCH * row + 16 * (i ^ swizzle_v(row)) + 8 * (r & 1));
+          v = widen8<true>(w8[0], w8[1]);
+        }
+        acc[i] = mfma16<PB>(v, pw, acc[i]);
+        if constexpr (SPLIT) acc[i] = mfma16<true>(v, pl, acc[i]);
+      }
+      slot = slot == S - 1 ? 0 : slot + 1;
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    l = half_sum(row_pair_sum(l));
+    __syncthreads();                                         // all rings have been read
+    {
+      float* const o = reinterpret_cast<float*>(lds) + wid * PART<DP>;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) *reinterpret_cast<v4f*>(o + DP * r + 16 * i + 4 * g) = acc[i];
+      if (g == 0) o[16 * DP + r] = m, o[16 * DP + 16 + r] = l;
+    }
+    __syncthreads();
+    {
+      // thread: head threadIdx / 16, values 8 i .. + 7
+      const int hd = threadIdx.x >> 4, i = threadIdx.x & 15;
+      const float* const o = reinterpret_cast<const float*>(lds);
+      float top = -INFINITY, total = 0.0f, sum[8];
+#pragma unroll
+      for (int u = 0; u < NW; ++u) top = fmaxf(top, o[u * PART<DP> + 16 * DP + hd]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < NW; ++u) {
+        const float mu = o[u * PART<DP> + 16 * DP + hd];
+        const float f = mu == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mu - top);
+        total = fmaf(f, o[u * PART<DP> + 16 * DP + 16 + hd], total);
+        if (8 * i < DP) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, o[u * PART<DP> + DP * hd + 8 * i + e], sum[e]);
+        }
+      }
+      if (hd < heads) {
+        if (j0 == 0 && j1 == nb) {
+          const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] *= inv;
+          store_row<BF16>(sum, a, b, head0 + hd, i);
+        } else {
+          float* const part = a.part + (int64_t)(2 * w + (first_piece ? 0 : 1)) * PART<DP>;
+          if (8 * i < DP) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+              *reinterpret_cast<v4f*>(part + DP * hd + 8 * i + e) = v4f{sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
+          }
+          if (i == 0) part[16 * DP + hd] = top, part[16 * DP + 16 + hd] = total;
+        }
+      }
+    }
+    __syncthreads();
+    first_piece = false;
+    x += j1 - j0;
+    j0 = 0;
+    if (x < end && ++unit == HH) {
+      unit = 0;
+      do {
+        if (++b >= c.B) return;
+        nb = blocks_of(c, b);
+      } while (nb == 0);
+    }
+  }
+}
+
+// Joins what the runs left of heads they share, and writes zeros where a sequence has no keys.  One
+// workgroup per sequence and query head; its 16 rows of 16 threads take the runs in turn.
+template <bool BF16, int DP>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W) {
+  __shared__ float so[16][DP + 2];
+  const Pages& c = a.c;
+  const int head = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
+  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16, HH = c.Hkv * HC;
+  const int unit = head / G * HC + head % G / 16, hd = head % G % 16;
+  const int nb = blocks_of(c, b);
+  const int k = threadIdx.x >> 4, i = threadIdx.x & 15;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  if (nb == 0) {
+    if (k == 0) store_row<BF16>(sum, a, b, head, i);
+    return;
+  }
+  int before = 0;
+  for (int s = threadIdx.x & 63; s < b; s += 64) before += lane_blocks_of(c, s);
+  before = __builtin_amdgcn_readfirstlane(wave_isum(before));
+  const int64_t N = (int64_t)all_blocks(c) * HH, x0 = (int64_t)before * HH + (int64_t)unit * nb;
+  W = (int)min((int64_t)W, N);
+  const int w0 = run_of(x0, N, W), w1 = run_of(x0 + nb - 1, N, W);
+  if (w0 == w1) return;                                      // a run has written it
+  float m = -INFINITY, l = 0.0f;
+  for (int w = w0 + k; w <= w1; w += 16) {
+    const float* const part = a.part + (int64_t)(2 * w + (w == w0 && run_start(w, N, W) != x0 ? 1 : 0)) * PART<DP>;
+    const float mw = part[16 * DP + hd], lw = part[16 * DP + 16 + hd];
+    const float to = fmaxf(m, mw);
+    const float f0 = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+    const float f1 = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw - to);
+    m = to;
+    l = fmaf(l, f0, f1 * lw);
+    if (8 * i < DP) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = fmaf(sum[e], f0, f1 * part[DP * hd + 8 * i + e]);
+    }
+  }
+  if (8 * i < DP) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) so[k][8 * i + e] = sum[e];
+  }
+  if (i == 0) so[k][DP] = m, so[k][DP + 1] = l;
+  __syncthreads();
+  if (k > 0) return;
+  float top = -INFINITY, total = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) top = fmaxf(top, so[u][DP]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  for (int u = 0; u < 16; ++u) {
+    const float f = so[u][DP] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(so[u][DP] - top);
+    total = fmaf(f, so[u][DP + 1], total);
+    if (8 * i < DP) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, so[u][8 * i + e], sum[e]);
+    }
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] *= inv;
+  store_row<BF16>(sum, a, b, head, i);
+}
+
+// One wavefront a token: its sequence, position and page, then the rows of its heads, four at a time, 16
+// lanes a row; 8-bit rows are quantized as a group (row16_umax, as the quantizer's).
+template <bool BF16, bool WIDE>
+__global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
+  const int lane = threadIdx.x & 63;
+  const Pages& c = a.c;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= a.T) return;
+  int64_t b = t, behind = 1;                                 // tokens of the sequence from this one on
+  if (a.cu) {
+    int n = 0;
+    for (int i0 = 0; i0 < c.B; i0 += 64) {
+      const int i = i0 + lane;
+      const int k = __popcll(__ballot(i < c.B && a.cu[i + 1] <= t));
+      n += k;
+      if (k < 64) break;
+    }
+    b = __builtin_amdgcn_readfirstlane(n);
+    if (b >= c.B || t < a.cu[b]) return;
+    behind = a.cu[b + 1] - t;
+  }
+  const int64_t at = (int64_t)c.lengths[b] - behind;
+  if (at < 0 || at >= (int64_t)c.width * c.page) return;
+  const int64_t page = c.table[b * c.width + at / c.page];
+  if (page < 0 || page >= c.pages) return;
+  const int sub = lane & 15, RB = WIDE ? 2 * c.D : c.D;
+  for (int r0 = 0; r0 < 2 * c.Hkv; r0 += 4) {
+    const int row = r0 + (lane >> 4);
+    const bool key = row < c.Hkv;
+    const int h = key ? row : row - c.Hkv;
+    const bool there = row < 2 * c.Hkv && 8 * sub < c.D;
+    v4u w = {0, 0, 0, 0};
+    if (there) {
+      const AttnRows& src = key ? a.k : a.v;
+      w = *reinterpret_cast<const v4u*>(src.p + t * src.ts + h * src.hs + 16 * sub);
+    }
+    const int64_t to = (page * c.Hkv + h) * c.page + at % c.page;
+    if constexpr (WIDE) {
+      if (there) *reinterpret_cast<v4u*>((key ? c.k : c.v) + to * RB + 16 * sub) = w;
+    } else {
+      float y[8];
+      unpack8_16<BF16>(w, y);
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = umax32(top, abs_bits(y[e]));
+      const uint32_t byte = f8_scale_byte(row16_umax(top));
+      const bool bad = byte == 255u;
+      const float inv = bad ? 1.0f : f8_inv_scale(byte);
+      if (there) {
+        *reinterpret_cast<uint2*>((key ? c.k : c.v) + to * RB + 8 * sub) =
+            uint2{bad ? 0x7F7F7F7Fu : f8_pack4(y[0], y[1], y[2], y[3], inv),
+                  bad ? 0x7F7F7F7Fu : f8_pack4(y[4], y[5], y[6], y[7], inv)};
+        if (sub == 0) (key ? c.ks : c.vs)[to] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+// Runs of a call: one for each workgroup that the compute units hold, and no more than blocks.
+int64_t runs(int64_t B, int Hq, int Hkv, int64_t longest) {
+  const int G = Hq / Hkv, HC = (G + 15) / 16;
+  const int64_t blocks = B * Hkv * HC * ((longest + BLOCK - 1) / BLOCK);
+  const int64_t most = device_cu_count();
+  return blocks < 1 ? 1 : blocks < most ? blocks : most;
+}
+
+template <bool BF16, bool WIDE, int DP>
+hipError_t go(const PagedArgs& a, hipStream_t s) {
+  constexpr int S = WIDE ? (DP == 128 ? 2 : 4) : (DP == 128 ? 4 : 8);
+  const int W = (int)runs(a.c.B, a.Hq, a.c.Hkv, (int64_t)a.c.width * a.c.page);
+  hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, S>), dim3(W), dim3(64 * NW), 0, s, a, W);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((paged_join_kernel<BF16, DP>), dim3((unsigned)(a.c.B * a.Hq)), dim3(256), 0, s, a, W);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int64_t longest) {
+  return (size_t)(2 * runs(B, Hq, Hkv, longest)) * (D <= 64 ? PART<64> : PART<128>) * 4;
+}
+
+hipError_t launch_paged_attention(bool bf16, bool wide, const PagedArgs& a, hipStream_t s) {
+  if (a.c.D <= 64) {
+    if (bf16) return wide ? go<true, true, 64>(a, s) : go<true, false, 64>(a, s);
+    return wide ? go<false, true, 64>(a, s) : go<false, false, 64>(a, s);
+  }
+  if (bf16) return wide ? go<true, true, 128>(a, s) : go<true, false, 128>(a, s);
+  return wide ? go<false, true, 128>(a, s) : go<false, false, 128>(a, s);
+}
+
+hipError_t launch_cache_append(bool bf16, bool wide, const AppendArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.T + 3) / 4)), block(256);
+  if (bf16 && wide) hipLaunchKernelGGL((cache_append_kernel<true, true>), grid, block, 0, s, a);
+  else if (bf16) hipLaunchKernelGGL((cache_append_kernel<true, false>), grid, block, 0, s, a);
+  else if (wide) hipLaunchKernelGGL((cache_append_kernel<false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((cache_append_kernel<false, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace kq
