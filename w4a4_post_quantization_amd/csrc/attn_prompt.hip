@@ -10,7 +10,12 @@
 // from LDS by transposing reads.
 //
 // The running maximum is only moved when a score passes it by 2^8 (weights up to 256 lose nothing in
-// float32 sums or 16-bit weights), which spares most rescalings of the 16 DT accumulators.
+// float32 sums or 16-bit weights), which spares most rescalings of the 16 DT accumulators.  fp16 weights are held
+// 2^6 larger, to 2^14 at most, so that what falls under fp16's smallest step is 2^-31 of the largest.
+//
+// A step multiplies the next tile's keys while the present tile's exponentials are taken, and the present
+// tile's values while the next maximum is, so that the matrix cores and the vector units have work of
+// the same wavefront side by side.
 #include "kq_attn.hpp"
 #include "kq_launch.hpp"
 
@@ -20,18 +25,20 @@ namespace {
 
 constexpr int KT = 64;                 // keys of a tile
 
-// Where a workgroup's queries and keys are.
+// Where a workgroup's queries and keys are.  Its rows are those of one key head: row i is query i / G of head
+// i % G of the G that share the key head, so that they share the tiles of keys, too, and a tile's rows
+// end at nearly the same key.
 struct Span {
   int64_t q0, k0;                      // first query of the sequence, first key
   int32_t nq, nk;                      // their numbers
-  int32_t first;                       // the workgroup's first query within the sequence
+  int32_t first;                       // the workgroup's first row within the sequence
 };
 
-// Sequence i's queries begin at slot cu_q[i] / QT + i of the grid, which leaves each at least as many
+// Sequence i's rows begin at slot G cu_q[i] / QT + i of the grid, which leaves each at least as many
 // slots as it has tiles without anyone having summed the tiles: a slot finds its sequence by counting
 // the starts up to itself, 64 at a time.  Entries are held to 0 .. T and to their order.
 template <int QT>
-__device__ bool find_span(const AttnArgs& a, int32_t slot, Span& s) {
+__device__ bool find_span(const AttnArgs& a, int G, int32_t slot, Span& s) {
   if (!a.cu_q) {
     s = {0, 0, (int32_t)a.T, (int32_t)a.Tk, slot * QT};
     return true;
@@ -41,7 +48,7 @@ __device__ bool find_span(const AttnArgs& a, int32_t slot, Span& s) {
   int n = 0;
   for (int i0 = 0; i0 < a.B; i0 += 64) {
     const int i = i0 + lane;
-    const bool before = i < a.B && min(max(a.cu_q[i], 0), T) / QT + i <= slot;
+    const bool before = i < a.B && min(max(a.cu_q[i], 0), T) * G / QT + i <= slot;
     const int c = __popcll(__ballot(before));
     n += c;
     if (c < 64) break;
@@ -49,16 +56,28 @@ __device__ bool find_span(const AttnArgs& a, int32_t slot, Span& s) {
   const int i = __builtin_amdgcn_readfirstlane(max(n - 1, 0));
   const int32_t q0 = min(max(a.cu_q[i], 0), T), q1 = min(max(a.cu_q[i + 1], q0), T);
   const int32_t k0 = min(max(a.cu_k[i], 0), Tk), k1 = min(max(a.cu_k[i + 1], k0), Tk);
-  s = {q0, k0, q1 - q0, k1 - k0, (slot - (q0 / QT + i)) * QT};
-  return s.first >= 0 && s.first < s.nq;                   // entries out of order lead to no slot below 0
+  s = {q0, k0, q1 - q0, k1 - k0, (slot - (q0 * G / QT + i)) * QT};
+  return s.first >= 0 && s.first < s.nq * G;                 // entries out of order lead to no slot below 0
+}
+
+// acc + both halves of a packed pair (their products by 1 are exact).
+template <bool BF16>
+__device__ __forceinline__ float add_pair(uint32_t w, float acc) {
+  if constexpr (BF16) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, w), __builtin_bit_cast(v2bf, 0x3F803F80u), acc, false);
+  } else {
+    return add_f16x2(w, acc);
+  }
 }
 
 // Scores of masked keys.
 constexpr float HIDDEN = -INFINITY;
 
-template <bool BF16, int KS, int DT, int NW>
+template <bool BF16, int KS, int DT, int NW, int R>
 struct Prompt {
-  static constexpr int QT = 32 * NW;
+  static constexpr int QT = 32 * R * NW;                              // R times 32 queries a wavefront
+  static constexpr float LIFT = BF16 ? 0.0f : 6.0f;
   static constexpr int PITCH = KS <= 4 ? 128 : 256;                  // bytes of a key's row in LDS
   static constexpr int TILE = KT * PITCH;
   static constexpr int LOADS = TILE / (1024 * NW);                   // of a wavefront, a matrix and tile
@@ -70,22 +89,28 @@ struct Prompt {
   __device__ static int swizzle_k(int row) { return PITCH == 256 ? row & 15 : (row >> 1) & 7; }
   __device__ static int swizzle_v(int row) { return PITCH == 256 ? 4 * (row & 3) : 4 * ((row >> 1) & 1); }
 
-  // One pass over the keys: unnormalized O^T in acc, this lane's part of the sums in l.  SAFE: infinities
-  // and NaN among the values reach only the queries that see them (0 times either would not be 0).
-  template <bool SAFE>
-  __device__ static void pass(const AttnArgs& a, const Span& s, int head, uint8_t* lds, const v4u (&q)[KS], v16f (&acc)[DT],
-                              float& l) {
+  // One pass over the keys: unnormalized O^T in acc, this lane's part of the sums in l.  A value that is not finite would
+  // reach queries that do not see it (0 times it is not 0), so where a result is not finite the pass is made
+  // again: FINITE leaves such values out; UP and DOWN count, instead of weighing, the visible values that
+  // are infinite upwards or NaN, and downwards or NaN.
+  enum Pass { PLAIN, FINITE, UP, DOWN };
+  static constexpr uint32_t ONE = BF16 ? 0x3F80u : 0x3C00u;
+  template <Pass PASS>
+  __device__ static void pass(const AttnArgs& a, const Span& s, int hk, int G, uint8_t* lds, const v4u (&q)[R][KS],
+                              v16f (&acc)[R][DT], float (&l)[R]) {
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = lane >> 5, hk = head / (a.Hq / a.Hkv);
+    const int half = lane >> 5;
     const int off = s.nk - s.nq;                                     // query i sees keys to i + off
-    const int last = min(s.first + QT, s.nq) - 1;
-    const int nk = a.causal ? max(min(s.nk, last + off + 1), 0) : s.nk;
-    const int tiles = (nk + KT - 1) / KT;
-    const int mine = s.first + 32 * wid + (lane & 31);               // this lane's query
-    const int sees = a.causal ? min(mine + off + 1, s.nk) : s.nk;    // keys it sees
-    const int w0 = s.first + 32 * wid;
-    const int wsees = w0 >= s.nq ? 0 : a.causal ? min(w0 + 32 + off, s.nk) : s.nk;   // any of the wavefront's
-    const int wall = a.causal ? min(w0 + off + 1, s.nk) : s.nk;      // all of them
+    const int rows = s.nq * G, w0 = s.first + 32 * R * wid;          // the wavefront's first row
+    auto sees_of = [&](int row) { return a.causal ? min(row / G + off + 1, s.nk) : s.nk; };
+    const int nk = max(sees_of(min(s.first + QT, rows) - 1), 0);
+    const int tiles = (nk + KT - 1) / KT;                            // that any of the workgroup's rows sees
+    int sees[R];                                                     // keys the lane's rows see
+#pragma unroll
+    for (int r = 0; r < R; ++r) sees[r] = sees_of(w0 + 32 * r + (lane & 31));
+    const int wsees = w0 >= rows ? 0 : sees_of(min(w0 + 32 * R, rows) - 1);      // any of the wavefront's
+    const int wall = sees_of(w0);                                    // all of them
+    const int wtiles = wsees > 0 ? (wsees + KT - 1) / KT : 0;
 
     const int row = ROWS * wid + lane / (PITCH / 16), ch = lane % (PITCH / 16);
     const int ck = ch ^ swizzle_k(row), cv = ch ^ swizzle_v(row), chunks = a.D / 8;
@@ -94,16 +119,20 @@ struct Prompt {
     const uint32_t lds0 = lds_addr(lds) + 1024 * wid;
     const uint8_t* const kp = a.k.p + s.k0 * a.k.ts + hk * a.k.hs;
     const uint8_t* const vp = a.v.p + s.k0 * a.v.ts + hk * a.v.hs;
-    auto load = [&](int t) {
-      const int left = s.nk - KT * t;                                // rows behind the last key: zeros
-      const v4i rk = rsrc_words(kp + (int64_t)KT * t * a.k.ts, (int64_t)(left - 1) * a.k.ts + 2 * a.D);
-      const v4i rv = rsrc_words(vp + (int64_t)KT * t * a.v.ts, (int64_t)(left - 1) * a.v.ts + 2 * a.D);
-      const uint32_t at = lds0 + (t & 1) * 2 * TILE;
-#pragma unroll
-      for (int n = 0; n < LOADS; ++n) lds_load16(rk, at + 1024 * NW * n, (int)(vk + (uint32_t)(ROWS * NW * n) * (uint32_t)a.k.ts));
+    // rows behind the last key: zeros; tiles behind the last: nothing
+    auto load_k = [&](int t) {
+      if (t >= tiles) return;
+      const v4i r = rsrc_words(kp + (int64_t)KT * t * a.k.ts, (int64_t)(s.nk - KT * t - 1) * a.k.ts + 2 * a.D);
 #pragma unroll
       for (int n = 0; n < LOADS; ++n)
-        lds_load16(rv, at + TILE + 1024 * NW * n, (int)(vv + (uint32_t)(ROWS * NW * n) * (uint32_t)a.v.ts));
+        lds_load16(r, lds0 + (t & 1) * TILE + 1024 * NW * n, (int)(vk + (uint32_t)(ROWS * NW * n) * (uint32_t)a.k.ts));
+    };
+    auto load_v = [&](int t) {
+      if (t >= tiles) return;
+      const v4i r = rsrc_words(vp + (int64_t)KT * t * a.v.ts, (int64_t)(s.nk - KT * t - 1) * a.v.ts + 2 * a.D);
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n)
+        lds_load16(r, lds0 + (2 + (t & 1)) * TILE + 1024 * NW * n, (int)(vv + (uint32_t)(ROWS * NW * n) * (uint32_t)a.v.ts));
     };
 
     // this lane's fragment addresses within a tile
@@ -116,200 +145,226 @@ struct Prompt {
     for (int i = 0; i < DT; ++i)
       va[i] = PITCH * vr + 16 * ((4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swizzle_v(vr)) + 8 * (lane & 1);
 
+    float m[R], base[R];                                             // scaled: weights are exp2(x c - base)
+    v16f x[R][2];                                                    // scores of a tile
+    v4u p[R][4];                                                     // its weights
 #pragma unroll
-    for (int i = 0; i < DT; ++i)
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
-    l = 0.0f;
-    float m = HIDDEN;                                                // scaled: exponents are x c - m
-    if (tiles > 0) load(0);
-    for (int t = 0; t < tiles; ++t) {
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[r][i][e] = 0.0f;
+      l[r] = base[r] = 0.0f;
+      m[r] = HIDDEN;
+    }
+
+    // fragment n of a tile's keys (rows 32 (n % 2) .. + 31, contraction step n / 2) and of its values (row block n % DT,
+    // contraction step n / DT)
+    auto key_frag = [&](int t, int n) {
+      return *reinterpret_cast<const v4u*>(lds + (t & 1) * TILE + 32 * PITCH * (n & 1) + ka[n >> 1]);
+    };
+    auto value_frag = [&](int t, int n) {
+      const uint8_t* const at = lds + (2 + (t & 1)) * TILE + va[n % DT] + 16 * PITCH * (n / DT);
+      const v2u lo = lds_tr16(at), hi = lds_tr16(at + 8 * PITCH);
+      v4u v = {lo[0], lo[1], hi[0], hi[1]};
+      if constexpr (PASS != PLAIN) {
+        constexpr uint32_t INF = BF16 ? 0x7F80u : 0x7C00u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int sh = 16 * (e & 1);
+          const uint32_t w = (v[e / 2] >> sh) & 0xFFFFu;
+          const bool fin = (w & INF) != INF;
+          const uint32_t to = PASS == FINITE ? (fin ? w : 0u) : fin || w == (PASS == UP ? INF | 0x8000u : INF) ? 0u : ONE;
+          v[e / 2] = (v[e / 2] & ~(0xFFFFu << sh)) | (to << sh);
+        }
+      }
+      return v;
+    };
+    // weights 2 n and 2 n + 1 of the lane's 32
+    auto weight_pair = [&](const v16f (&y)[R][2], int key, int r, int n) {
+      const int h = n >> 3, e = 2 * (n & 7);
+      const float p0 = __builtin_amdgcn_exp2f(fmaf(y[r][h][e], a.c, -base[r]));
+      const float p1 = __builtin_amdgcn_exp2f(fmaf(y[r][h][e + 1], a.c, -base[r]));
+      const uint32_t w = pack2_16<BF16>(p0, p1);
+      l[r] = add_pair<BF16>(w, l[r]);
+      if constexpr (PASS < UP) {
+        p[r][n >> 2][n & 3] = w;
+      } else {
+        const int at = key + 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
+        p[r][n >> 2][n & 3] = (at < sees[r] ? ONE : 0u) | (at + 1 < sees[r] ? ONE << 16 : 0u);
+      }
+    };
+    // The compiler's own order reads each fragment just before its product; these loops keep AHEAD fragments in
+    // flight and put a share of the vector work behind each product.
+    constexpr int AHEAD = 4, NK = 2 * KS, NV = 4 * DT;
+    auto scores = [&](int t, auto beside) {
+      v4u f[NK];
+      v16f z;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) f[n] = key_frag(t, n);
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        if (n + AHEAD < NK) f[n + AHEAD] = key_frag(t, n + AHEAD);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          x[r][n & 1] = mfma32<BF16>(f[n], q[r][n >> 1], n < 2 ? z : x[r][n & 1]);
+#pragma unroll
+          for (int i = 16 * n / NK; i < 16 * (n + 1) / NK; ++i) beside(r, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+    auto values = [&](int t, auto beside) {
+      v4u f[NV];
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) f[n] = value_frag(t, n);
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        if (n + AHEAD < NV) f[n + AHEAD] = value_frag(t, n + AHEAD);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          acc[r][n % DT] = mfma32<BF16>(f[n], p[r][n / DT], acc[r][n % DT]);
+#pragma unroll
+          for (int i = 16 * n / NV; i < 16 * (n + 1) / NV; ++i) beside(r, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+    auto hide = [&](int key) {
+      if (key + KT > wall) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int left = sees[r] - key - 4 * half;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[r][h][e] = 32 * h + 8 * (e >> 2) + (e & 3) < left ? x[r][h][e] : HIDDEN;
+        }
+      }
+    };
+    auto raise = [&](float (&top)[R]) {
+      bool up = false;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        top[r] = half_max(top[r]) * a.c;
+        up |= top[r] > m[r] + 8.0f;
+      }
+      if (__any(up)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float to = fmaxf(m[r], top[r]);
+          const float f = to == HIDDEN ? 1.0f : __builtin_amdgcn_exp2f(m[r] - to);
+          m[r] = to;
+          base[r] = (to == HIDDEN ? 0.0f : to) - LIFT;
+          if constexpr (PASS < UP) {
+            l[r] *= f;
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[r][i][e] *= f;
+          }
+        }
+      }
+    };
+    // Tile t's keys one step ahead of its values: a step's products need K(t + 1) and V(t), its loads fill the slots of
+    // K(t) and V(t - 1), which the step before has read.
+    auto step = [&](int t) {
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
       lds_barrier();
-      if (t + 1 < tiles) load(t + 1);
-      const int key = KT * t;
-      if (key >= wsees) continue;                                    // nothing here that this wavefront sees
-      const uint8_t* const tk = lds + (t & 1) * 2 * TILE;
-      const uint8_t* const tv = tk + TILE;
-      v16f x[2];
+      load_k(t + 2);
+      load_v(t + 1);
+    };
+
+    load_k(0);
+    step(-1);
+    float top[R];
+    auto reset = [&] {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int r = 0; r < R; ++r) top[r] = HIDDEN;
+    };
+    auto compare = [&](int r, int n) { top[r] = fmaxf(fmaxf(top[r], x[r][n >> 3][2 * (n & 7)]), x[r][n >> 3][2 * (n & 7) + 1]); };
+    if (wtiles > 0) {
+      scores(0, [](int, int) {});
+      hide(0);
+      reset();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[h][e] = 0.0f;
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < KS; ++i)
-          x[h] = mfma32<BF16>(*reinterpret_cast<const v4u*>(tk + 32 * PITCH * h + ka[i]), q[i], x[h]);
-      }
-      if (key + KT > wall) {
-        const int left = sees - key - 4 * half;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            x[h][e] = 32 * h + 8 * (e >> 2) + (e & 3) < left ? x[h][e] : HIDDEN;
-      }
-      float top = HIDDEN;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, x[h][e]);
-      top = half_max(top) * a.c;
-      if (__any(top > m + 8.0f)) {
-        const float to = fmaxf(m, top);
-        const float f = to == HIDDEN ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-        m = to;
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-      }
-      const float base = m == HIDDEN ? 0.0f : m;
-      float sum = 0.0f;
-      v4u p[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float p0 = __builtin_amdgcn_exp2f(fmaf(x[h][e], a.c, -base));
-          const float p1 = __builtin_amdgcn_exp2f(fmaf(x[h][e + 1], a.c, -base));
-          sum += p0 + p1;
-          p[2 * h + (e >> 3)][(e & 7) >> 1] = pack2_16<BF16>(p0, p1);
-        }
-      l += sum;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        if constexpr (SAFE) {
-          v16f up, down;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) up[e] = down[e] = 0.0f;
-          constexpr uint32_t INF = BF16 ? 0x7F80u : 0x7C00u, ONE = BF16 ? 0x3F80u : 0x3C00u;
-          for (int j = 0; j < 4; ++j) {
-            const uint8_t* const at = tv + va[i] + 16 * PITCH * j;
-            const v2u lo = lds_tr16(at), hi = lds_tr16(at + 8 * PITCH);
-            const v4u b = j == 0 ? p[0] : j == 1 ? p[1] : j == 2 ? p[2] : p[3];
-            v4u fin = {lo[0], lo[1], hi[0], hi[1]}, pos = {0, 0, 0, 0}, neg = {0, 0, 0, 0}, see = {0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int sh = 16 * (e & 1);
-              const uint32_t w = (fin[e / 2] >> sh) & 0xFFFFu;
-              if ((w & INF) == INF) {
-                fin[e / 2] &= ~(0xFFFFu << sh);
-                if (w != (INF | 0x8000u)) pos[e / 2] |= ONE << sh;
-                if (w != INF) neg[e / 2] |= ONE << sh;
-              }
-              if (key + 16 * j + 8 * (e >> 2) + 4 * half + (e & 3) < sees) see[e / 2] |= ONE << sh;
-            }
-            acc[i] = mfma32<BF16>(fin, b, acc[i]);
-            up = mfma32<BF16>(pos, see, up);
-            down = mfma32<BF16>(neg, see, down);
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            acc[i][e] += (up[e] > 0.0f ? INFINITY : 0.0f) + (down[e] > 0.0f ? -INFINITY : 0.0f);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint8_t* const at = tv + va[i] + 16 * PITCH * j;
-            const v2u lo = lds_tr16(at), hi = lds_tr16(at + 8 * PITCH);
-            acc[i] = mfma32<BF16>(v4u{lo[0], lo[1], hi[0], hi[1]}, p[j], acc[i]);
-          }
-        }
-      }
+        for (int n = 0; n < 16; ++n) compare(r, n);
+      raise(top);
     }
+    int t = 0;
+    for (; t + 1 < wtiles; ++t) {
+      step(t);
+      v16f y[R][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r) y[r][0] = x[r][0], y[r][1] = x[r][1];
+      scores(t + 1, [&](int r, int n) { weight_pair(y, KT * t, r, n); });
+#pragma unroll
+      for (int r = 0; r < R; ++r)                                    // here, not behind the branch
+        asm volatile("" : "+v"(p[r][0]), "+v"(p[r][1]), "+v"(p[r][2]), "+v"(p[r][3]));
+      hide(KT * (t + 1));
+      reset();
+      values(t, compare);
+      raise(top);
+    }
+    if (t < wtiles) {
+      step(t);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) weight_pair(x, KT * t, r, n);
+      values(t, [](int, int) {});
+      ++t;
+    }
+    for (; t < tiles; ++t) step(t);
   }
 };
 
-template <bool BF16, int KS, int DT, int NW>
-__global__ __launch_bounds__(64 * NW) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
-  using P = Prompt<BF16, KS, DT, NW>;
-  constexpr int QT = P::QT;
-  constexpr int LDS = 4 * P::TILE > 32 * NW * P::OPITCH ? 4 * P::TILE : 32 * NW * P::OPITCH;
-  __shared__ __align__(1024) uint8_t lds[LDS];
-  // The compute dies take workgroups in turn; each is given heads of its own (the queries' heads of one
-  // key head next to each other), so that a die's level-2 cache holds few heads' keys.  The last queries,
-  // who see the most keys, go first.
-  const uint32_t id = blockIdx.x, H = a.Hq;
-  uint32_t head, slot;
-  if (H % 8 == 0) {
-    const uint32_t per = H / 8, i = id / 8;
-    head = id % 8 * per + i % per;
-    slot = i / per;
-  } else {
-    head = id % H;
-    slot = id / H;
-  }
-  Span s;
-  if (!find_span<QT>(a, slots - 1 - (int32_t)slot, s)) return;
-
-  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half = lane >> 5, w0 = s.first + 32 * wid, rows = min(32, s.nq - w0);
-  v4u q[KS];
-  {
-    const __amdgpu_buffer_rsrc_t rq =
-        make_rsrc(a.q.p + (s.q0 + w0) * a.q.ts + head * a.q.hs, rows > 0 ? (rows - 1) * a.q.ts + 2 * a.D : 0);
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      const int ch = 2 * i + half;
-      const int at = ch < a.D / 8 ? (lane & 31) * (int)a.q.ts + 16 * ch : KQ_OOB;
-      q[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rq, at, 0, 0));
-    }
-#pragma unroll
-    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i]));      // here before the loop's own loads
-  }
-  v16f acc[DT];
-  float l;
-  P::template pass<false>(a, s, head, lds, q, acc, l);
-  l = half_sum(l);
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) bad |= !(fabsf(acc[i][e]) < INFINITY);
-  if (__builtin_expect(__syncthreads_or(bad), 0)) {                  // rare: the pass again, with care
-    P::template pass<true>(a, s, head, lds, q, acc, l);
-    l = half_sum(l);
-    __syncthreads();
-  }
-  const float r = l == 0.0f ? 0.0f : 1.0f / l;                       // a query that sees nothing: zeros
-  const int64_t t0 = s.q0 + w0;
-
-  // whole rows through LDS
-  uint8_t* const mine = lds + 32 * P::OPITCH * wid;
-  if constexpr (DT == 4 && KS == 8) {
-    if (a.scales) {
+// Outputs of rows row0 .. + 31 (below `rows`): acc holds their O^T, unnormalized; `mine` is the wavefront's own LDS.
+template <bool BF16, int DT, int OPITCH>
+__device__ __forceinline__ void store_rows(const AttnArgs& a, const v16f (&acc)[DT], float inv, int64_t q0, int hk, int G,
+                                           int row0, int rows, uint8_t* mine) {
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  auto place = [&](int row) { return (q0 + row / G) * a.Hq + hk * G + row % G; };      // of a row among all outputs
+  if constexpr (DT == 4) {
+    if (a.scales) {                                                  // D is 128
       uint32_t top = 0;
+      float o[DT][16];
 #pragma unroll
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          acc[i][e] *= r;
-          top = umax32(top, abs_bits(acc[i][e]));
+          o[i][e] = acc[i][e] * inv;
+          top = umax32(top, abs_bits(o[i][e]));
         }
-      const auto o = __builtin_amdgcn_permlane32_swap(top, top, false, false);
-      const uint32_t byte = f8_scale_byte(umax32(o[0], o[1]));
+      const auto x = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+      const uint32_t byte = f8_scale_byte(umax32(x[0], x[1]));
       const bool nan = byte == 255u;
-      const float inv = nan ? 1.0f : f8_inv_scale(byte);
+      const float unit = nan ? 1.0f : f8_inv_scale(byte);
 #pragma unroll
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<uint32_t*>(mine + P::OPITCH * (lane & 31) + 32 * i + 2 * e + 4 * half) =
-              nan ? 0x7F7F7F7Fu : f8_pack4(acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3], inv);
-      const int64_t SC = f8_scale_cols((int64_t)a.Hq * 128);
-      if (half == 0 && lane < rows) {
-        uint8_t* const at = a.scales + (t0 + lane) * SC;
+          *reinterpret_cast<uint32_t*>(mine + OPITCH * (lane & 31) + 32 * i + 2 * e + 4 * half) =
+              nan ? 0x7F7F7F7Fu : f8_pack4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3], unit);
+      if (half == 0 && row0 + lane < rows) {
+        const int row = row0 + lane, head = hk * G + row % G, SC = (int)f8_scale_cols((int64_t)a.Hq * 128);
+        uint8_t* const at = a.scales + (q0 + row / G) * SC;
         at[head] = (uint8_t)byte;
-        if (head == H - 1)
-          for (int64_t c = H; c < SC; ++c) at[c] = 0;
+        if (head == a.Hq - 1)
+          for (int c = a.Hq; c < SC; ++c) at[c] = 0;
       }
       __builtin_amdgcn_wave_barrier();
-      uint8_t* const out = static_cast<uint8_t*>(a.out) + (t0 * a.Hq + head) * 128;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = 8 * i + (lane >> 3), c = 16 * (lane & 7);
-        if (row < rows)
-          *reinterpret_cast<v4u*>(out + (int64_t)row * a.Hq * 128 + c) = *reinterpret_cast<const v4u*>(mine + P::OPITCH * row + c);
+        if (row0 + row < rows)
+          *reinterpret_cast<v4u*>(static_cast<uint8_t*>(a.out) + place(row0 + row) * 128 + c) =
+              *reinterpret_cast<const v4u*>(mine + OPITCH * row + c);
       }
       return;
     }
@@ -318,37 +373,132 @@ __global__ __launch_bounds__(64 * NW) void attn_prompt_kernel(AttnArgs a, int32_
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int e = 0; e < 16; e += 4)
-      *reinterpret_cast<v2u*>(mine + P::OPITCH * (lane & 31) + 64 * i + 4 * e + 8 * half) =
-          v2u{pack2_16<BF16>(acc[i][e] * r, acc[i][e + 1] * r), pack2_16<BF16>(acc[i][e + 2] * r, acc[i][e + 3] * r)};
+      *reinterpret_cast<v2u*>(mine + OPITCH * (lane & 31) + 64 * i + 4 * e + 8 * half) =
+          v2u{pack2_16<BF16>(acc[i][e] * inv, acc[i][e + 1] * inv), pack2_16<BF16>(acc[i][e + 2] * inv, acc[i][e + 3] * inv)};
   __builtin_amdgcn_wave_barrier();
-  uint8_t* const out = static_cast<uint8_t*>(a.out) + (t0 * a.Hq + head) * 2 * a.D;
   const int chunks = a.D / 8;
   constexpr int PER = 4 * DT;                                        // chunks of a row in LDS
 #pragma unroll
   for (int i = 0; i < PER / 2; ++i) {
     const int n = 64 * i + lane, row = n / PER, c = n % PER;
-    if (row < rows && c < chunks)
-      *reinterpret_cast<v4u*>(out + (int64_t)row * a.Hq * 2 * a.D + 16 * c) =
-          *reinterpret_cast<const v4u*>(mine + P::OPITCH * row + 16 * c);
+    if (row0 + row < rows && c < chunks)
+      *reinterpret_cast<v4u*>(static_cast<uint8_t*>(a.out) + place(row0 + row) * 2 * a.D + 16 * c) =
+          *reinterpret_cast<const v4u*>(mine + OPITCH * row + 16 * c);
   }
 }
 
-template <bool BF16, int KS, int DT>
+// Which of the lane's counts are above zero.
+template <int R, int DT>
+__device__ __forceinline__ void seen_bits(const v16f (&acc)[R][DT], uint32_t (&bits)[R][DT]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      bits[r][i] = 0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) bits[r][i] |= acc[r][i][e] > 0.0f ? 1u << e : 0u;
+    }
+}
+
+template <bool BF16, int KS, int DT, int NW, int R>
+__global__ __launch_bounds__(64 * NW, R == 1 && NW == 4 ? 2 : 1) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
+  using P = Prompt<BF16, KS, DT, NW, R>;
+  constexpr int QT = P::QT;
+  constexpr int LDS = 4 * P::TILE > 32 * NW * P::OPITCH ? 4 * P::TILE : 32 * NW * P::OPITCH;
+  __shared__ __align__(1024) uint8_t lds[LDS];
+  // The eight compute dies take workgroups in turn.  Each is given key heads of its own (or a share of one head's
+  // rows), so that its level-2 cache holds few heads' keys.  The last rows, which see the most keys, go first.
+  const uint32_t id = blockIdx.x, H = a.Hkv, die = id % 8;
+  uint32_t hk, slot;
+  if (H % 8 == 0) {
+    const uint32_t per = H / 8, i = id / 8;
+    hk = die * per + i % per;
+    slot = i / per;
+  } else if (8 % H == 0) {
+    hk = die % H;
+    slot = id / 8 * (8 / H) + die / H;
+    if (slot >= (uint32_t)slots) return;
+  } else {
+    hk = id % H;
+    slot = id / H;
+  }
+  const int G = a.Hq / a.Hkv;
+  Span s;
+  if (!find_span<QT>(a, G, slots - 1 - (int32_t)slot, s)) return;
+
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, w0 = s.first + 32 * R * wid, rows = s.nq * G;
+  v4u q[R][KS];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = w0 + 32 * r + (lane & 31);
+    const uint8_t* const at = a.q.p + (s.q0 + row / G) * a.q.ts + (int64_t)(hk * G + row % G) * a.q.hs + 16 * half;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      q[r][i] = v4u{0, 0, 0, 0};
+      if (row < rows && 2 * i + half < a.D / 8) q[r][i] = *reinterpret_cast<const v4u*>(at + 32 * i);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[r][i]));   // here before the loop's own loads
+  v16f acc[R][DT];
+  float l[R];
+  P::template pass<P::PLAIN>(a, s, hk, G, lds, q, acc, l);
+  bool bad = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) bad |= !(fabsf(acc[r][i][e]) < INFINITY);
+  if (__builtin_expect(__syncthreads_or(bad), 0)) {
+    uint32_t up[R][DT], down[R][DT];
+    P::template pass<P::UP>(a, s, hk, G, lds, q, acc, l);
+    seen_bits(acc, up);
+    __syncthreads();
+    P::template pass<P::DOWN>(a, s, hk, G, lds, q, acc, l);
+    seen_bits(acc, down);
+    __syncthreads();
+    P::template pass<P::FINITE>(a, s, hk, G, lds, q, acc, l);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[r][i][e] += (up[r][i] >> e & 1 ? INFINITY : 0.0f) + (down[r][i] >> e & 1 ? -INFINITY : 0.0f);
+    __syncthreads();
+  }
+  // whole rows through LDS, 32 at a time
+  uint8_t* const mine = lds + 32 * P::OPITCH * wid;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float sum = half_sum(l[r]);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;               // a query that sees nothing: zeros
+    store_rows<BF16, DT, P::OPITCH>(a, acc[r], inv, s.q0, hk, G, w0 + 32 * r, rows, mine);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+template <bool BF16, int KS, int DT, int NW, int R>
 hipError_t go(const AttnArgs& a, hipStream_t s) {
-  constexpr int NW = 4, QT = 32 * NW;
-  const int64_t slots = a.cu_q ? a.T / QT + a.B : (a.T + QT - 1) / QT;
-  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW>), dim3((unsigned)(slots * a.Hq)), dim3(64 * NW), 0, s, a,
+  constexpr int QT = 32 * R * NW;
+  const int64_t rows = a.T * (a.Hq / a.Hkv);
+  const int64_t slots = a.cu_q ? rows / QT + a.B : (rows + QT - 1) / QT;
+  const int64_t grid = a.Hkv % 8 && 8 % a.Hkv == 0 ? (slots + 8 / a.Hkv - 1) / (8 / a.Hkv) * 8 : slots * a.Hkv;
+  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, R>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a,
                      (int32_t)slots);
   return hipGetLastError();
 }
 
 template <bool BF16>
 hipError_t by_width(const AttnArgs& a, hipStream_t s) {
-  if (a.D <= 32) return go<BF16, 2, 1>(a, s);
-  if (a.D <= 64) return go<BF16, 4, 2>(a, s);
-  if (a.D <= 80) return go<BF16, 5, 3>(a, s);
-  if (a.D <= 96) return go<BF16, 6, 3>(a, s);
-  return go<BF16, 8, 4>(a, s);
+  if (a.D <= 32) return go<BF16, 2, 1, 4, 1>(a, s);
+  if (a.D <= 64) return go<BF16, 4, 2, 4, 1>(a, s);
+  if (a.D <= 80) return go<BF16, 5, 3, 4, 1>(a, s);
+  if (a.D <= 96) return go<BF16, 6, 3, 4, 1>(a, s);
+  return go<BF16, 8, 4, 4, 1>(a, s);
 }
 
 }  // namespace
