@@ -3,15 +3,17 @@
 // The cache's bytes bound it.  The batch's keys are cut into blocks of 128 (a key head's blocks after one
 // another, then the next head's, then the next sequence's) and the blocks are dealt to a fixed number of
 // workgroups in equal runs, whatever the lengths: a run may end inside a head's keys and begin inside
-// another's.  A run's whole heads go out at once; of a head that several runs share, each leaves its
-// unnormalized sum, maximum and sum of weights in the workspace (a run has two such at most), and a second
-// kernel joins them in a fixed order.
+// another's.  The part of a run in one head is a piece.  Pieces that are whole heads go out at once; of a head
+// that several runs share, each leaves its unnormalized sum, maximum and sum of weights in the
+// workspace (a run has two such at most), and a second kernel joins them in a fixed order.
 //
-// Within a run, each of four wavefronts takes 32 keys of a block, through a ring of its own in LDS that is
-// filled two blocks ahead, so there is no barrier in the loop.  As for prompts everything is transposed:
+// Within a run, each of four wavefronts takes 32 keys of a block, through a ring of two slots of its own in
+// LDS: the next block's loads (the next piece's first ones, too) are in flight while the present one is
+// multiplied, and the loop has no barrier.  As for prompts everything is transposed:
 // S^T = K Q^T with the key head's queries as 16 columns, O^T += V^T P^T in the order of keys in which the
 // scores came out, V^T by transposing reads.  8-bit rows are widened exactly; their scales go to the scores
-// (keys) and to the weights (values).
+// (keys) and to the weights (values).  The weights are multiplied as the sum of two 16-bit numbers, which
+// costs eight products where there is time for them.
 #include "kq_attn.hpp"
 #include "kq_launch.hpp"
 
@@ -43,19 +45,35 @@ __device__ __forceinline__ int wave_isum(int v) {
   return v;
 }
 
-// Blocks of all sequences (one head's).
-__device__ int all_blocks(const Pages& c) {
-  int n = 0;
-  for (int b = threadIdx.x & 63; b < c.B; b += 64) n += lane_blocks_of(c, b);
-  return __builtin_amdgcn_readfirstlane(wave_isum(n));
-}
+// Block x of N belongs to run ((x + 1) W - 1) / N.
+__device__ __forceinline__ int64_t run_start(int64_t w, int64_t N, int W) { return w * N / W; }
 
-// The sequence that holds block y of them all, and the blocks before that sequence.
-__device__ int find_sequence(const Pages& c, int y, int& before) {
+// A piece: blocks j0 .. j1 - 1 of the nb of one unit (a key head, or 16 of its queries where there are more) of
+// sequence b, of len keys.
+struct Piece {
+  int b, unit, j0, j1, nb, len;
+};
+
+// What the joining kernel has to know of a run: its first piece, and the blocks of the whole batch.
+struct Run {
+  int64_t N;
+  int32_t b, unit, j0, nb, pad[2];
+};
+
+// The run's first piece and its number of blocks (0: none); N and W (no run is to be empty) for all runs.
+__device__ int64_t find_run(const Pages& c, int HH, int w, int& W, int64_t& N, Piece& p) {
   const int lane = threadIdx.x & 63;
+  const int n0 = lane < c.B ? lane_blocks_of(c, lane) : 0;
+  int all = n0;
+  for (int b = 64 + lane; b < c.B; b += 64) all += lane_blocks_of(c, b);
+  N = (int64_t)__builtin_amdgcn_readfirstlane(wave_isum(all)) * HH;
+  W = (int)min((int64_t)W, N);
+  if (w >= W) return 0;
+  const int64_t x = run_start(w, N, W);
+  const int y = (int)(x / HH);                               // the block, counting one unit of each sequence
   int base = 0;
   for (int b0 = 0; b0 < c.B; b0 += 64) {
-    const int n = b0 + lane < c.B ? lane_blocks_of(c, b0 + lane) : 0;
+    const int n = b0 == 0 ? n0 : b0 + lane < c.B ? lane_blocks_of(c, b0 + lane) : 0;
     int upto = n;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -65,18 +83,20 @@ __device__ int find_sequence(const Pages& c, int y, int& before) {
     const uint64_t hit = __ballot(y < base + upto);
     if (hit) {
       const int i = __builtin_ctzll(hit);
-      before = __builtin_amdgcn_readfirstlane(base + __shfl(upto - n, i, 64));
-      return b0 + i;
+      p.b = b0 + i;
+      p.nb = __builtin_amdgcn_readlane(n, i);
+      const int64_t in = x - (int64_t)(base + __builtin_amdgcn_readlane(upto, i) - p.nb) * HH;
+      p.unit = (int)(in / p.nb);
+      p.j0 = (int)(in % p.nb);
+      const int64_t blocks = run_start(w + 1, N, W) - x;
+      p.j1 = (int)min((int64_t)p.nb, p.j0 + blocks);
+      p.len = length_of(c, p.b);
+      return blocks;
     }
-    base += __builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64));
+    base += __builtin_amdgcn_readlane(upto, 63);
   }
-  before = base;
-  return c.B;
+  return 0;
 }
-
-// What the runs share of a head's keys.  Block x of them all belongs to run ((x + 1) W - 1) / N.
-__device__ __forceinline__ int run_of(int64_t x, int64_t N, int W) { return (int)(((x + 1) * W - 1) / N); }
-__device__ __forceinline__ int64_t run_start(int64_t w, int64_t N, int W) { return w * N / W; }
 
 __device__ __forceinline__ float row_pair_max(float v) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -147,37 +167,43 @@ __device__ __forceinline__ void store_row(const float* o, const PagedArgs& a, in
 // Floats of a partial result: 16 heads' sums, then their maxima and their sums of weights.
 template <int DP> constexpr int PART = 16 * DP + 32;
 
-// BF16: of queries and outputs.  WIDE: 16-bit rows of that type, else E4M3.  DP: D rounded up.
-template <bool BF16, bool WIDE, int DP, int S>
-__global__ __launch_bounds__(64 * NW) void paged_kernel(PagedArgs a, int W) {
+// A row of rows that has no page.
+constexpr uint32_t NOWHERE = 0xFFFFFFFFu;
+
+// BF16: of queries and outputs.  WIDE: 16-bit rows of that type, else E4M3.  DP: D rounded up.  RES: workgroups
+// on a compute unit.
+template <bool BF16, bool WIDE, int DP, int RES>
+__global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W) {
   constexpr int PITCH = WIDE ? 2 * DP : DP;                  // bytes of a row in LDS
   constexpr int CH = PITCH / 16;                             // its 16-byte chunks
   constexpr int LOADS = 16 * PITCH / 1024;                   // of 16 rows
-  constexpr int SLOT = 64 * PITCH + (WIDE ? 0 : 64);         // 32 keys, 32 values, scales
-  constexpr int NV = 4 * LOADS + (WIDE ? 0 : 1);             // vector loads of a step
+  constexpr int SLOT = 64 * PITCH + (WIDE ? 0 : 128);        // 32 keys, 32 values, scales
+  constexpr int NV = 4 * LOADS + (WIDE ? 0 : 1);             // vector loads of a block
   constexpr int KS = DP / 32, DT = DP / 16;
-  constexpr int RING = S * SLOT;
-  constexpr int LIFT = BF16 || !WIDE ? 0 : 6;                // fp16 weights are held 2^6 larger: see below
-  constexpr bool SPLIT = !WIDE && !BF16;                     // weights as two bf16 numbers
-  constexpr int LDS = NW * RING > NW * 4 * PART<DP> ? NW * RING : NW * 4 * PART<DP>;
-  __shared__ __align__(1024) uint8_t lds[LDS];
+  constexpr int RING = 2 * SLOT;
+  constexpr bool PB = BF16 || !WIDE;                         // the weights' 16-bit type
+  static_assert(PART<DP> * 4 <= SLOT, "a slot takes a wavefront's results");
+  __shared__ __align__(1024) uint8_t lds[NW * RING];
   const Pages& c = a.c;
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int G = a.Hq / c.Hkv, HC = (G + 15) / 16, HH = c.Hkv * HC;
   const int RB = WIDE ? 2 * c.D : c.D;                       // bytes of a row
-  const int64_t N = (int64_t)all_blocks(c) * HH;
-  W = (int)min((int64_t)W, N);                               // no run is empty
   const int w = blockIdx.x;
-  if (w >= W) return;
-  int64_t x = run_start(w, N, W);
-  const int64_t end = run_start(w + 1, N, W);
+  Run* const runs = reinterpret_cast<Run*>(a.part + (int64_t)2 * W * PART<DP>);
 
-  int before;
-  int b = find_sequence(c, (int)(x / HH), before);
-  if (b >= c.B) return;
-  int nb = blocks_of(c, b);
-  int unit = (int)((x - (int64_t)before * HH) / nb), j0 = (int)((x - (int64_t)before * HH) % nb);
+  // sequences of no keys: zeros
+  for (int b = w; b < c.B; b += gridDim.x)
+    if (length_of(c, b) == 0) {
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int h = threadIdx.x >> 4; h < a.Hq; h += 4 * NW) store_row<BF16>(zero, a, b, h, threadIdx.x & 15);
+    }
+
+  int64_t N;
+  Piece p;
+  int64_t left = find_run(c, HH, w, W, N, p);
+  if (threadIdx.x == 0) runs[w] = left > 0 ? Run{N, p.b, p.unit, p.j0, p.nb, {0, 0}} : Run{N, 0, 0, 0, 0, {0, 0}};
+  if (left == 0) return;
 
   auto swizzle_k = [](int row) { return PITCH == 256 ? row & 15 : PITCH == 128 ? (row >> 1) & 7 : (row >> 2) & 3; };
   auto swizzle_v = [](int row) {
@@ -196,89 +222,113 @@ __global__ __launch_bounds__(64 * NW) void paged_kernel(PagedArgs a, int W) {
   const uint32_t ring0 = lds_addr(lds) + wid * RING;
   const uint8_t* const ring = lds + wid * RING;
 
+  // Where the cache has the wavefront's keys of 32 blocks from j on: lane i has the sixteenth of the row of key
+  // 16 (i % 2) of block j + i / 2 (pages are multiples of 16 rows).
+  auto rows_of = [&](const Piece& p, int j) {
+    const int64_t key = (int64_t)BLOCK * (j + (lane >> 1)) + 32 * wid + 16 * (lane & 1);
+    uint32_t at = NOWHERE;
+    if (key < p.len && j + (lane >> 1) < p.j1) {
+      const int k = (int)key, page = c.table[(int64_t)p.b * c.width + k / c.page];
+      if (page >= 0 && page < c.pages)
+        at = (uint32_t)((((int64_t)page * c.Hkv + p.unit / HC) * c.page + k % c.page) >> 4);
+    }
+    return at;
+  };
+  // the wavefront's 32 keys of block j; n: how many of each 16 there are
+  auto load = [&](int slot, const Piece& p, int j, uint32_t rows, int first, int (&n)[2]) {
+    const uint32_t at = ring0 + slot * SLOT;
+    int64_t row[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t r16 = __builtin_amdgcn_readlane(rows, 2 * (j - first) + s);
+      n[s] = r16 == NOWHERE ? 0 : min(16, p.len - (BLOCK * j + 32 * wid + 16 * s));
+      row[s] = r16 == NOWHERE ? 0 : (int64_t)r16 * 16;
+      const v4i rk = rsrc_words(c.k + row[s] * RB, (int64_t)n[s] * RB), rv = rsrc_words(c.v + row[s] * RB, (int64_t)n[s] * RB);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) lds_load16(rk, at + 16 * PITCH * s + 1024 * i, vk[i]);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) lds_load16(rv, at + 16 * PITCH * (2 + s) + 1024 * i, vv[i]);
+    }
+    if constexpr (!WIDE) {
+      if (lane < 4) lds_load16_at(at + 64 * PITCH, (lane < 2 ? c.ks : c.vs) + ((lane & 1) ? row[1] : row[0]));
+    }
+  };
+  // queries: this lane's column is head r of the unit; 8-bit rows give a lane 16 codes at a time, which are two
+  // products' worth
+  auto queries = [&](const Piece& p, v4u (&q)[KS]) {
+    const int h0 = 16 * (p.unit % HC);
+    const uint8_t* const at = a.q + p.b * a.qs + (int64_t)(p.unit / HC * G + h0 + r) * a.qh;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const int d = WIDE ? 32 * i + 8 * g : 64 * (i / 2) + 16 * g + 8 * (i % 2);
+      q[i] = v4u{0, 0, 0, 0};
+      if (h0 + r < G && d < c.D) q[i] = *reinterpret_cast<const v4u*>(at + 2 * d);
+    }
+  };
+
+  uint32_t rows = rows_of(p, p.j0), rows2 = 0;
+  int first = p.j0;
+  v4u q[KS], q2[KS];
+  queries(p, q);
+  int n[2], n2[2], slot = 0;
+  load(0, p, p.j0, rows, first, n);
   bool first_piece = true;
-  while (x < end) {
-    const int len = length_of(c, b);
-    const int h = unit / HC, hc = unit % HC;
-    const int j1 = (int)min((int64_t)nb, j0 + (end - x));
-    const int heads = min(16, G - 16 * hc), head0 = h * G + 16 * hc;
-
-    // page of 16 keys from key0 on, and how many of them there are
-    auto page_of = [&](int key0, int& n) {
-      n = max(0, min(16, len - key0));
-      int64_t p = 0;
-      if (n > 0) {
-        p = scalar_at(c.table, (int64_t)b * c.width + key0 / c.page);
-        if (p < 0 || p >= c.pages) n = 0, p = 0;
+  for (;;) {
+    // the piece after this one, and what its first block needs
+    Piece p2 = p;
+    left -= p.j1 - p.j0;
+    if (left > 0) {
+      p2.j0 = 0;
+      if (++p2.unit == HH) {
+        p2.unit = 0;
+        do {
+          if (++p2.b >= c.B) return;
+          p2.len = length_of(c, p2.b);
+          p2.nb = blocks_in(p2.len);
+        } while (p2.nb == 0);
       }
-      return (p * c.Hkv + h) * c.page + (n > 0 ? key0 % c.page : 0);         // row in the cache
-    };
-    auto load = [&](int slot, int j) {                       // block j's 32 keys of this wavefront
-      const int key = j < j1 ? BLOCK * j + 32 * wid : len;
-      const uint32_t at = ring0 + slot * SLOT;
-      int64_t row[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        int n;
-        row[s] = page_of(key + 16 * s, n);
-        const v4i rk = rsrc_words(c.k + row[s] * RB, (int64_t)n * RB), rv = rsrc_words(c.v + row[s] * RB, (int64_t)n * RB);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) lds_load16(rk, at + 16 * PITCH * s + 1024 * i, vk[i]);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) lds_load16(rv, at + 16 * PITCH * (2 + s) + 1024 * i, vv[i]);
-      }
-      if constexpr (!WIDE) {
-        if (lane < 4) lds_load16_at(at + 64 * PITCH, (lane < 2 ? c.ks : c.vs) + ((lane & 1) ? row[1] : row[0]));
-      }
-    };
-
-    // queries: this lane's column is head r of the unit
-    v4u q[KS];
-    {
-      const __amdgpu_buffer_rsrc_t rq =
-          make_rsrc(a.q + b * a.qs + head0 * a.qh, (heads - 1) * a.qh + 2 * c.D);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        // 8-bit rows give a lane 16 codes at a time, which are two products' worth
-        const int d = WIDE ? 32 * i + 8 * g : 64 * (i / 2) + 16 * g + 8 * (i % 2);
-        q[i] = __builtin_bit_cast(
-            v4u, __builtin_amdgcn_raw_buffer_load_b128(rq, r < heads && d < c.D ? r * (int)a.qh + 2 * d : KQ_OOB, 0, 0));
-      }
-#pragma unroll
-      for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i]));
+      p2.j1 = (int)min((int64_t)p2.nb, left);
+      rows2 = rows_of(p2, 0);
+      queries(p2, q2);
     }
     v4f acc[DT];
 #pragma unroll
     for (int i = 0; i < DT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.0f;
-
-    int slot = 0;
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) load(i, j0 + i);
-    for (int j = j0; j < j1; ++j) {
+    for (int j = p.j0; j < p.j1; ++j) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the slot that is filled next has been read
-      load(slot == 0 ? S - 1 : slot - 1, j + S - 1);
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm((S - 1) * NV));
+      if (j + 1 < p.j1) {
+        if (j + 1 == first + 32) first = j + 1, rows = rows_of(p, first);
+        load(slot ^ 1, p, j + 1, rows, first, n2);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(NV));
+      } else if (left > 0) {
+        load(slot ^ 1, p2, 0, rows2, 0, n2);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(NV));
+      } else {
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      }
       asm volatile("" ::: "memory");
       const uint8_t* const sk = ring + slot * SLOT;
       const uint8_t* const sv = sk + 32 * PITCH;
       v4f t[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        t[s] = v4f{0.f, 0.f, 0.f, 0.f};
-        const uint8_t* const row = sk + PITCH * (16 * s + r);
-        if constexpr (WIDE) {
+      for (int s = 0; s < 2; ++s) t[s] = v4f{0.f, 0.f, 0.f, 0.f};
+      if constexpr (WIDE) {
 #pragma unroll
-          for (int i = 0; i < KS; ++i)
-            t[s] = mfma16<BF16>(*reinterpret_cast<const v4u*>(row + 16 * ((4 * i + g) ^ swizzle_k(r))), q[i], t[s]);
-        } else {
+        for (int i = 0; i < KS; ++i)
 #pragma unroll
-          for (int i = 0; i < KS / 2; ++i) {
-            const v4u w16 = *reinterpret_cast<const v4u*>(row + 16 * ((4 * i + g) ^ swizzle_k(r)));
-            t[s] = mfma16<BF16>(widen8<BF16>(w16[0], w16[1]), q[2 * i], t[s]);
-            t[s] = mfma16<BF16>(widen8<BF16>(w16[2], w16[3]), q[2 * i + 1], t[s]);
+          for (int s = 0; s < 2; ++s)
+            t[s] = mfma16<BF16>(
+                *reinterpret_cast<const v4u*>(sk + PITCH * (16 * s + r) + 16 * ((4 * i + g) ^ swizzle_k(r))), q[i], t[s]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const v4u k16 = *reinterpret_cast<const v4u*>(sk + PITCH * (16 * s + r) + 16 * ((4 * i + g) ^ swizzle_k(r)));
+            t[s] = mfma16<BF16>(widen8<BF16>(k16[0], k16[1]), q[2 * i], t[s]);
+            t[s] = mfma16<BF16>(widen8<BF16>(k16[2], k16[3]), q[2 * i + 1], t[s]);
           }
-        }
       }
       float vscale[8];
       if constexpr (!WIDE) {
@@ -293,14 +343,10 @@ __global__ __launch_bounds__(64 * NW) void paged_kernel(PagedArgs a, int W) {
           }
         }
       }
-      const int key = BLOCK * j + 32 * wid;
-      int n0, n1;
-      page_of(key, n0);
-      page_of(key + 16, n1);
-      if (n0 + n1 < 32) {
+      if (n[0] + n[1] < 32) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const bool seen = 4 * g + (e & 3) < (e < 4 ? n0 : n1);
+          const bool seen = 4 * g + (e & 3) < (e < 4 ? n[0] : n[1]);
           t[e / 4][e & 3] = seen ? t[e / 4][e & 3] : -INFINITY;
           if constexpr (!WIDE) vscale[e] = seen ? vscale[e] : 0.0f;
         }
@@ -319,21 +365,22 @@ __global__ __launch_bounds__(64 * NW) void paged_kernel(PagedArgs a, int W) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][e] *= f;
       }
-      const float base = (m == -INFINITY ? 0.0f : m) - LIFT;
-      float p[8];
+      const float base = m == -INFINITY ? 0.0f : m;
+      float pr[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(fmaf(t[e / 4][e & 3], a.scale, -base));
-        l += p[e];
-        if constexpr (!WIDE) p[e] *= vscale[e];
+        pr[e] = __builtin_amdgcn_exp2f(fmaf(t[e / 4][e & 3], a.scale, -base));
+        l += pr[e];
+        if constexpr (!WIDE) pr[e] *= vscale[e];
       }
-      constexpr bool PB = BF16 || !WIDE;                     // the weights' 16-bit type
-      v4u pw, pl;
+      // a weight is hi + lo, each of 16 bits: relative error 2^-16 (bf16), 2^-22 (fp16, at most 2^8; below
+      // 2^-14 an absolute one of 2^-25)
+      v4u hi, lo;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        pw[e] = pack2_16<PB>(p[2 * e], p[2 * e + 1]);
-        if constexpr (SPLIT)
-          pl[e] = pack2_16<true>(p[2 * e] - __uint_as_float(pw[e] << 16), p[2 * e + 1] - __uint_as_float(pw[e] & 0xFFFF0000u));
+        hi[e] = pack2_16<PB>(pr[2 * e], pr[2 * e + 1]);
+        const uint32_t h = hi[e];
+        lo[e] = pack2_16<PB>(pr[2 * e] - unpack1_16<PB>((uint16_t)h), pr[2 * e + 1] - unpack1_16<PB>((uint16_t)(h >> 16)));
       }
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
@@ -341,53 +388,57 @@ __global__ __launch_bounds__(64 * NW) void paged_kernel(PagedArgs a, int W) {
         if constexpr (WIDE) {
           const int row = 4 * g + (r >> 2);
           const uint8_t* const at = sv + PITCH * row + 16 * ((2 * i + ((r & 3) >> 1)) ^ swizzle_v(row)) + 8 * (r & 1);
-          const v2u lo = lds_tr16(at), hi = lds_tr16(at + 16 * PITCH);
-          v = v4u{lo[0], lo[1], hi[0], hi[1]};
+          const v2u v0 = lds_tr16(at), v1 = lds_tr16(at + 16 * PITCH);
+          v = v4u{v0[0], v0[1], v1[0], v1[1]};
         } else {
           const int k = r >> 1, row = 4 * g + (k & 3) + 16 * (k >> 2);
           const v2u w8 = lds_tr8(sv + PITCH * row + 16 * (i ^ swizzle_v(row)) + 8 * (r & 1));
           v = widen8<true>(w8[0], w8[1]);
         }
-        acc[i] = mfma16<PB>(v, pw, acc[i]);
-        if constexpr (SPLIT) acc[i] = mfma16<true>(v, pl, acc[i]);
+        acc[i] = mfma16<PB>(v, lo, mfma16<PB>(v, hi, acc[i]));
       }
-      slot = slot == S - 1 ? 0 : slot + 1;
+      slot ^= 1;
+      n[0] = n2[0], n[1] = n2[1];
     }
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    // the wavefronts' results meet in the slots that were read last; the others are being filled
+    const int done = slot ^ 1;
     l = half_sum(row_pair_sum(l));
-    __syncthreads();                                         // all rings have been read
     {
-      float* const o = reinterpret_cast<float*>(lds) + wid * PART<DP>;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      float* const o = reinterpret_cast<float*>(lds + wid * RING + done * SLOT);
 #pragma unroll
       for (int i = 0; i < DT; ++i) *reinterpret_cast<v4f*>(o + DP * r + 16 * i + 4 * g) = acc[i];
       if (g == 0) o[16 * DP + r] = m, o[16 * DP + 16 + r] = l;
     }
-    __syncthreads();
+    lds_barrier();
     {
       // thread: head threadIdx / 16, values 8 i .. + 7
       const int hd = threadIdx.x >> 4, i = threadIdx.x & 15;
-      const float* const o = reinterpret_cast<const float*>(lds);
+      const float* o[NW];
       float top = -INFINITY, total = 0.0f, sum[8];
 #pragma unroll
-      for (int u = 0; u < NW; ++u) top = fmaxf(top, o[u * PART<DP> + 16 * DP + hd]);
+      for (int u = 0; u < NW; ++u) {
+        o[u] = reinterpret_cast<const float*>(lds + u * RING + done * SLOT);
+        top = fmaxf(top, o[u][16 * DP + hd]);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
 #pragma unroll
       for (int u = 0; u < NW; ++u) {
-        const float mu = o[u * PART<DP> + 16 * DP + hd];
+        const float mu = o[u][16 * DP + hd];
         const float f = mu == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mu - top);
-        total = fmaf(f, o[u * PART<DP> + 16 * DP + 16 + hd], total);
+        total = fmaf(f, o[u][16 * DP + 16 + hd], total);
         if (8 * i < DP) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, o[u * PART<DP> + DP * hd + 8 * i + e], sum[e]);
+          for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, o[u][DP * hd + 8 * i + e], sum[e]);
         }
       }
-      if (hd < heads) {
-        if (j0 == 0 && j1 == nb) {
+      if (16 * (p.unit % HC) + hd < G) {
+        if (p.j0 == 0 && p.j1 == p.nb) {
           const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum[e] *= inv;
-          store_row<BF16>(sum, a, b, head0 + hd, i);
+          store_row<BF16>(sum, a, p.b, p.unit / HC * G + 16 * (p.unit % HC) + hd, i);
         } else {
           float* const part = a.part + (int64_t)(2 * w + (first_piece ? 0 : 1)) * PART<DP>;
           if (8 * i < DP) {
@@ -399,54 +450,48 @@ __global__ __launch_bounds__(64 * NW) void paged_kernel(PagedArgs a, int W) {
         }
       }
     }
-    __syncthreads();
+    if (left == 0) return;
+    lds_barrier();                                           // before the slots are filled again
     first_piece = false;
-    x += j1 - j0;
-    j0 = 0;
-    if (x < end && ++unit == HH) {
-      unit = 0;
-      do {
-        if (++b >= c.B) return;
-        nb = blocks_of(c, b);
-      } while (nb == 0);
-    }
+    p = p2;
+    rows = rows2;
+    first = 0;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) q[i] = q2[i];
   }
 }
 
-// Joins what the runs left of heads they share, and writes zeros where a sequence has no keys.  One
-// workgroup per sequence and query head; its 16 rows of 16 threads take the runs in turn.
+// Joins what the runs left of units they share: one workgroup for each run that begins inside a unit (the first of
+// those in it) and each of the unit's heads; its 16 rows of 16 threads take the unit's runs in turn.
 template <bool BF16, int DP>
-__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W) {
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int heads) {
   __shared__ float so[16][DP + 2];
   const Pages& c = a.c;
-  const int head = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
-  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16, HH = c.Hkv * HC;
-  const int unit = head / G * HC + head % G / 16, hd = head % G % 16;
-  const int nb = blocks_of(c, b);
+  const int w = blockIdx.x / heads + 1, hd = blockIdx.x % heads;
+  const Run* const runs = reinterpret_cast<const Run*>(a.part + (int64_t)2 * W * PART<DP>);
+  const int64_t N = runs[0].N;
+  const Run u = runs[w];
+  W = (int)min((int64_t)W, N);
+  if (w >= W || u.j0 == 0) return;
+  const int64_t x0 = run_start(w, N, W) - u.j0;              // the unit's first block
+  if (run_start(w - 1, N, W) > x0) return;                   // the run before began inside it, too
+  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16;
+  if (16 * (u.unit % HC) + hd >= G) return;
+  const int head = u.unit / HC * G + 16 * (u.unit % HC) + hd;
   const int k = threadIdx.x >> 4, i = threadIdx.x & 15;
-  float sum[8];
+  float sum[8], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-  if (nb == 0) {
-    if (k == 0) store_row<BF16>(sum, a, b, head, i);
-    return;
-  }
-  int before = 0;
-  for (int s = threadIdx.x & 63; s < b; s += 64) before += lane_blocks_of(c, s);
-  before = __builtin_amdgcn_readfirstlane(wave_isum(before));
-  const int64_t N = (int64_t)all_blocks(c) * HH, x0 = (int64_t)before * HH + (int64_t)unit * nb;
-  W = (int)min((int64_t)W, N);
-  const int w0 = run_of(x0, N, W), w1 = run_of(x0 + nb - 1, N, W);
-  if (w0 == w1) return;                                      // a run has written it
-  float m = -INFINITY, l = 0.0f;
-  for (int w = w0 + k; w <= w1; w += 16) {
-    const float* const part = a.part + (int64_t)(2 * w + (w == w0 && run_start(w, N, W) != x0 ? 1 : 0)) * PART<DP>;
-    const float mw = part[16 * DP + hd], lw = part[16 * DP + 16 + hd];
-    const float to = fmaxf(m, mw);
+  for (int v = w - 1 + k; v < W; v += 16) {
+    const int64_t start = run_start(v, N, W);
+    if (start >= x0 + u.nb) break;
+    const float* const part = a.part + (int64_t)(2 * v + (start < x0 ? 1 : 0)) * PART<DP>;
+    const float mv = part[16 * DP + hd], lv = part[16 * DP + 16 + hd];
+    const float to = fmaxf(m, mv);
     const float f0 = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-    const float f1 = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw - to);
+    const float f1 = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mv - to);
     m = to;
-    l = fmaf(l, f0, f1 * lw);
+    l = fmaf(l, f0, f1 * lv);
     if (8 * i < DP) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] = fmaf(sum[e], f0, f1 * part[DP * hd + 8 * i + e]);
@@ -475,7 +520,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W) {
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] *= inv;
-  store_row<BF16>(sum, a, b, head, i);
+  store_row<BF16>(sum, a, u.b, head, i);
 }
 
 // One wavefront a token: its sequence, position and page, then the rows of its heads, four at a time, 16
@@ -536,29 +581,36 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   }
 }
 
+// Workgroups on a compute unit, by their rings in LDS.
+constexpr int resident(bool wide, int DP) { return wide ? (DP == 128 ? 1 : 2) : (DP == 128 ? 2 : 4); }
+
 // Runs of a call: one for each workgroup that the compute units hold, and no more than blocks.
-int64_t runs(int64_t B, int Hq, int Hkv, int64_t longest) {
+int64_t runs(int64_t B, int Hq, int Hkv, int64_t longest, int res) {
   const int G = Hq / Hkv, HC = (G + 15) / 16;
   const int64_t blocks = B * Hkv * HC * ((longest + BLOCK - 1) / BLOCK);
-  const int64_t most = device_cu_count();
+  const int64_t most = (int64_t)device_cu_count() * res;
   return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 
 template <bool BF16, bool WIDE, int DP>
 hipError_t go(const PagedArgs& a, hipStream_t s) {
-  constexpr int S = WIDE ? (DP == 128 ? 2 : 4) : (DP == 128 ? 4 : 8);
-  const int W = (int)runs(a.c.B, a.Hq, a.c.Hkv, (int64_t)a.c.width * a.c.page);
-  hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, S>), dim3(W), dim3(64 * NW), 0, s, a, W);
+  constexpr int RES = resident(WIDE, DP);
+  const int W = (int)runs(a.c.B, a.Hq, a.c.Hkv, (int64_t)a.c.width * a.c.page, RES);
+  hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, RES>), dim3(W), dim3(64 * NW), 0, s, a, W);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((paged_join_kernel<BF16, DP>), dim3((unsigned)(a.c.B * a.Hq)), dim3(256), 0, s, a, W);
+  if (e != hipSuccess || W == 1) return e;
+  const int G = a.Hq / a.c.Hkv, heads = G < 16 ? G : 16;
+  hipLaunchKernelGGL((paged_join_kernel<BF16, DP>), dim3((unsigned)((W - 1) * heads)), dim3(256), 0, s, a, W, heads);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// For both kinds of cache: 8-bit rings are smaller, so there are more runs.
 size_t paged_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int64_t longest) {
-  return (size_t)(2 * runs(B, Hq, Hkv, longest)) * (D <= 64 ? PART<64> : PART<128>) * 4;
+  const int DP = D <= 64 ? 64 : 128;
+  const int64_t part = DP == 64 ? PART<64> : PART<128>;
+  return (size_t)runs(B, Hq, Hkv, longest, resident(false, DP)) * (2 * part * sizeof(float) + sizeof(Run));
 }
 
 hipError_t launch_paged_attention(bool bf16, bool wide, const PagedArgs& a, hipStream_t s) {
