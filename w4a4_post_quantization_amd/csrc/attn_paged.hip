@@ -21,13 +21,13 @@ namespace kq {
 
 namespace {
 
-constexpr int NW = 4, BLOCK = 32 * NW;
-
 // Lengths are held to what the table's rows can hold.
 __device__ __forceinline__ int held(const Pages& c, int32_t len) {
   return (int)min((int64_t)max(len, 0), (int64_t)c.width * c.page);
 }
-__device__ __forceinline__ int blocks_in(int len) { return (int)(((int64_t)len + BLOCK - 1) / BLOCK); }
+// Blocks of a sequence: 32 keys for each of a workgroup's NW wavefronts.
+template <int NW>
+__device__ __forceinline__ int blocks_in(int len) { return (int)(((int64_t)len + 32 * NW - 1) / (32 * NW)); }
 
 // An entry at an index that the whole wavefront shares, as a scalar load: a vector load would have to be
 // waited for together with the rings'.
@@ -35,14 +35,17 @@ __device__ __forceinline__ int32_t scalar_at(const int32_t* p, int64_t i) {
   return ((const __attribute__((address_space(4))) int32_t*)p)[i];
 }
 __device__ __forceinline__ int length_of(const Pages& c, int b) { return held(c, scalar_at(c.lengths, b)); }
-__device__ __forceinline__ int blocks_of(const Pages& c, int b) { return blocks_in(length_of(c, b)); }
-__device__ __forceinline__ int lane_blocks_of(const Pages& c, int b) { return blocks_in(held(c, c.lengths[b])); }
 
-// Sum over a wavefront, the same in each lane.
-__device__ __forceinline__ int wave_isum(int v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+// Sums over the lanes up to each one.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+  // within rows of 16 by shifts, then the rows' totals
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);      // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  const int t0 = __builtin_amdgcn_readlane(v, 15), t1 = __builtin_amdgcn_readlane(v, 31), t2 = __builtin_amdgcn_readlane(v, 47);
+  return v + (lane >= 16 ? t0 : 0) + (lane >= 32 ? t1 : 0) + (lane >= 48 ? t2 : 0);
 }
 
 // Block x of N belongs to run ((x + 1) W - 1) / N.
@@ -61,36 +64,38 @@ struct Run {
 };
 
 // The run's first piece and its number of blocks (0: none); N and W (no run is to be empty) for all runs.
+template <int NW>
 __device__ int64_t find_run(const Pages& c, int HH, int w, int& W, int64_t& N, Piece& p) {
   const int lane = threadIdx.x & 63;
-  const int n0 = lane < c.B ? lane_blocks_of(c, lane) : 0;
-  int all = n0;
-  for (int b = 64 + lane; b < c.B; b += 64) all += lane_blocks_of(c, b);
-  N = (int64_t)__builtin_amdgcn_readfirstlane(wave_isum(all)) * HH;
+  auto length = [&](int b) { return b < c.B ? held(c, c.lengths[b]) : 0; };
+  // up to 64 sequences: the scan that the search needs has the sum, too
+  const int len0 = length(lane), n0 = blocks_in<NW>(len0), upto0 = wave_scan(n0);
+  int all = __builtin_amdgcn_readlane(upto0, 63);
+  if (c.B > 64) {
+    int more = 0;
+    for (int b = 64; b < c.B; b += 64) more += blocks_in<NW>(length(b + lane));
+    all += __builtin_amdgcn_readlane(wave_scan(more), 63);
+  }
+  N = (int64_t)all * HH;
   W = (int)min((int64_t)W, N);
   if (w >= W) return 0;
   const int64_t x = run_start(w, N, W);
   const int y = (int)(x / HH);                               // the block, counting one unit of each sequence
   int base = 0;
   for (int b0 = 0; b0 < c.B; b0 += 64) {
-    const int n = b0 == 0 ? n0 : b0 + lane < c.B ? lane_blocks_of(c, b0 + lane) : 0;
-    int upto = n;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(upto, off, 64);
-      upto += lane >= off ? o : 0;
-    }
+    const int len = b0 == 0 ? len0 : length(b0 + lane);
+    const int upto = b0 == 0 ? upto0 : wave_scan(blocks_in<NW>(len));
     const uint64_t hit = __ballot(y < base + upto);
     if (hit) {
       const int i = __builtin_ctzll(hit);
       p.b = b0 + i;
-      p.nb = __builtin_amdgcn_readlane(n, i);
+      p.len = __builtin_amdgcn_readlane(len, i);
+      p.nb = blocks_in<NW>(p.len);
       const int64_t in = x - (int64_t)(base + __builtin_amdgcn_readlane(upto, i) - p.nb) * HH;
       p.unit = (int)(in / p.nb);
       p.j0 = (int)(in % p.nb);
       const int64_t blocks = run_start(w + 1, N, W) - x;
       p.j1 = (int)min((int64_t)p.nb, p.j0 + blocks);
-      p.len = length_of(c, p.b);
       return blocks;
     }
     base += __builtin_amdgcn_readlane(upto, 63);
@@ -172,8 +177,10 @@ constexpr uint32_t NOWHERE = 0xFFFFFFFFu;
 
 // BF16: of queries and outputs.  WIDE: 16-bit rows of that type, else E4M3.  DP: D rounded up.  RES: workgroups
 // on a compute unit.
-template <bool BF16, bool WIDE, int DP, int RES>
+// WHOLE: a run is a unit, without looking at the other sequences' lengths; nothing is left to be joined.
+template <bool BF16, bool WIDE, int DP, int NW, int RES, bool WHOLE>
 __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W) {
+  constexpr int BLK = 32 * NW;                               // keys of a block
   constexpr int PITCH = WIDE ? 2 * DP : DP;                  // bytes of a row in LDS
   constexpr int CH = PITCH / 16;                             // its 16-byte chunks
   constexpr int LOADS = 16 * PITCH / 1024;                   // of 16 rows
@@ -192,18 +199,24 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
   const int w = blockIdx.x;
   Run* const runs = reinterpret_cast<Run*>(a.part + (int64_t)2 * W * PART<DP>);
 
-  // sequences of no keys: zeros
-  for (int b = w; b < c.B; b += gridDim.x)
-    if (length_of(c, b) == 0) {
-      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int h = threadIdx.x >> 4; h < a.Hq; h += 4 * NW) store_row<BF16>(zero, a, b, h, threadIdx.x & 15);
-    }
-
-  int64_t N;
   Piece p;
-  int64_t left = find_run(c, HH, w, W, N, p);
-  if (threadIdx.x == 0) runs[w] = left > 0 ? Run{N, p.b, p.unit, p.j0, p.nb, {0, 0}} : Run{N, 0, 0, 0, 0, {0, 0}};
-  if (left == 0) return;
+  int64_t left;
+  if (WHOLE) {
+    p.b = w / HH, p.unit = w % HH, p.j0 = 0;
+    p.len = length_of(c, p.b);
+    left = p.j1 = p.nb = blocks_in<NW>(p.len);
+    if (left == 0) {                                         // no keys: zeros
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int i = 16 * (p.unit % HC) + (threadIdx.x >> 4); i < min(G, 16 * (p.unit % HC + 1)); i += 4 * NW)
+        store_row<BF16>(zero, a, p.b, p.unit / HC * G + i, threadIdx.x & 15);
+      return;
+    }
+  } else {
+    int64_t N;
+    left = find_run<NW>(c, HH, w, W, N, p);
+    if (threadIdx.x == 0) runs[w] = left > 0 ? Run{N, p.b, p.unit, p.j0, p.nb, {0, 0}} : Run{N, 0, 0, 0, 0, {0, 0}};
+    if (left == 0) return;
+  }
 
   auto swizzle_k = [](int row) { return PITCH == 256 ? row & 15 : PITCH == 128 ? (row >> 1) & 7 : (row >> 2) & 3; };
   auto swizzle_v = [](int row) {
@@ -225,7 +238,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
   // Where the cache has the wavefront's keys of 32 blocks from j on: lane i has the sixteenth of the row of key
   // 16 (i % 2) of block j + i / 2 (pages are multiples of 16 rows).
   auto rows_of = [&](const Piece& p, int j) {
-    const int64_t key = (int64_t)BLOCK * (j + (lane >> 1)) + 32 * wid + 16 * (lane & 1);
+    const int64_t key = (int64_t)BLK * (j + (lane >> 1)) + 32 * wid + 16 * (lane & 1);
     uint32_t at = NOWHERE;
     if (key < p.len && j + (lane >> 1) < p.j1) {
       const int k = (int)key, page = c.table[(int64_t)p.b * c.width + k / c.page];
@@ -241,7 +254,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const uint32_t r16 = __builtin_amdgcn_readlane(rows, 2 * (j - first) + s);
-      n[s] = r16 == NOWHERE ? 0 : min(16, p.len - (BLOCK * j + 32 * wid + 16 * s));
+      n[s] = r16 == NOWHERE ? 0 : min(16, p.len - (BLK * j + 32 * wid + 16 * s));
       row[s] = r16 == NOWHERE ? 0 : (int64_t)r16 * 16;
       const v4i rk = rsrc_words(c.k + row[s] * RB, (int64_t)n[s] * RB), rv = rsrc_words(c.v + row[s] * RB, (int64_t)n[s] * RB);
 #pragma unroll
@@ -284,7 +297,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
         do {
           if (++p2.b >= c.B) return;
           p2.len = length_of(c, p2.b);
-          p2.nb = blocks_in(p2.len);
+          p2.nb = blocks_in<NW>(p2.len);
         } while (p2.nb == 0);
       }
       p2.j1 = (int)min((int64_t)p2.nb, left);
@@ -411,9 +424,9 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
       if (g == 0) o[16 * DP + r] = m, o[16 * DP + 16 + r] = l;
     }
     lds_barrier();
-    {
-      // thread: head threadIdx / 16, values 8 i .. + 7
-      const int hd = threadIdx.x >> 4, i = threadIdx.x & 15;
+    // thread: head threadIdx / 16, values 8 i .. + 7
+    for (int hd = threadIdx.x >> 4; hd < min(16, G - 16 * (p.unit % HC)); hd += 4 * NW) {
+      const int i = threadIdx.x & 15;
       const float* o[NW];
       float top = -INFINITY, total = 0.0f, sum[8];
 #pragma unroll
@@ -433,21 +446,19 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
           for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, o[u][DP * hd + 8 * i + e], sum[e]);
         }
       }
-      if (16 * (p.unit % HC) + hd < G) {
-        if (p.j0 == 0 && p.j1 == p.nb) {
-          const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      if (WHOLE || (p.j0 == 0 && p.j1 == p.nb)) {
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] *= inv;
-          store_row<BF16>(sum, a, p.b, p.unit / HC * G + 16 * (p.unit % HC) + hd, i);
-        } else {
-          float* const part = a.part + (int64_t)(2 * w + (first_piece ? 0 : 1)) * PART<DP>;
-          if (8 * i < DP) {
+        for (int e = 0; e < 8; ++e) sum[e] *= inv;
+        store_row<BF16>(sum, a, p.b, p.unit / HC * G + 16 * (p.unit % HC) + hd, i);
+      } else {
+        float* const part = a.part + (int64_t)(2 * w + (first_piece ? 0 : 1)) * PART<DP>;
+        if (8 * i < DP) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 4)
-              *reinterpret_cast<v4f*>(part + DP * hd + 8 * i + e) = v4f{sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
-          }
-          if (i == 0) part[16 * DP + hd] = top, part[16 * DP + 16 + hd] = total;
+          for (int e = 0; e < 8; e += 4)
+            *reinterpret_cast<v4f*>(part + DP * hd + 8 * i + e) = v4f{sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
         }
+        if (i == 0) part[16 * DP + hd] = top, part[16 * DP + 16 + hd] = total;
       }
     }
     if (left == 0) return;
@@ -461,40 +472,70 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
   }
 }
 
-// Joins what the runs left of units they share: one workgroup for each run that begins inside a unit (the first of
-// those in it) and each of the unit's heads; its 16 rows of 16 threads take the unit's runs in turn.
-template <bool BF16, int DP>
-__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int heads) {
+// Joins what the runs left of units they share: each run that begins inside a unit (the first of those in it) is a
+// workgroup's, for 16 / ROWS of the unit's heads; ROWS rows of 16 threads take the unit's runs in turn for each head, four at
+// a time.  Further workgroups write zeros for the sequences without keys, 64 each.
+template <bool BF16, int DP, int ROWS>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int groups) {
+  constexpr int HEADS = 16 / ROWS, AT = 4;
   __shared__ float so[16][DP + 2];
   const Pages& c = a.c;
-  const int w = blockIdx.x / heads + 1, hd = blockIdx.x % heads;
+  const int k = threadIdx.x >> 4, i = threadIdx.x & 15;
+  float sum[8], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  if (blockIdx.x >= (uint32_t)((W - 1) * groups)) {
+    const int b0 = 64 * (blockIdx.x - (W - 1) * groups), b = b0 + (threadIdx.x & 63);
+    uint64_t none = __ballot(b < c.B && c.lengths[b] <= 0);
+    for (; none; none &= none - 1)
+      for (int h = k; h < a.Hq; h += 16) store_row<BF16>(sum, a, b0 + __builtin_ctzll(none), h, i);
+    return;
+  }
+  const int w = blockIdx.x / groups + 1, hd = blockIdx.x % groups * HEADS + k / ROWS;
   const Run* const runs = reinterpret_cast<const Run*>(a.part + (int64_t)2 * W * PART<DP>);
   const int64_t N = runs[0].N;
   const Run u = runs[w];
   W = (int)min((int64_t)W, N);
   if (w >= W || u.j0 == 0) return;
   const int64_t x0 = run_start(w, N, W) - u.j0;              // the unit's first block
-  if (run_start(w - 1, N, W) > x0) return;                   // the run before began inside it, too
-  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16;
-  if (16 * (u.unit % HC) + hd >= G) return;
-  const int head = u.unit / HC * G + 16 * (u.unit % HC) + hd;
-  const int k = threadIdx.x >> 4, i = threadIdx.x & 15;
-  float sum[8], m = -INFINITY, l = 0.0f;
+  const int64_t before = run_start(w - 1, N, W);
+  if (before > x0) return;                                   // the run before began inside it, too
+  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16, h0 = 16 * (u.unit % HC);
+  // the last run with a block of the unit: ((x + 1) W - 1) / N for its last block x
+  const int last = (int)(((x0 + u.nb) * W - 1) / N);
+  if (hd < min(16, G - h0)) {
+    for (int v0 = w - 1 + k % ROWS; v0 <= last; v0 += ROWS * AT) {
+      float mv[AT], lv[AT];
+      v4f ov[AT][2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-  for (int v = w - 1 + k; v < W; v += 16) {
-    const int64_t start = run_start(v, N, W);
-    if (start >= x0 + u.nb) break;
-    const float* const part = a.part + (int64_t)(2 * v + (start < x0 ? 1 : 0)) * PART<DP>;
-    const float mv = part[16 * DP + hd], lv = part[16 * DP + 16 + hd];
-    const float to = fmaxf(m, mv);
-    const float f0 = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-    const float f1 = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mv - to);
-    m = to;
-    l = fmaf(l, f0, f1 * lv);
-    if (8 * i < DP) {
+      for (int t = 0; t < AT; ++t) {
+        const int v = v0 + ROWS * t;
+        mv[t] = -INFINITY, lv[t] = 0.0f;
+        ov[t][0] = ov[t][1] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (v <= last) {
+          const float* const part = a.part + (int64_t)(2 * v + (v == w - 1 && before < x0 ? 1 : 0)) * PART<DP>;
+          mv[t] = part[16 * DP + hd], lv[t] = part[16 * DP + 16 + hd];
+          if (8 * i < DP) {
+            ov[t][0] = *reinterpret_cast<const v4f*>(part + DP * hd + 8 * i);
+            ov[t][1] = *reinterpret_cast<const v4f*>(part + DP * hd + 8 * i + 4);
+          }
+        }
+      }
+      float to = m;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] = fmaf(sum[e], f0, f1 * part[DP * hd + 8 * i + e]);
+      for (int t = 0; t < AT; ++t) to = fmaxf(to, mv[t]);
+      const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] *= f;
+#pragma unroll
+      for (int t = 0; t < AT; ++t) {
+        const float ft = mv[t] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mv[t] - to);
+        l = fmaf(ft, lv[t], l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = fmaf(ft, ov[t][e / 4][e % 4], sum[e]);
+      }
     }
   }
   if (8 * i < DP) {
@@ -503,24 +544,33 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int
   }
   if (i == 0) so[k][DP] = m, so[k][DP + 1] = l;
   __syncthreads();
-  if (k > 0) return;
+  if (k % ROWS > 0 || hd >= min(16, G - h0)) return;
   float top = -INFINITY, total = 0.0f;
 #pragma unroll
-  for (int u = 0; u < 16; ++u) top = fmaxf(top, so[u][DP]);
+  for (int r = 0; r < ROWS; ++r) top = fmaxf(top, so[k + r][DP]);
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-  for (int u = 0; u < 16; ++u) {
-    const float f = so[u][DP] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(so[u][DP] - top);
-    total = fmaf(f, so[u][DP + 1], total);
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const float f = so[k + r][DP] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(so[k + r][DP] - top);
+    total = fmaf(f, so[k + r][DP + 1], total);
     if (8 * i < DP) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, so[u][8 * i + e], sum[e]);
+      for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, so[k + r][8 * i + e], sum[e]);
     }
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] *= inv;
-  store_row<BF16>(sum, a, u.b, head, i);
+  store_row<BF16>(sum, a, u.b, u.unit / HC * G + h0 + hd, i);
+}
+
+template <bool BF16, int DP, int ROWS>
+hipError_t join(const PagedArgs& a, int W, int heads, hipStream_t s) {
+  const int groups = (heads + 16 / ROWS - 1) / (16 / ROWS);
+  hipLaunchKernelGGL((paged_join_kernel<BF16, DP, ROWS>), dim3((unsigned)((W - 1) * groups + (a.c.B + 63) / 64)), dim3(256), 0, s,
+                     a, W, groups);
+  return hipGetLastError();
 }
 
 // One wavefront a token: its sequence, position and page, then the rows of its heads, four at a time, 16
@@ -581,36 +631,55 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   }
 }
 
-// Workgroups on a compute unit, by their rings in LDS.
-constexpr int resident(bool wide, int DP) { return wide ? (DP == 128 ? 1 : 2) : (DP == 128 ? 2 : 4); }
+// Wavefronts of a workgroup and workgroups on a compute unit, which together fill its LDS with rings.  (Four wavefronts and
+// half as many workgroups wait longer at a piece's end: 37 sequences of 50 to 4000 in 16 bits 70 and 64 us, 160 of 200 to
+// 8000 in 8 bits 261 and 250; one wavefront each leaves more to join, two of 131072 in 8 bits 112 and 107.)
+constexpr int NW = 2;
+constexpr int resident(bool wide, int DP) { return wide && DP == 128 ? 2 : wide || DP == 128 ? 4 : 8; }
 
 // Runs of a call: one for each workgroup that the compute units hold, and no more than blocks.
-int64_t runs(int64_t B, int Hq, int Hkv, int64_t longest, int res) {
-  const int G = Hq / Hkv, HC = (G + 15) / 16;
-  const int64_t blocks = B * Hkv * HC * ((longest + BLOCK - 1) / BLOCK);
-  const int64_t most = (int64_t)device_cu_count() * res;
+int64_t runs(int64_t B, int Hq, int Hkv, int64_t longest, bool wide, int DP) {
+  const int G = Hq / Hkv, HC = (G + 15) / 16, block = 32 * NW;
+  const int64_t blocks = B * Hkv * HC * ((longest + block - 1) / block);
+  const int64_t most = (int64_t)device_cu_count() * resident(wide, DP);
   return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 
+// A unit is one workgroup's, and nothing is joined, where tables hold up to 640 keys, or up to 2048 and there is a unit
+// for every compute unit: 32 / 8 heads of 128, whole and dealt (us): one sequence of 500 9.4 and 9.6, 1000 14 and 9.9; 8 of
+// 1000 16.3 and 15.7; 64 of 0 to 2000 in 8 bits 38 and 44; 300 of 100 in 16 bits 43 and 46; 160 of 200 to 8000 in 8 bits 281 and
+// 250.  Four wavefronts then, so that a unit is sooner done, or two where the units fill the chip (300 of 0 to 1000: 130
+// and 148; 64 of 500 in 8 bits the other way, 21 and 19).
 template <bool BF16, bool WIDE, int DP>
 hipError_t go(const PagedArgs& a, hipStream_t s) {
   constexpr int RES = resident(WIDE, DP);
-  const int W = (int)runs(a.c.B, a.Hq, a.c.Hkv, (int64_t)a.c.width * a.c.page, RES);
-  hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, RES>), dim3(W), dim3(64 * NW), 0, s, a, W);
+  const int64_t longest = (int64_t)a.c.width * a.c.page;
+  const int G = a.Hq / a.c.Hkv, HC = (G + 15) / 16, cus = device_cu_count();
+  const int64_t units = (int64_t)a.c.B * a.c.Hkv * HC;
+  if (longest <= 640 || (longest <= 2048 && units >= cus)) {
+    if (units >= (int64_t)cus * RES)
+      hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, 2, RES, true>), dim3((unsigned)units), dim3(128), 0, s, a, 0);
+    else
+      hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, 4, RES / 2, true>), dim3((unsigned)units), dim3(256), 0, s, a, 0);
+    return hipGetLastError();
+  }
+  const int W = (int)runs(a.c.B, a.Hq, a.c.Hkv, longest, WIDE, DP);
+  hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, NW, RES, false>), dim3(W), dim3(64 * NW), 0, s, a, W);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || W == 1) return e;
-  const int G = a.Hq / a.c.Hkv, heads = G < 16 ? G : 16;
-  hipLaunchKernelGGL((paged_join_kernel<BF16, DP>), dim3((unsigned)((W - 1) * heads)), dim3(256), 0, s, a, W, heads);
-  return hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int heads = G < 16 ? G : 16;
+  // many runs of each unit: 16 at once for a head; else as few workgroups as there can be (1023 joins 10 and 5 us)
+  return W > 16 * units ? join<BF16, DP, 16>(a, W, heads, s) : join<BF16, DP, 4>(a, W, heads, s);
 }
 
 }  // namespace
 
-// For both kinds of cache: 8-bit rings are smaller, so there are more runs.
+// For both kinds of cache.
 size_t paged_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int64_t longest) {
   const int DP = D <= 64 ? 64 : 128;
   const int64_t part = DP == 64 ? PART<64> : PART<128>;
-  return (size_t)runs(B, Hq, Hkv, longest, resident(false, DP)) * (2 * part * sizeof(float) + sizeof(Run));
+  const int64_t a = runs(B, Hq, Hkv, longest, false, DP), b = runs(B, Hq, Hkv, longest, true, DP);
+  return (size_t)(a > b ? a : b) * (2 * part * sizeof(float) + sizeof(Run));
 }
 
 hipError_t launch_paged_attention(bool bf16, bool wide, const PagedArgs& a, hipStream_t s) {
