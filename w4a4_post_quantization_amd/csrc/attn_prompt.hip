@@ -19,6 +19,8 @@
 #include "kq_attn.hpp"
 #include "kq_launch.hpp"
 
+#include <type_traits>
+
 namespace kq {
 
 namespace {
@@ -45,17 +47,23 @@ __device__ bool find_span(const AttnArgs& a, int G, int32_t slot, Span& s) {
   }
   const int lane = threadIdx.x & 63;
   const int32_t T = (int32_t)a.T, Tk = (int32_t)a.Tk;
-  int n = 0;
+  // lane i: sequence i0 + i's four entries, so that the search's loads are the only ones
+  int32_t q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+  int i = 0;
   for (int i0 = 0; i0 < a.B; i0 += 64) {
-    const int i = i0 + lane;
-    const bool before = i < a.B && min(max(a.cu_q[i], 0), T) * G / QT + i <= slot;
+    const int at = min(i0 + lane, a.B - 1);
+    const int32_t lq0 = a.cu_q[at], lq1 = a.cu_q[at + 1], lk0 = a.cu_k[at], lk1 = a.cu_k[at + 1];
+    const bool before = i0 + lane < a.B && min(max(lq0, 0), T) * G / QT + i0 + lane <= slot;
     const int c = __popcll(__ballot(before));
-    n += c;
+    if (c > 0) {
+      i = i0 + c - 1;
+      q0 = __builtin_amdgcn_readlane(lq0, c - 1), q1 = __builtin_amdgcn_readlane(lq1, c - 1);
+      k0 = __builtin_amdgcn_readlane(lk0, c - 1), k1 = __builtin_amdgcn_readlane(lk1, c - 1);
+    }
     if (c < 64) break;
   }
-  const int i = __builtin_amdgcn_readfirstlane(max(n - 1, 0));
-  const int32_t q0 = min(max(a.cu_q[i], 0), T), q1 = min(max(a.cu_q[i + 1], q0), T);
-  const int32_t k0 = min(max(a.cu_k[i], 0), Tk), k1 = min(max(a.cu_k[i + 1], k0), Tk);
+  q0 = min(max(q0, 0), T), q1 = min(max(q1, q0), T);
+  k0 = min(max(k0, 0), Tk), k1 = min(max(k1, k0), Tk);
   s = {q0, k0, q1 - q0, k1 - k0, (slot - (q0 * G / QT + i)) * QT};
   return s.first >= 0 && s.first < s.nq * G;                 // entries out of order lead to no slot below 0
 }
@@ -74,9 +82,9 @@ __device__ __forceinline__ float add_pair(uint32_t w, float acc) {
 // Scores of masked keys.
 constexpr float HIDDEN = -INFINITY;
 
-template <bool BF16, int KS, int DT, int NW, int R>
+template <bool BF16, int KS, int DT, int NW>
 struct Prompt {
-  static constexpr int QT = 32 * R * NW;                              // R times 32 queries a wavefront
+  static constexpr int QT = 32 * NW;
   static constexpr float LIFT = BF16 ? 0.0f : 6.0f;
   static constexpr int PITCH = KS <= 4 ? 128 : 256;                  // bytes of a key's row in LDS
   static constexpr int TILE = KT * PITCH;
@@ -96,19 +104,17 @@ struct Prompt {
   enum Pass { PLAIN, FINITE, UP, DOWN };
   static constexpr uint32_t ONE = BF16 ? 0x3F80u : 0x3C00u;
   template <Pass PASS>
-  __device__ static void pass(const AttnArgs& a, const Span& s, int hk, int G, uint8_t* lds, const v4u (&q)[R][KS],
-                              v16f (&acc)[R][DT], float (&l)[R]) {
+  __device__ static void pass(const AttnArgs& a, const Span& s, int hk, int G, uint8_t* lds, v4u (&q)[KS],
+                              v16f (&acc)[DT], float& l) {
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5;
     const int off = s.nk - s.nq;                                     // query i sees keys to i + off
-    const int rows = s.nq * G, w0 = s.first + 32 * R * wid;          // the wavefront's first row
+    const int rows = s.nq * G, w0 = s.first + 32 * wid;          // the wavefront's first row
     auto sees_of = [&](int row) { return a.causal ? min(row / G + off + 1, s.nk) : s.nk; };
     const int nk = max(sees_of(min(s.first + QT, rows) - 1), 0);
     const int tiles = (nk + KT - 1) / KT;                            // that any of the workgroup's rows sees
-    int sees[R];                                                     // keys the lane's rows see
-#pragma unroll
-    for (int r = 0; r < R; ++r) sees[r] = sees_of(w0 + 32 * r + (lane & 31));
-    const int wsees = w0 >= rows ? 0 : sees_of(min(w0 + 32 * R, rows) - 1);      // any of the wavefront's
+    const int sees = sees_of(w0 + (lane & 31));                      // keys the lane's row sees
+    const int wsees = w0 >= rows ? 0 : sees_of(min(w0 + 32, rows) - 1);          // any of the wavefront's
     const int wall = sees_of(w0);                                    // all of them
     const int wtiles = wsees > 0 ? (wsees + KT - 1) / KT : 0;
 
@@ -119,21 +125,15 @@ struct Prompt {
     const uint32_t lds0 = lds_addr(lds) + 1024 * wid;
     const uint8_t* const kp = a.k.p + s.k0 * a.k.ts + hk * a.k.hs;
     const uint8_t* const vp = a.v.p + s.k0 * a.v.ts + hk * a.v.hs;
-    // rows behind the last key: zeros; tiles behind the last: nothing
-    auto load_k = [&](int t) {
+    // rows behind the last key: zeros; tiles behind the last: nothing.  Tile t goes to slot t % 2.
+    auto load = [&](const uint8_t* p, int64_t ts, uint32_t off, uint32_t at, int t) {
       if (t >= tiles) return;
-      const v4i r = rsrc_words(kp + (int64_t)KT * t * a.k.ts, (int64_t)(s.nk - KT * t - 1) * a.k.ts + 2 * a.D);
+      const v4i r = rsrc_words(p + (int64_t)KT * t * ts, (int64_t)(s.nk - KT * t - 1) * ts + 2 * a.D);
 #pragma unroll
-      for (int n = 0; n < LOADS; ++n)
-        lds_load16(r, lds0 + (t & 1) * TILE + 1024 * NW * n, (int)(vk + (uint32_t)(ROWS * NW * n) * (uint32_t)a.k.ts));
+      for (int n = 0; n < LOADS; ++n) lds_load16(r, at + 1024 * NW * n, (int)(off + (uint32_t)(ROWS * NW * n) * (uint32_t)ts));
     };
-    auto load_v = [&](int t) {
-      if (t >= tiles) return;
-      const v4i r = rsrc_words(vp + (int64_t)KT * t * a.v.ts, (int64_t)(s.nk - KT * t - 1) * a.v.ts + 2 * a.D);
-#pragma unroll
-      for (int n = 0; n < LOADS; ++n)
-        lds_load16(r, lds0 + (2 + (t & 1)) * TILE + 1024 * NW * n, (int)(vv + (uint32_t)(ROWS * NW * n) * (uint32_t)a.v.ts));
-    };
+    auto load_k = [&](int t, int slot) { load(kp, a.k.ts, vk, lds0 + slot * TILE, t); };
+    auto load_v = [&](int t, int slot) { load(vp, a.v.ts, vv, lds0 + (2 + slot) * TILE, t); };
 
     // this lane's fragment addresses within a tile
     const int kr = lane & 31;
@@ -145,26 +145,22 @@ struct Prompt {
     for (int i = 0; i < DT; ++i)
       va[i] = PITCH * vr + 16 * ((4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swizzle_v(vr)) + 8 * (lane & 1);
 
-    float m[R], base[R];                                             // scaled: weights are exp2(x c - base)
-    v16f x[R][2];                                                    // scores of a tile
-    v4u p[R][4];                                                     // its weights
+    float m = HIDDEN, base = 0.0f;                                   // scaled: weights are exp2(x c - base)
+    v16f x[2][2];                                                    // scores of a tile, in x[t % 2]
+    v4u p[4];                                                        // weights of a tile
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[r][i][e] = 0.0f;
-      l[r] = base[r] = 0.0f;
-      m[r] = HIDDEN;
-    }
+      for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
+    l = 0.0f;
 
-    // fragment n of a tile's keys (rows 32 (n % 2) .. + 31, contraction step n / 2) and of its values (row block n % DT,
+    // fragment n of a slot's keys (rows 32 (n % 2) .. + 31, contraction step n / 2) and of its values (row block n % DT,
     // contraction step n / DT)
-    auto key_frag = [&](int t, int n) {
-      return *reinterpret_cast<const v4u*>(lds + (t & 1) * TILE + 32 * PITCH * (n & 1) + ka[n >> 1]);
+    auto key_frag = [&](int slot, int n) {
+      return *reinterpret_cast<const v4u*>(lds + slot * TILE + 32 * PITCH * (n & 1) + ka[n >> 1]);
     };
-    auto value_frag = [&](int t, int n) {
-      const uint8_t* const at = lds + (2 + (t & 1)) * TILE + va[n % DT] + 16 * PITCH * (n / DT);
+    auto value_frag = [&](int slot, int n) {
+      const uint8_t* const at = lds + (2 + slot) * TILE + va[n % DT] + 16 * PITCH * (n / DT);
       const v2u lo = lds_tr16(at), hi = lds_tr16(at + 8 * PITCH);
       v4u v = {lo[0], lo[1], hi[0], hi[1]};
       if constexpr (PASS != PLAIN) {
@@ -180,147 +176,138 @@ struct Prompt {
       }
       return v;
     };
-    // weights 2 n and 2 n + 1 of the lane's 32
-    auto weight_pair = [&](const v16f (&y)[R][2], int key, int r, int n) {
+    // weights 2 n and 2 n + 1 of the lane's 32; their sum is that of the rounded ones
+    auto weight_pair = [&](const v16f (&y)[2], int key, int n) {
       const int h = n >> 3, e = 2 * (n & 7);
-      const float p0 = __builtin_amdgcn_exp2f(fmaf(y[r][h][e], a.c, -base[r]));
-      const float p1 = __builtin_amdgcn_exp2f(fmaf(y[r][h][e + 1], a.c, -base[r]));
+      const float p0 = __builtin_amdgcn_exp2f(fmaf(y[h][e], a.c, -base));
+      const float p1 = __builtin_amdgcn_exp2f(fmaf(y[h][e + 1], a.c, -base));
       const uint32_t w = pack2_16<BF16>(p0, p1);
-      l[r] = add_pair<BF16>(w, l[r]);
+      l = add_pair<BF16>(w, l);
       if constexpr (PASS < UP) {
-        p[r][n >> 2][n & 3] = w;
+        p[n >> 2][n & 3] = w;
       } else {
         const int at = key + 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
-        p[r][n >> 2][n & 3] = (at < sees[r] ? ONE : 0u) | (at + 1 < sees[r] ? ONE << 16 : 0u);
+        p[n >> 2][n & 3] = (at < sees ? ONE : 0u) | (at + 1 < sees ? ONE << 16 : 0u);
       }
     };
     // The compiler's own order reads each fragment just before its product; these loops keep AHEAD fragments in
     // flight and put a share of the vector work behind each product.
     constexpr int AHEAD = 4, NK = 2 * KS, NV = 4 * DT;
-    auto scores = [&](int t, auto beside) {
+    auto scores = [&](v16f (&y)[2], int slot, auto beside) {
       v4u f[NK];
       v16f z;
 #pragma unroll
       for (int e = 0; e < 16; ++e) z[e] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < AHEAD; ++n) f[n] = key_frag(t, n);
+      for (int n = 0; n < AHEAD; ++n) f[n] = key_frag(slot, n);
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
-        if (n + AHEAD < NK) f[n + AHEAD] = key_frag(t, n + AHEAD);
+        if (n + AHEAD < NK) f[n + AHEAD] = key_frag(slot, n + AHEAD);
+        y[n & 1] = mfma32<BF16>(f[n], q[n >> 1], n < 2 ? z : y[n & 1]);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          x[r][n & 1] = mfma32<BF16>(f[n], q[r][n >> 1], n < 2 ? z : x[r][n & 1]);
-#pragma unroll
-          for (int i = 16 * n / NK; i < 16 * (n + 1) / NK; ++i) beside(r, i);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int i = 16 * n / NK; i < 16 * (n + 1) / NK; ++i) beside(i);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
-    auto values = [&](int t, auto beside) {
+    auto values = [&](int slot, auto beside) {
       v4u f[NV];
 #pragma unroll
-      for (int n = 0; n < AHEAD; ++n) f[n] = value_frag(t, n);
+      for (int n = 0; n < AHEAD; ++n) f[n] = value_frag(slot, n);
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        if (n + AHEAD < NV) f[n + AHEAD] = value_frag(t, n + AHEAD);
+        if (n + AHEAD < NV) f[n + AHEAD] = value_frag(slot, n + AHEAD);
+        acc[n % DT] = mfma32<BF16>(f[n], p[n / DT], acc[n % DT]);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          acc[r][n % DT] = mfma32<BF16>(f[n], p[r][n / DT], acc[r][n % DT]);
-#pragma unroll
-          for (int i = 16 * n / NV; i < 16 * (n + 1) / NV; ++i) beside(r, i);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int i = 16 * n / NV; i < 16 * (n + 1) / NV; ++i) beside(i);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
-    auto hide = [&](int key) {
+    auto hide = [&](v16f (&y)[2], int key) {
       if (key + KT > wall) {
+        const int left = sees - key - 4 * half;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int left = sees[r] - key - 4 * half;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              x[r][h][e] = 32 * h + 8 * (e >> 2) + (e & 3) < left ? x[r][h][e] : HIDDEN;
-        }
+          for (int e = 0; e < 16; ++e)
+            y[h][e] = 32 * h + 8 * (e >> 2) + (e & 3) < left ? y[h][e] : HIDDEN;
       }
     };
-    auto raise = [&](float (&top)[R]) {
-      bool up = false;
+    float top;
+    auto compare = [&](const v16f (&y)[2], int n) {
+      top = fmaxf(fmaxf(top, y[n >> 3][2 * (n & 7)]), y[n >> 3][2 * (n & 7) + 1]);
+    };
+    auto raise = [&] {
+      top = half_max(top) * a.c;
+      if (__any(top > m + 8.0f)) {
+        const float to = fmaxf(m, top);
+        const float f = to == HIDDEN ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        base = (to == HIDDEN ? 0.0f : to) - LIFT;
+        if constexpr (PASS < UP) {
+          l *= f;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        top[r] = half_max(top[r]) * a.c;
-        up |= top[r] > m[r] + 8.0f;
-      }
-      if (__any(up)) {
+          for (int i = 0; i < DT; ++i)
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float to = fmaxf(m[r], top[r]);
-          const float f = to == HIDDEN ? 1.0f : __builtin_amdgcn_exp2f(m[r] - to);
-          m[r] = to;
-          base[r] = (to == HIDDEN ? 0.0f : to) - LIFT;
-          if constexpr (PASS < UP) {
-            l[r] *= f;
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) acc[r][i][e] *= f;
-          }
+            for (int e = 0; e < 16; ++e) acc[i][e] *= f;
         }
       }
     };
     // Tile t's keys one step ahead of its values: a step's products need K(t + 1) and V(t), its loads fill the slots of
-    // K(t) and V(t - 1), which the step before has read.
-    auto step = [&](int t) {
+    // K(t) and V(t - 1), which the step before has read.  (The first tiles' are loaded together, below.)
+    auto step = [&](int t, int slot) {
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
       lds_barrier();
-      load_k(t + 2);
-      load_v(t + 1);
+      load_k(t + 2, slot);
+      load_v(t + 1, slot ^ 1);
     };
+    // tile t, in slot S, and the scores of the next
+    auto both = [&](int t, auto S) {
+      constexpr int S0 = decltype(S)::value, S1 = S0 ^ 1;
+      step(t, S0);
+      scores(x[S1], S1, [&](int n) { weight_pair(x[S0], KT * t, n); });
+      asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]));       // here, not behind the branch
+      hide(x[S1], KT * (t + 1));
+      top = HIDDEN;
+      values(S0, [&](int n) { compare(x[S1], n); });
+      raise();
+    };
+    auto last = [&](int t, auto S) {
+      constexpr int S0 = decltype(S)::value;
+      step(t, S0);
+#pragma unroll
+      for (int n = 0; n < 16; ++n) weight_pair(x[S0], KT * t, n);
+      values(S0, [](int) {});
+    };
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
 
-    load_k(0);
-    step(-1);
-    float top[R];
-    auto reset = [&] {
+    load_k(0, 0);
+    load_v(0, 0);
+    load_k(1, 1);
 #pragma unroll
-      for (int r = 0; r < R; ++r) top[r] = HIDDEN;
-    };
-    auto compare = [&](int r, int n) { top[r] = fmaxf(fmaxf(top[r], x[r][n >> 3][2 * (n & 7)]), x[r][n >> 3][2 * (n & 7) + 1]); };
-    if (wtiles > 0) {
-      scores(0, [](int, int) {});
-      hide(0);
-      reset();
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int n = 0; n < 16; ++n) compare(r, n);
-      raise(top);
-    }
+    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i]));      // the queries are waited for here, not in the loop
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    lds_barrier();
     int t = 0;
-    for (; t + 1 < wtiles; ++t) {
-      step(t);
-      v16f y[R][2];
+    if (wtiles > 0) {
+      scores(x[0], 0, [](int) {});
+      hide(x[0], 0);
+      top = HIDDEN;
 #pragma unroll
-      for (int r = 0; r < R; ++r) y[r][0] = x[r][0], y[r][1] = x[r][1];
-      scores(t + 1, [&](int r, int n) { weight_pair(y, KT * t, r, n); });
-#pragma unroll
-      for (int r = 0; r < R; ++r)                                    // here, not behind the branch
-        asm volatile("" : "+v"(p[r][0]), "+v"(p[r][1]), "+v"(p[r][2]), "+v"(p[r][3]));
-      hide(KT * (t + 1));
-      reset();
-      values(t, compare);
-      raise(top);
+      for (int n = 0; n < 16; ++n) compare(x[0], n);
+      raise();
+      for (; t + 2 < wtiles; t += 2) {
+        both(t, even);
+        both(t + 1, odd);
+      }
+      if (t + 1 < wtiles) {
+        both(t++, even);
+        last(t++, odd);
+      } else {
+        last(t++, even);
+      }
     }
-    if (t < wtiles) {
-      step(t);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int n = 0; n < 16; ++n) weight_pair(x, KT * t, r, n);
-      values(t, [](int, int) {});
-      ++t;
-    }
-    for (; t < tiles; ++t) step(t);
+    for (; t < tiles; ++t) step(t, t & 1);                           // the workgroup's other wavefronts see more
   }
 };
 
@@ -388,21 +375,19 @@ __device__ __forceinline__ void store_rows(const AttnArgs& a, const v16f (&acc)[
 }
 
 // Which of the lane's counts are above zero.
-template <int R, int DT>
-__device__ __forceinline__ void seen_bits(const v16f (&acc)[R][DT], uint32_t (&bits)[R][DT]) {
+template <int DT>
+__device__ __forceinline__ void seen_bits(const v16f (&acc)[DT], uint32_t (&bits)[DT]) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int i = 0; i < DT; ++i) {
+    bits[i] = 0;
 #pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      bits[r][i] = 0;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) bits[r][i] |= acc[r][i][e] > 0.0f ? 1u << e : 0u;
-    }
+    for (int e = 0; e < 16; ++e) bits[i] |= acc[i][e] > 0.0f ? 1u << e : 0u;
+  }
 }
 
-template <bool BF16, int KS, int DT, int NW, int R>
-__global__ __launch_bounds__(64 * NW, R == 1 && NW == 4 ? 2 : 1) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
-  using P = Prompt<BF16, KS, DT, NW, R>;
+template <bool BF16, int KS, int DT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
+  using P = Prompt<BF16, KS, DT, NW>;
   constexpr int QT = P::QT;
   constexpr int LDS = 4 * P::TILE > 32 * NW * P::OPITCH ? 4 * P::TILE : 32 * NW * P::OPITCH;
   __shared__ __align__(1024) uint8_t lds[LDS];
@@ -427,34 +412,27 @@ __global__ __launch_bounds__(64 * NW, R == 1 && NW == 4 ? 2 : 1) void attn_promp
   if (!find_span<QT>(a, G, slots - 1 - (int32_t)slot, s)) return;
 
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half = lane >> 5, w0 = s.first + 32 * R * wid, rows = s.nq * G;
-  v4u q[R][KS];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = w0 + 32 * r + (lane & 31);
+  const int half = lane >> 5, w0 = s.first + 32 * wid, rows = s.nq * G;
+  v4u q[KS];
+  {
+    const int row = w0 + (lane & 31);
     const uint8_t* const at = a.q.p + (s.q0 + row / G) * a.q.ts + (int64_t)(hk * G + row % G) * a.q.hs + 16 * half;
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-      q[r][i] = v4u{0, 0, 0, 0};
-      if (row < rows && 2 * i + half < a.D / 8) q[r][i] = *reinterpret_cast<const v4u*>(at + 32 * i);
+      q[i] = v4u{0, 0, 0, 0};
+      if (row < rows && 2 * i + half < a.D / 8) q[i] = *reinterpret_cast<const v4u*>(at + 32 * i);
     }
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[r][i]));   // here before the loop's own loads
-  v16f acc[R][DT];
-  float l[R];
+  v16f acc[DT];
+  float l;
   P::template pass<P::PLAIN>(a, s, hk, G, lds, q, acc, l);
   bool bad = false;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int i = 0; i < DT; ++i)
 #pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) bad |= !(fabsf(acc[r][i][e]) < INFINITY);
+    for (int e = 0; e < 16; ++e) bad |= !(fabsf(acc[i][e]) < INFINITY);
   if (__builtin_expect(__syncthreads_or(bad), 0)) {
-    uint32_t up[R][DT], down[R][DT];
+    uint32_t up[DT], down[DT];
     P::template pass<P::UP>(a, s, hk, G, lds, q, acc, l);
     seen_bits(acc, up);
     __syncthreads();
@@ -463,42 +441,34 @@ __global__ __launch_bounds__(64 * NW, R == 1 && NW == 4 ? 2 : 1) void attn_promp
     __syncthreads();
     P::template pass<P::FINITE>(a, s, hk, G, lds, q, acc, l);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          acc[r][i][e] += (up[r][i] >> e & 1 ? INFINITY : 0.0f) + (down[r][i] >> e & 1 ? -INFINITY : 0.0f);
+      for (int e = 0; e < 16; ++e)
+        acc[i][e] += (up[i] >> e & 1 ? INFINITY : 0.0f) + (down[i] >> e & 1 ? -INFINITY : 0.0f);
     __syncthreads();
   }
-  // whole rows through LDS, 32 at a time
-  uint8_t* const mine = lds + 32 * P::OPITCH * wid;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float sum = half_sum(l[r]);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;               // a query that sees nothing: zeros
-    store_rows<BF16, DT, P::OPITCH>(a, acc[r], inv, s.q0, hk, G, w0 + 32 * r, rows, mine);
-    __builtin_amdgcn_wave_barrier();
-  }
+  const float sum = half_sum(l), inv = sum == 0.0f ? 0.0f : 1.0f / sum;        // a query that sees nothing: zeros
+  store_rows<BF16, DT, P::OPITCH>(a, acc, inv, s.q0, hk, G, w0, rows, lds + 32 * P::OPITCH * wid);
 }
-template <bool BF16, int KS, int DT, int NW, int R>
+
+template <bool BF16, int KS, int DT>
 hipError_t go(const AttnArgs& a, hipStream_t s) {
-  constexpr int QT = 32 * R * NW;
+  constexpr int NW = 4, QT = 32 * NW;
   const int64_t rows = a.T * (a.Hq / a.Hkv);
   const int64_t slots = a.cu_q ? rows / QT + a.B : (rows + QT - 1) / QT;
   const int64_t grid = a.Hkv % 8 && 8 % a.Hkv == 0 ? (slots + 8 / a.Hkv - 1) / (8 / a.Hkv) * 8 : slots * a.Hkv;
-  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, R>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a,
+  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a,
                      (int32_t)slots);
   return hipGetLastError();
 }
 
 template <bool BF16>
 hipError_t by_width(const AttnArgs& a, hipStream_t s) {
-  if (a.D <= 32) return go<BF16, 2, 1, 4, 1>(a, s);
-  if (a.D <= 64) return go<BF16, 4, 2, 4, 1>(a, s);
-  if (a.D <= 80) return go<BF16, 5, 3, 4, 1>(a, s);
-  if (a.D <= 96) return go<BF16, 6, 3, 4, 1>(a, s);
-  return go<BF16, 8, 4, 4, 1>(a, s);
+  if (a.D <= 32) return go<BF16, 2, 1>(a, s);
+  if (a.D <= 64) return go<BF16, 4, 2>(a, s);
+  if (a.D <= 80) return go<BF16, 5, 3>(a, s);
+  if (a.D <= 96) return go<BF16, 6, 3>(a, s);
+  return go<BF16, 8, 4>(a, s);
 }
 
 }  // namespace
