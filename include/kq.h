@@ -394,8 +394,8 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
  *
  *   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j - max),  over the keys j that the query sees;
  *
- * a query that sees no key gets zeros, and what is at keys that it does not see (NaN and infinities
- * included) does not reach it.  Scores, maxima and sums are float32; the weights are rounded to the
+ * a query that sees no key (or none with a score above minus infinity) gets zeros, and what is at keys that
+ * it does not see (NaN and infinities included) does not reach it.  Scores, maxima and sums are float32; the weights are rounded to the
  * 16-bit type for the product with the values (in an 8-bit cache: to bf16, for fp16 outputs to the sum of
  * two bf16 numbers).  They are divided by their sum at the end, so values beyond 10^30 may overflow.  The
  * order of additions is fixed for one device: equal inputs of equal shape give equal bits.

@@ -97,13 +97,7 @@ struct Prompt {
   __device__ static int swizzle_k(int row) { return PITCH == 256 ? row & 15 : (row >> 1) & 7; }
   __device__ static int swizzle_v(int row) { return PITCH == 256 ? 4 * (row & 3) : 4 * ((row >> 1) & 1); }
 
-  // One pass over the keys: unnormalized O^T in acc, this lane's part of the sums in l.  A value that is not finite would
-  // reach queries that do not see it (0 times it is not 0), so where a result is not finite the pass is made
-  // again: FINITE leaves such values out; UP and DOWN count, instead of weighing, the visible values that
-  // are infinite upwards or NaN, and downwards or NaN.
-  enum Pass { PLAIN, FINITE, UP, DOWN };
-  static constexpr uint32_t ONE = BF16 ? 0x3F80u : 0x3C00u;
-  template <Pass PASS>
+  // One pass over the keys: unnormalized O^T in acc, this lane's part of the sums in l.
   __device__ static void pass(const AttnArgs& a, const Span& s, int hk, int G, uint8_t* lds, v4u (&q)[KS],
                               v16f (&acc)[DT], float& l) {
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -162,33 +156,16 @@ struct Prompt {
     auto value_frag = [&](int slot, int n) {
       const uint8_t* const at = lds + (2 + slot) * TILE + va[n % DT] + 16 * PITCH * (n / DT);
       const v2u lo = lds_tr16(at), hi = lds_tr16(at + 8 * PITCH);
-      v4u v = {lo[0], lo[1], hi[0], hi[1]};
-      if constexpr (PASS != PLAIN) {
-        constexpr uint32_t INF = BF16 ? 0x7F80u : 0x7C00u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int sh = 16 * (e & 1);
-          const uint32_t w = (v[e / 2] >> sh) & 0xFFFFu;
-          const bool fin = (w & INF) != INF;
-          const uint32_t to = PASS == FINITE ? (fin ? w : 0u) : fin || w == (PASS == UP ? INF | 0x8000u : INF) ? 0u : ONE;
-          v[e / 2] = (v[e / 2] & ~(0xFFFFu << sh)) | (to << sh);
-        }
-      }
-      return v;
+      return v4u{lo[0], lo[1], hi[0], hi[1]};
     };
     // weights 2 n and 2 n + 1 of the lane's 32; their sum is that of the rounded ones
-    auto weight_pair = [&](const v16f (&y)[2], int key, int n) {
+    auto weight_pair = [&](const v16f (&y)[2], int n) {
       const int h = n >> 3, e = 2 * (n & 7);
       const float p0 = __builtin_amdgcn_exp2f(fmaf(y[h][e], a.c, -base));
       const float p1 = __builtin_amdgcn_exp2f(fmaf(y[h][e + 1], a.c, -base));
       const uint32_t w = pack2_16<BF16>(p0, p1);
       l = add_pair<BF16>(w, l);
-      if constexpr (PASS < UP) {
-        p[n >> 2][n & 3] = w;
-      } else {
-        const int at = key + 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
-        p[n >> 2][n & 3] = (at < sees ? ONE : 0u) | (at + 1 < sees ? ONE << 16 : 0u);
-      }
+      p[n >> 2][n & 3] = w;
     };
     // The compiler's own order reads each fragment just before its product; these loops keep AHEAD fragments in
     // flight and put a share of the vector work behind each product.
@@ -243,13 +220,11 @@ struct Prompt {
         const float f = to == HIDDEN ? 1.0f : __builtin_amdgcn_exp2f(m - to);
         m = to;
         base = (to == HIDDEN ? 0.0f : to) - LIFT;
-        if constexpr (PASS < UP) {
-          l *= f;
+        l *= f;
 #pragma unroll
-          for (int i = 0; i < DT; ++i)
+        for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-        }
+          for (int e = 0; e < 16; ++e) acc[i][e] *= f;
       }
     };
     // Tile t's keys one step ahead of its values: a step's products need K(t + 1) and V(t), its loads fill the slots of
@@ -264,7 +239,7 @@ struct Prompt {
     auto both = [&](int t, auto S) {
       constexpr int S0 = decltype(S)::value, S1 = S0 ^ 1;
       step(t, S0);
-      scores(x[S1], S1, [&](int n) { weight_pair(x[S0], KT * t, n); });
+      scores(x[S1], S1, [&](int n) { weight_pair(x[S0], n); });
       asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]));       // here, not behind the branch
       hide(x[S1], KT * (t + 1));
       top = HIDDEN;
@@ -275,7 +250,7 @@ struct Prompt {
       constexpr int S0 = decltype(S)::value;
       step(t, S0);
 #pragma unroll
-      for (int n = 0; n < 16; ++n) weight_pair(x[S0], KT * t, n);
+      for (int n = 0; n < 16; ++n) weight_pair(x[S0], n);
       values(S0, [](int) {});
     };
     const std::integral_constant<int, 0> even;
@@ -374,14 +349,65 @@ __device__ __forceinline__ void store_rows(const AttnArgs& a, const v16f (&acc)[
   }
 }
 
-// Which of the lane's counts are above zero.
-template <int DT>
-__device__ __forceinline__ void seen_bits(const v16f (&acc)[DT], uint32_t (&bits)[DT]) {
+// Rows row0 .. + 31 again, by the definition: a value that is not finite has reached rows that do not see it (0 times it
+// is not 0), or such values are seen.  A row at a time, 64 keys at a time: a lane has a key's score, then values 2 l and
+// 2 l + 1 of the sum.  Slow (ten vector instructions a key), and small: it needs none of the tiles' registers.
+template <bool BF16>
+__device__ void exact_rows(const AttnArgs& a, const Span& s, int hk, int G, int row0) {
+  const int lane = threadIdx.x & 63, end = min(row0 + 32, s.nq * G);
+  const uint8_t* const kp = a.k.p + s.k0 * a.k.ts + hk * a.k.hs;
+  const uint8_t* const vp = a.v.p + s.k0 * a.v.ts + hk * a.v.hs + 4 * lane;
+  for (int row = row0; row < end; ++row) {
+    const int head = hk * G + row % G, n = a.causal ? min(row / G + s.nk - s.nq + 1, s.nk) : s.nk;
+    const int64_t token = s.q0 + row / G;
+    const uint8_t* const qp = a.q.p + token * a.q.ts + head * a.q.hs;
+    float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+    for (int k0 = 0; k0 < n; k0 += 64) {
+      const bool there = k0 + lane < n;
+      float x = 0.0f;
+      for (int c = 0; c < a.D / 8; ++c) {
+        v4u kw = {0, 0, 0, 0};
+        if (there) kw = *reinterpret_cast<const v4u*>(kp + (int64_t)(k0 + lane) * a.k.ts + 16 * c);
+        float k[8], q[8];
+        unpack8_16<BF16>(kw, k);
+        unpack8_16<BF16>(*reinterpret_cast<const v4u*>(qp + 16 * c), q);
 #pragma unroll
-  for (int i = 0; i < DT; ++i) {
-    bits[i] = 0;
+        for (int e = 0; e < 8; ++e) x = fmaf(k[e], q[e], x);
+      }
+      x = there ? x * a.c : -INFINITY;
+      float to = fmaxf(m, x);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) bits[i] |= acc[i][e] > 0.0f ? 1u << e : 0u;
+      for (int off = 32; off >= 1; off >>= 1) to = fmaxf(to, __shfl_xor(to, off, 64));
+      const float base = to == -INFINITY ? 0.0f : to, f = __builtin_amdgcn_exp2f(m - base);
+      const float p = there ? __builtin_amdgcn_exp2f(x - base) : 0.0f;
+      m = to;
+      l = fmaf(l, f, p);
+      o0 *= f, o1 *= f;
+      for (int i = 0; i < min(64, n - k0); ++i) {
+        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), i));
+        uint32_t v = 0;
+        if (2 * lane < a.D) v = *reinterpret_cast<const uint32_t*>(vp + (int64_t)(k0 + i) * a.v.ts);
+        o0 = fmaf(w, unpack1_16<BF16>((uint16_t)v), o0);
+        o1 = fmaf(w, unpack1_16<BF16>((uint16_t)(v >> 16)), o1);
+      }
+    }
+    const float sum = wave_sum(l), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    o0 *= inv, o1 *= inv;
+    if (a.scales) {                                                  // D is 128
+      uint32_t top = row16_umax(umax32(abs_bits(o0), abs_bits(o1)));
+      top = umax32(top, __shfl_xor(top, 16, 64));
+      top = umax32(top, __shfl_xor(top, 32, 64));
+      const uint32_t byte = f8_scale_byte(top);
+      const float unit = byte == 255u ? 1.0f : f8_inv_scale(byte);
+      const uint32_t w = byte == 255u ? 0x7F7Fu : f8_pack4(o0, o1, 0.0f, 0.0f, unit);
+      *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + (token * a.Hq + head) * 128 + 2 * lane) = (uint16_t)w;
+      const int SC = (int)f8_scale_cols((int64_t)a.Hq * 128);
+      if (lane == 0) a.scales[token * SC + head] = (uint8_t)byte;
+      if (head == a.Hq - 1 && head + 1 + lane < SC) a.scales[token * SC + head + 1 + lane] = 0;
+    } else if (2 * lane < a.D) {
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + ((token * a.Hq + head) * a.D + 2 * lane) * 2) =
+          pack2_16<BF16>(o0, o1);
+    }
   }
 }
 
@@ -425,27 +451,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_kernel(AttnArgs a, int
   }
   v16f acc[DT];
   float l;
-  P::template pass<P::PLAIN>(a, s, hk, G, lds, q, acc, l);
-  bool bad = false;
+  P::pass(a, s, hk, G, lds, q, acc, l);
+  lds_barrier();                                                     // the tiles have been read: outputs go there
+  float zero = 0.0f;
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) bad |= !(fabsf(acc[i][e]) < INFINITY);
-  if (__builtin_expect(__syncthreads_or(bad), 0)) {
-    uint32_t up[DT], down[DT];
-    P::template pass<P::UP>(a, s, hk, G, lds, q, acc, l);
-    seen_bits(acc, up);
-    __syncthreads();
-    P::template pass<P::DOWN>(a, s, hk, G, lds, q, acc, l);
-    seen_bits(acc, down);
-    __syncthreads();
-    P::template pass<P::FINITE>(a, s, hk, G, lds, q, acc, l);
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        acc[i][e] += (up[i] >> e & 1 ? INFINITY : 0.0f) + (down[i] >> e & 1 ? -INFINITY : 0.0f);
-    __syncthreads();
+    for (int e = 0; e < 16; ++e) zero = fmaf(acc[i][e], 0.0f, zero);
+  if (__builtin_expect(__any(!(zero == 0.0f)), 0)) {
+    exact_rows<BF16>(a, s, hk, G, w0);
+    return;
   }
   const float sum = half_sum(l), inv = sum == 0.0f ? 0.0f : 1.0f / sum;        // a query that sees nothing: zeros
   store_rows<BF16, DT, P::OPITCH>(a, acc, inv, s.q0, hk, G, w0, rows, lds + 32 * P::OPITCH * wid);
