@@ -438,8 +438,8 @@ kq_status kq_cache_append(int32_t dtype, const void* K, int64_t k_token, int64_t
                           uint8_t* kscales, uint8_t* vscales, int64_t pages, int32_t page, hipStream_t stream);
 
 /* One new token a sequence: query b of Q [B][Hq][D] (strides as above, both D to 2^21) sees the lengths[b]
- * tokens of its sequence.  workspace: at least kq_paged_attention_workspace_bytes bytes, 256-byte aligned (it
- * depends on the device's compute units: ask on the device that runs the call).  Calls that share a workspace
+ * tokens of its sequence.  workspace: at least kq_paged_attention_workspace_bytes bytes, 256-byte aligned (0: none
+ * needed; it depends on the device's compute units: ask on the device that runs the call).  Calls that share a workspace
  * must not overlap, replays of captured graphs that hold it included.  B Hq <= 2^23.  scale finite, above 0. */
 size_t kq_paged_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t width, int32_t page);
 kq_status kq_paged_attention(int32_t dtype, const void* Q, int64_t q_seq, int64_t q_head, const void* kcache,

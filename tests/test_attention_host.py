@@ -152,9 +152,11 @@ def test_paged_refusals(lib):
     assert call(B=1 << 20, width=1, Hq=16, st=(2048, 128)) == UNSUPPORTED
     assert call(B=1 << 18, width=1 << 16) == UNSUPPORTED        # blocks past 32 bits
     assert call(st=(512, (1 << 21) + 8)) == UNSUPPORTED
-    need = lib.kq_paged_attention_workspace_bytes(3, 4, 2, 128, 4, 16)
-    assert need > 0 and lib.kq_paged_attention_workspace_bytes(3, 4, 3, 128, 4, 16) == 0
-    assert call(wk=None) == WORKSPACE and call(nb=need - 1) == WORKSPACE and call(wk=ODD16) == ALIGN
+    need = lib.kq_paged_attention_workspace_bytes(3, 4, 2, 128, 400, 16)
+    assert need > 0 and lib.kq_paged_attention_workspace_bytes(3, 4, 3, 128, 400, 16) == 0
+    assert call(width=400, wk=None) == WORKSPACE and call(width=400, nb=need - 1) == WORKSPACE
+    assert call(width=400, wk=ODD16) == ALIGN
+    assert lib.kq_paged_attention_workspace_bytes(3, 4, 2, 128, 40, 16) == 0          # short tables are not split
 
 
 def test_append_refusals(lib):

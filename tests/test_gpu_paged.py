@@ -40,14 +40,26 @@ def test_split(kq, lengths, dtype, cache):
     check_codes(*kq.paged_attention(Q, *c.args(), **c.scales(), fp8=True), o, tau)
 
 
-def test_many_sequences(kq):
-    """More sequences than a wavefront has lanes and than there are compute units, most of them short."""
+@pytest.mark.parametrize("width", [None, 70, 200])          # whole heads, by the table's width; else dealt to runs
+@pytest.mark.parametrize("Hkv,D,cache", [(1, 64, "fp16"), (4, 64, "fp16"), (2, 128, "fp16"), (8, 64, "fp8")])
+def test_many_sequences(kq, Hkv, D, cache, width):
+    """More sequences than a wavefront has lanes and than there are compute units, most of them short, some empty
+    (the first and last among them)."""
     rng = np.random.default_rng(5)
     lengths = [int(n) for n in rng.integers(0, 60, size=300)]
-    lengths[77], lengths[299] = 900, 400
-    c = Cache(lengths, 1, 64, 16, "fp16", "fp16", 6)
-    Q = heads((300, 2, 64), "fp16", 7)
-    check(kq.paged_attention(Q, *c.args()), *_expect(Q, c, "fp16", "fp16"), "fp16")
+    lengths[0] = lengths[64] = lengths[299] = 0
+    lengths[77], lengths[200] = 900, 400
+    c = Cache(lengths, Hkv, D, 16, "fp16", cache, 6, width=width)
+    Q = heads((300, 2 * Hkv, D), "fp16", 7)
+    check(kq.paged_attention(Q, *c.args(), **c.scales()), *_expect(Q, c, "fp16", cache), "fp16")
+
+
+def test_no_keys_at_all(kq):
+    for width in (4, 300):
+        c = Cache([0, 0, 0], 2, 64, 16, "bf16", "bf16", 6, width=width)
+        O = torch.full((3, 4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        kq.paged_attention(heads((3, 4, 64), "bf16", 7), *c.args(), O=O)
+        assert (O == 0).all()
 
 
 @pytest.mark.parametrize("cache", ["fp16", "fp8"])
@@ -246,10 +258,11 @@ def test_block(kq, cache):
     assert y.shape == x.shape and torch.isfinite(y).all()
 
 
-def test_captured_step(kq):
+@pytest.mark.parametrize("width", [8, 100])                  # not split, and split
+def test_captured_step(kq, width):
     """A step (append, attention) captured and replayed on new tokens and lengths, with eager work between."""
     lengths = [40, 7, 90]
-    c = Cache([n + 8 for n in lengths], 2, 128, 16, "bf16", "bf16", 40)
+    c = Cache([n + 8 for n in lengths], 2, 128, 16, "bf16", "bf16", 40, width=width)
     k2, v2 = c.k.clone(), c.v.clone()
     table, ln = on_gpu(c.table), on_gpu(np.array(lengths, np.int32))
     qkv = heads((3, 8, 128), "bf16", 41)
@@ -327,8 +340,9 @@ def test_refusals(kq):
             kq.paged_attention(Q, *bad[:4], **bad[4])
         with pytest.raises(ValueError):
             kq.cache_append(Q[:, :2], Q[:, 2:], *bad[:4], **bad[4])
+    long = table[:, :1].expand(2, 300).contiguous()
     with pytest.raises(kq.KQError):
-        kq.paged_attention(Q, k, v, table, ln, **c.scales(), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        kq.paged_attention(Q, k, v, long, ln, **c.scales(), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="shape"):
         kq.cache_append(Q[:, :2], Q[:, 2:], k, v, table, ln, on_gpu(np.zeros(2, np.int32)), **c.scales())
     with pytest.raises(kq.KQError):                            # three tokens of two sequences, and no cu

@@ -894,7 +894,7 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
         cq = _ints(torch, cu_q, "cu_q", (B + 1,), index)
         if cu_k is None and Tk != T:
             raise ValueError(f"cu_k must be given where there are {Tk} keys for {T} queries")
-        ck = cq if cu_k is None else _ints(torch, cu_k, "cu_k", (B + 1,), index)
+        ck = cq if cu_k is None or cu_k is cu_q else _ints(torch, cu_k, "cu_k", (B + 1,), index)
     elif cu_k is not None:
         raise ValueError("cu_k is given without cu_q")
     out, o, c, s = _attn_out(torch, T, Hq, D, dtype, fp8, O, codes, scales, index)
@@ -952,7 +952,7 @@ def cache_append(K, V, kcache, vcache, table, lengths, cu=None, kscales=None, vs
 
 
 def paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page):
-    """Workspace bytes kq_paged_attention needs on the current device."""
+    """Workspace bytes kq_paged_attention needs on the current device (0: none)."""
     return load().kq_paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page)
 
 
@@ -983,8 +983,10 @@ def paged_attention(Q, kcache, vcache, table, lengths, kscales=None, vscales=Non
         else:
             with torch.cuda.device(index):
                 nb = paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page)
-        workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
-        wk = workspace.data_ptr()
+        wk = None
+        if nb:
+            workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
+            wk = workspace.data_ptr()
     _call(torch, "kq_paged_attention", index, (dt, *q, kc, vc, ks, vs, pages, page, tb, width, ln, B, Hq, Hkv, D,
                                                D ** -0.5 if scale is None else scale, o, c, s, wk or None, nb))
     return out

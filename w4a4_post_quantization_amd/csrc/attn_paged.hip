@@ -637,6 +637,13 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
 constexpr int NW = 2;
 constexpr int resident(bool wide, int DP) { return wide && DP == 128 ? 2 : wide || DP == 128 ? 4 : 8; }
 
+// A unit is one workgroup's, and nothing is joined (so no workspace is needed), where tables hold up to 640 keys, or up to 2048 and there is a unit
+// for every compute unit: 32 / 8 heads of 128, whole and dealt (us): one sequence of 500 9.4 and 9.6, 1000 14 and 9.9; 8 of
+// 1000 16.3 and 15.7; 64 of 0 to 2000 in 8 bits 38 and 44; 300 of 100 in 16 bits 43 and 46; 160 of 200 to 8000 in 8 bits 281 and
+// 250.  Four wavefronts then, so that a unit is sooner done, or two where the units fill the chip (300 of 0 to 1000: 130
+// and 148; 64 of 500 in 8 bits the other way, 21 and 19).
+bool whole(int64_t units, int64_t longest) { return longest <= 640 || (longest <= 2048 && units >= device_cu_count()); }
+
 // Runs of a call: one for each workgroup that the compute units hold, and no more than blocks.
 int64_t runs(int64_t B, int Hq, int Hkv, int64_t longest, bool wide, int DP) {
   const int G = Hq / Hkv, HC = (G + 15) / 16, block = 32 * NW;
@@ -645,19 +652,14 @@ int64_t runs(int64_t B, int Hq, int Hkv, int64_t longest, bool wide, int DP) {
   return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 
-// A unit is one workgroup's, and nothing is joined, where tables hold up to 640 keys, or up to 2048 and there is a unit
-// for every compute unit: 32 / 8 heads of 128, whole and dealt (us): one sequence of 500 9.4 and 9.6, 1000 14 and 9.9; 8 of
-// 1000 16.3 and 15.7; 64 of 0 to 2000 in 8 bits 38 and 44; 300 of 100 in 16 bits 43 and 46; 160 of 200 to 8000 in 8 bits 281 and
-// 250.  Four wavefronts then, so that a unit is sooner done, or two where the units fill the chip (300 of 0 to 1000: 130
-// and 148; 64 of 500 in 8 bits the other way, 21 and 19).
 template <bool BF16, bool WIDE, int DP>
 hipError_t go(const PagedArgs& a, hipStream_t s) {
   constexpr int RES = resident(WIDE, DP);
   const int64_t longest = (int64_t)a.c.width * a.c.page;
-  const int G = a.Hq / a.c.Hkv, HC = (G + 15) / 16, cus = device_cu_count();
+  const int G = a.Hq / a.c.Hkv, HC = (G + 15) / 16;
   const int64_t units = (int64_t)a.c.B * a.c.Hkv * HC;
-  if (longest <= 640 || (longest <= 2048 && units >= cus)) {
-    if (units >= (int64_t)cus * RES)
+  if (whole(units, longest)) {
+    if (units >= (int64_t)device_cu_count() * RES)
       hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, 2, RES, true>), dim3((unsigned)units), dim3(128), 0, s, a, 0);
     else
       hipLaunchKernelGGL((paged_kernel<BF16, WIDE, DP, 4, RES / 2, true>), dim3((unsigned)units), dim3(256), 0, s, a, 0);
@@ -676,6 +678,7 @@ hipError_t go(const PagedArgs& a, hipStream_t s) {
 
 // For both kinds of cache.
 size_t paged_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int64_t longest) {
+  if (whole(B * Hkv * ((Hq / Hkv + 15) / 16), longest)) return 0;
   const int DP = D <= 64 ? 64 : 128;
   const int64_t part = DP == 64 ? PART<64> : PART<128>;
   const int64_t a = runs(B, Hq, Hkv, longest, false, DP), b = runs(B, Hq, Hkv, longest, true, DP);

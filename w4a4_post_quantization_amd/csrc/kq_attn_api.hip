@@ -139,8 +139,8 @@ kq_status kq_paged_attention(int32_t dtype, const void* Q, int64_t q_seq, int64_
   if (st != KQ_OK) return st;
   if (!std::isfinite(scale) || !(scale > 0.0f) || !std::isfinite(scale * LOG2E)) return KQ_ERR_VALUE;
   const size_t need = paged_workspace_bytes(B, Hq, Hkv, D, width * page);
-  if (!workspace || workspace_bytes < need) return KQ_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return KQ_ERR_ALIGN;
+  if (need && (!workspace || workspace_bytes < need)) return KQ_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 256)) return KQ_ERR_ALIGN;
   PagedArgs a;
   a.c = {static_cast<uint8_t*>(const_cast<void*>(kcache)), static_cast<uint8_t*>(const_cast<void*>(vcache)),
          const_cast<uint8_t*>(kscales), const_cast<uint8_t*>(vscales), table, lengths, pages, (int32_t)B, (int32_t)width,
