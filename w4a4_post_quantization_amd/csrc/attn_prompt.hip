@@ -168,8 +168,9 @@ struct Prompt {
       p[n >> 2][n & 3] = w;
     };
     // The compiler's own order reads each fragment just before its product; these loops keep AHEAD fragments in
-    // flight and put a share of the vector work behind each product.
-    constexpr int AHEAD = 4, NK = 2 * KS, NV = 4 * DT;
+    // flight and put a share of the vector work behind each product.  (Heads of 128, 8192 tokens: 512, 497 and 502 us with 2,
+    // 3 and 4; heads of 72 206, 207 and 205; heads of 64 leave registers for a third workgroup with 3.)
+    constexpr int AHEAD = KS == 5 || KS == 6 ? 4 : 3, NK = 2 * KS, NV = 4 * DT;
     auto scores = [&](v16f (&y)[2], int slot, auto beside) {
       v4u f[NK];
       v16f z;
@@ -411,8 +412,9 @@ __device__ void exact_rows(const AttnArgs& a, const Span& s, int hk, int G, int 
   }
 }
 
+// Two workgroups on a compute unit, three or four for narrow heads (64: 4096 tokens, 32 / 8 heads, causal 100 and 92 us).
 template <bool BF16, int KS, int DT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
+__global__ __launch_bounds__(64 * NW, KS <= 2 ? 4 : KS <= 4 ? 3 : 2) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
   using P = Prompt<BF16, KS, DT, NW>;
   constexpr int QT = P::QT;
   constexpr int LDS = 4 * P::TILE > 32 * NW * P::OPITCH ? 4 * P::TILE : 32 * NW * P::OPITCH;
