@@ -413,11 +413,17 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
  * and to their order.
  * Q, K, V: element (token, head, d) at token * token stride + head * head stride + d, strides in elements,
  * multiples of 8; token strides D to 2^21, head strides 0 to 2^40.  Views of one projection's output
- * [T][(Hq + 2 Hkv) D] are the usual case.  T, Tk <= 2^30, T Hq <= 2^29, B Hq <= 2^22.  scale finite, above 0. */
+ * [T][(Hq + 2 Hkv) D] are the usual case.  T, Tk <= 2^30, T Hq <= 2^29, B Hq <= 2^22.  scale finite, above 0.
+ * workspace: at least kq_attention_workspace_bytes bytes (packed: whether cu is given), 256-byte aligned (0: none needed; few
+ * queries of many keys are split over the keys, and it holds the parts.  It depends on the device's compute units:
+ * ask on the device that runs the call).  Calls that share a workspace must not overlap, replays of captured
+ * graphs that hold it included. */
+size_t kq_attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, int32_t packed, int32_t Hq, int32_t Hkv, int32_t D);
 kq_status kq_attention(int32_t dtype, const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token,
                        int64_t k_head, const void* V, int64_t v_token, int64_t v_head, const int32_t* cu_q,
                        const int32_t* cu_k, int64_t B, int64_t T, int64_t Tk, int32_t Hq, int32_t Hkv, int32_t D,
-                       int32_t causal, float scale, void* O, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+                       int32_t causal, float scale, void* O, uint8_t* codes, uint8_t* scales, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
 
 /* A cache of keys and values in pages of `page` tokens (a multiple of 16, to 65536): kcache, vcache
  * [pages][Hkv][page][D], in the 16-bit type; or, with kscales and vscales (both or neither; [pages][Hkv][page]),

@@ -61,11 +61,12 @@ def test_oracle_paged_equals_packed():
 
 def _attention(lib, **kw):
     a = dict(dt=1, Q=P, K=P, V=P, st=(512, 128), kst=(256, 128), vst=(256, 128), cq=P, ck=P, B=2, T=10, Tk=12, Hq=4, Hkv=2,
-             D=128, causal=1, scale=0.1, O=P, c=None, s=None)
+             D=128, causal=1, scale=0.1, O=P, c=None, s=None, wk=None, nb=0)
     assert set(kw) <= set(a)
     a.update(kw)
     return lib.kq_attention(a["dt"], a["Q"], *a["st"], a["K"], *a["kst"], a["V"], *a["vst"], a["cq"], a["ck"], a["B"], a["T"],
-                            a["Tk"], a["Hq"], a["Hkv"], a["D"], a["causal"], a["scale"], a["O"], a["c"], a["s"], None)
+                            a["Tk"], a["Hq"], a["Hkv"], a["D"], a["causal"], a["scale"], a["O"], a["c"], a["s"], a["wk"],
+                            a["nb"], None)
 
 
 def _paged(lib, **kw):
@@ -138,6 +139,18 @@ def test_attention_refusals(lib):
         assert call(**{name: (516, 128)}) == SHAPE and call(**{name: (512, 12)}) == SHAPE
         assert call(**{name: (120, 128)}) == SHAPE and call(**{name: (512, -128)}) == SHAPE
         assert call(**{name: ((1 << 21) + 8, 128)}) == UNSUPPORTED
+
+
+def test_attention_workspace(lib):
+    """Few queries of many keys need one; prompts and few keys do not."""
+    f = lib.kq_attention_workspace_bytes
+    need = f(2, 10, 5000, 1, 4, 2, 128)
+    assert need > 0
+    assert all(f(B, T, 704, 1, 4, 2, 128) == 0 for B in (1, 2, 7) for T in (1, 10, 100, 1000))     # as the binding relies on
+    assert f(1, 8192, 8192, 0, 32, 8, 128) == 0
+    assert f(2, 10, 5000, 1, 4, 3, 128) == 0 and f(0, 10, 5000, 1, 4, 2, 128) == 0
+    assert _attention(lib, Tk=5000) == WORKSPACE and _attention(lib, Tk=5000, wk=P, nb=need - 1) == WORKSPACE
+    assert _attention(lib, Tk=5000, wk=ODD16, nb=need) == ALIGN
 
 
 def test_paged_refusals(lib):

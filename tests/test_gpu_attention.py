@@ -82,6 +82,56 @@ def test_many_tiles(kq, dtype, D):
         check(O[rows, h], o, tau, dtype, f"head {h}")
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(4, 2, 128, "bf16"), (3, 3, 72, "fp16"), (8, 1, 64, "bf16"), (2, 1, 32, "fp16"),
+                                            (2, 2, 96, "bf16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_split_keys(kq, Hq, Hkv, D, dtype, causal):
+    """Few queries of many keys: split over the keys.  Sequences without keys, without queries, with fewer keys than
+    queries, and rows of no sequence, among them."""
+    q, k = [3, 0, 20, 1, 70, 5, 9], [1500, 40, 700, 0, 100, 130, 4]
+    cq, ck = cumulative(q) + 2, cumulative(k) + 7
+    T, Tk = int(cq[-1]) + 4, int(ck[-1]) + 9
+    Q, K, V = heads((T, Hq, D), dtype, 70, 1.5), heads((Tk, Hkv, D), dtype, 71), heads((Tk, Hkv, D), dtype, 72)
+    for t, c in ((Q, cq), (K, ck), (V, ck)):
+        t[:c[0]] = float("nan")
+        t[c[-1]:] = float("nan")
+    K[ck[0]:ck[1]] *= torch.linspace(0.3, 3.0, 1500).to(DT[dtype]).cuda()[:, None, None]
+    assert kq.attention_workspace_bytes(len(q), T, Tk, True, Hq, Hkv, D) > 0
+    O = torch.full((T, Hq, D), 7.0, dtype=DT[dtype], device="cuda")
+    kq.attention(Q, K, V, on_gpu(cq), on_gpu(ck), causal=causal, O=O)
+    o, tau = _expect(Q, K, V, cq, ck, causal, dtype)
+    o[:2] = o[-4:] = 7.0
+    check(O, o, tau, dtype)
+    if D == 128:
+        codes, scales = kq.attention(Q, K, V, on_gpu(cq), on_gpu(ck), causal=causal, fp8=True)
+        check_codes(codes[2:-4], scales[2:-4], o[2:-4], tau[2:-4])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_split_keys_hidden_nan(kq, dtype):
+    """As test_hidden_nan_and_infinities, with the keys split; one sequence, no cu."""
+    Q, K, V = heads((6, 2, 64), dtype, 80), heads((2000, 1, 64), dtype, 81), heads((2000, 1, 64), dtype, 82)
+    V[1996, 0, 3], V[1997, 0, 4], V[100, 0, 9] = float("nan"), float("inf"), float("-inf")
+    K[1998, 0, 7] = float("nan")
+    assert kq.attention_workspace_bytes(1, 6, 2000, False, 2, 1, 64) > 0
+    o, tau = _expect(Q, K, V, [0, 6], [0, 2000], True, dtype)
+    assert np.isfinite(o[0, 0, 3]) and np.isnan(o[2, 0, 3]) and np.isneginf(o[0, 0, 9]) and np.isnan(o[4]).all()
+    check(kq.attention(Q, K, V), o, tau, dtype)
+
+
+def test_split_keys_workspace(kq):
+    """A given workspace serves; one that is too small is refused."""
+    Q, K, V = heads((5, 4, 128), "bf16", 90), heads((3000, 2, 128), "bf16", 91), heads((3000, 2, 128), "bf16", 92)
+    ref = kq.attention(Q, K, V)
+    nb = kq.attention_workspace_bytes(1, 5, 3000, False, 4, 2, 128)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    assert np.array_equal(raw(kq.attention(Q, K, V, workspace=ws)), raw(ref))
+    with pytest.raises(kq.KQError):
+        kq.attention(Q, K, V, workspace=ws[:nb - 256])
+    with pytest.raises(ValueError):
+        kq.attention(Q, K, V, workspace=ws.int())
+
+
 def test_large_scores(kq):
     """Scores of tens of thousands: the softmax is one key's, whatever the order of the maxima."""
     Q, K, V, cq, ck = _case("single", 2, 2, 64, "fp16", 9)

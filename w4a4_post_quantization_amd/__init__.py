@@ -43,7 +43,7 @@ __all__ = ["mfma_fp4_probe", "load", "lib_path", "abi_version", "status_str", "l
            "lowrank_down", "lowrank_down_workspace_bytes", "transform_quantize_lowrank",
            "svd_lowrank", "svd_lowrank_workspace_bytes", "fp8_scale_cols", "quantize_fp8", "rmsnorm_quantize_fp8",
            "fp8_linear", "fp8_gated_linear", "fp8_gated_linear_workspace_bytes",
-           "attention", "cache_append", "paged_attention", "paged_attention_workspace_bytes",
+           "attention", "attention_workspace_bytes", "cache_append", "paged_attention", "paged_attention_workspace_bytes",
            "KQError"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -136,7 +136,9 @@ def load():
     f32 = ctypes.c_float
     lib.kq_attention.restype = i32
     lib.kq_attention.argtypes = [i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, i32, i32, i32, i32,
-                                 f32, vp, vp, vp, vp]
+                                 f32, vp, vp, vp, vp, sz, vp]
+    lib.kq_attention_workspace_bytes.restype = sz
+    lib.kq_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32]
     lib.kq_cache_append.restype = i32
     lib.kq_cache_append.argtypes = [i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp,
                                     i64, i32, vp]
@@ -867,8 +869,30 @@ def _attn_out(torch, rows, H, D, dtype, fp8, O, codes, scales, index):
     return O, _same(O, "O", dtype, (rows, H, D), index), None, None
 
 
+def attention_workspace_bytes(B, T, Tk, packed, Hq, Hkv, D):
+    """Workspace bytes kq_attention needs on the current device (0: none); packed: whether cu is given."""
+    return load().kq_attention_workspace_bytes(B, T, Tk, packed, Hq, Hkv, D)
+
+
+def _workspace(torch, workspace, index, need, *sizes):
+    """Address and bytes of a call's workspace, made here where none is given and need(*sizes) asks for one; and the
+    workspace itself, to be held until the call."""
+    if workspace is not None:
+        return (_same(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), index) or None,
+                workspace.numel(), workspace)
+    if torch._C._cuda_getDevice() == index:
+        nb = need(*sizes)
+    else:
+        with torch.cuda.device(index):
+            nb = need(*sizes)
+    if not nb:
+        return None, 0, None
+    workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
+    return workspace.data_ptr(), nb, workspace
+
+
 def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False, O=None, codes=None, scales=None,
-              stream=None):
+              workspace=None, stream=None):
     """Attention of packed sequences.  Q [T][Hq][D], K and V [Tk][Hkv][D], fp16 or bf16, Hq a multiple of Hkv (head h
     reads key head h Hkv // Hq), D a multiple of 8 up to 128; any strides that are multiples of 8 (the values
     of a row next to each other), so views of a projection's output serve.  cu_q, cu_k (int32 [B + 1]): where each
@@ -876,9 +900,10 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     one sequence.  causal: query i of Lq sees the keys j <= i + Lk - Lq of Lk.  scale (above 0) defaults to
     D ** -0.5.  A query that sees no key gets zeros; rows outside all sequences are left as they were.  Returns O
     [T][Hq][D] in the inputs' dtype, or with fp8 (D 128) codes [T][Hq * 128] and scales as quantize_fp8 gives them,
-    which fp8_linear takes."""
+    which fp8_linear takes.  workspace: a uint8 device tensor of attention_workspace_bytes bytes (256-byte aligned; few
+    queries of many keys need one); by default one is taken from torch's allocator."""
     if stream is not None:
-        return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales)
+        return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales, workspace)
     torch = _torch()
     shape = T, Hq, D = _heads3(Q, "Q")
     Tk, Hkv, _ = _heads3(K, "K")
@@ -898,8 +923,11 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     elif cu_k is not None:
         raise ValueError("cu_k is given without cu_q")
     out, o, c, s = _attn_out(torch, T, Hq, D, dtype, fp8, O, codes, scales, index)
+    wk = nb = None
+    if workspace is not None or Tk > 704:                    # no fewer keys are split: spared a library call
+        wk, nb, workspace = _workspace(torch, workspace, index, attention_workspace_bytes, B, T, Tk, cq is not None, Hq, Hkv, D)
     _call(torch, "kq_attention", index, (dt, *q, *k, *v, cq, ck, B, T, Tk, Hq, Hkv, D, 1 if causal else 0,
-                                         D ** -0.5 if scale is None else scale, o, c, s))
+                                         D ** -0.5 if scale is None else scale, o, c, s, wk, nb or 0))
     return out
 
 
@@ -974,19 +1002,7 @@ def paged_attention(Q, kcache, vcache, table, lengths, kscales=None, vscales=Non
     kc, vc, ks, vs, pages, page, tb, width, ln = _cache(torch, kcache, vcache, kscales, vscales, table, lengths, dtype, B,
                                                         Hkv, D, index)
     out, o, c, s = _attn_out(torch, B, Hq, D, dtype, fp8, O, codes, scales, index)
-    if workspace is not None:
-        wk = _same(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), index)
-        nb = workspace.numel()
-    else:
-        if torch._C._cuda_getDevice() == index:
-            nb = paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page)
-        else:
-            with torch.cuda.device(index):
-                nb = paged_attention_workspace_bytes(B, Hq, Hkv, D, width, page)
-        wk = None
-        if nb:
-            workspace = torch.empty((nb,), dtype=torch.uint8, device=index)
-            wk = workspace.data_ptr()
+    wk, nb, workspace = _workspace(torch, workspace, index, paged_attention_workspace_bytes, B, Hq, Hkv, D, width, page)
     _call(torch, "kq_paged_attention", index, (dt, *q, kc, vc, ks, vs, pages, page, tb, width, ln, B, Hq, Hkv, D,
-                                               D ** -0.5 if scale is None else scale, o, c, s, wk or None, nb))
+                                               D ** -0.5 if scale is None else scale, o, c, s, wk, nb))
     return out

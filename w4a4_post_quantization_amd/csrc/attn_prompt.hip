@@ -97,14 +97,15 @@ struct Prompt {
   __device__ static int swizzle_k(int row) { return PITCH == 256 ? row & 15 : (row >> 1) & 7; }
   __device__ static int swizzle_v(int row) { return PITCH == 256 ? 4 * (row & 3) : 4 * ((row >> 1) & 1); }
 
-  // One pass over the keys: unnormalized O^T in acc, this lane's part of the sums in l.
-  __device__ static void pass(const AttnArgs& a, const Span& s, int hk, int G, uint8_t* lds, v4u (&q)[KS],
-                              v16f (&acc)[DT], float& l) {
+  // One pass over the keys: unnormalized O^T in acc, this lane's part of the sums in l, the (scaled) maximum in m;
+  // keys kb .. ke - 1 of the sequence
+  __device__ static void pass(const AttnArgs& a, const Span& s, int hk, int G, int kb, int ke, uint8_t* lds, v4u (&q)[KS],
+                              v16f (&acc)[DT], float& l, float& m) {
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5;
     const int off = s.nk - s.nq;                                     // query i sees keys to i + off
     const int rows = s.nq * G, w0 = s.first + 32 * wid;          // the wavefront's first row
-    auto sees_of = [&](int row) { return a.causal ? min(row / G + off + 1, s.nk) : s.nk; };
+    auto sees_of = [&](int row) { return (a.causal ? min(row / G + off + 1, ke) : ke) - kb; };     // counted from kb
     const int nk = max(sees_of(min(s.first + QT, rows) - 1), 0);
     const int tiles = (nk + KT - 1) / KT;                            // that any of the workgroup's rows sees
     const int sees = sees_of(w0 + (lane & 31));                      // keys the lane's row sees
@@ -117,12 +118,12 @@ struct Prompt {
     const uint32_t vk = ck < chunks ? (uint32_t)(row * a.k.ts) + 16 * ck : (uint32_t)KQ_OOB;
     const uint32_t vv = cv < chunks ? (uint32_t)(row * a.v.ts) + 16 * cv : (uint32_t)KQ_OOB;
     const uint32_t lds0 = lds_addr(lds) + 1024 * wid;
-    const uint8_t* const kp = a.k.p + s.k0 * a.k.ts + hk * a.k.hs;
-    const uint8_t* const vp = a.v.p + s.k0 * a.v.ts + hk * a.v.hs;
+    const uint8_t* const kp = a.k.p + (s.k0 + kb) * a.k.ts + hk * a.k.hs;
+    const uint8_t* const vp = a.v.p + (s.k0 + kb) * a.v.ts + hk * a.v.hs;
     // rows behind the last key: zeros; tiles behind the last: nothing.  Tile t goes to slot t % 2.
     auto load = [&](const uint8_t* p, int64_t ts, uint32_t off, uint32_t at, int t) {
       if (t >= tiles) return;
-      const v4i r = rsrc_words(p + (int64_t)KT * t * ts, (int64_t)(s.nk - KT * t - 1) * ts + 2 * a.D);
+      const v4i r = rsrc_words(p + (int64_t)KT * t * ts, (int64_t)(ke - kb - KT * t - 1) * ts + 2 * a.D);
 #pragma unroll
       for (int n = 0; n < LOADS; ++n) lds_load16(r, at + 1024 * NW * n, (int)(off + (uint32_t)(ROWS * NW * n) * (uint32_t)ts));
     };
@@ -139,7 +140,7 @@ struct Prompt {
     for (int i = 0; i < DT; ++i)
       va[i] = PITCH * vr + 16 * ((4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swizzle_v(vr)) + 8 * (lane & 1);
 
-    float m = HIDDEN, base = 0.0f;                                   // scaled: weights are exp2(x c - base)
+    float base = 0.0f;                                               // m scaled: weights are exp2(x c - base)
     v16f x[2][2];                                                    // scores of a tile, in x[t % 2]
     v4u p[4];                                                        // weights of a tile
 #pragma unroll
@@ -147,6 +148,7 @@ struct Prompt {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
     l = 0.0f;
+    m = HIDDEN;
 
     // fragment n of a slot's keys (rows 32 (n % 2) .. + 31, contraction step n / 2) and of its values (row block n % DT,
     // contraction step n / DT)
@@ -350,70 +352,82 @@ __device__ __forceinline__ void store_rows(const AttnArgs& a, const v16f (&acc)[
   }
 }
 
-// Rows row0 .. + 31 again, by the definition: a value that is not finite has reached rows that do not see it (0 times it
-// is not 0), or such values are seen.  A row at a time, 64 keys at a time: a lane has a key's score, then values 2 l and
-// 2 l + 1 of the sum.  Slow (ten vector instructions a key), and small: it needs none of the tiles' registers.
+// Values 2 l and 2 l + 1 (l the lane) of a query's output.
 template <bool BF16>
-__device__ void exact_rows(const AttnArgs& a, const Span& s, int hk, int G, int row0) {
-  const int lane = threadIdx.x & 63, end = min(row0 + 32, s.nq * G);
-  const uint8_t* const kp = a.k.p + s.k0 * a.k.ts + hk * a.k.hs;
-  const uint8_t* const vp = a.v.p + s.k0 * a.v.ts + hk * a.v.hs + 4 * lane;
-  for (int row = row0; row < end; ++row) {
-    const int head = hk * G + row % G, n = a.causal ? min(row / G + s.nk - s.nq + 1, s.nk) : s.nk;
-    const int64_t token = s.q0 + row / G;
-    const uint8_t* const qp = a.q.p + token * a.q.ts + head * a.q.hs;
-    float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-    for (int k0 = 0; k0 < n; k0 += 64) {
-      const bool there = k0 + lane < n;
-      float x = 0.0f;
-      for (int c = 0; c < a.D / 8; ++c) {
-        v4u kw = {0, 0, 0, 0};
-        if (there) kw = *reinterpret_cast<const v4u*>(kp + (int64_t)(k0 + lane) * a.k.ts + 16 * c);
-        float k[8], q[8];
-        unpack8_16<BF16>(kw, k);
-        unpack8_16<BF16>(*reinterpret_cast<const v4u*>(qp + 16 * c), q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x = fmaf(k[e], q[e], x);
-      }
-      x = there ? x * a.c : -INFINITY;
-      float to = fmaxf(m, x);
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) to = fmaxf(to, __shfl_xor(to, off, 64));
-      const float base = to == -INFINITY ? 0.0f : to, f = __builtin_amdgcn_exp2f(m - base);
-      const float p = there ? __builtin_amdgcn_exp2f(x - base) : 0.0f;
-      m = to;
-      l = fmaf(l, f, p);
-      o0 *= f, o1 *= f;
-      for (int i = 0; i < min(64, n - k0); ++i) {
-        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), i));
-        uint32_t v = 0;
-        if (2 * lane < a.D) v = *reinterpret_cast<const uint32_t*>(vp + (int64_t)(k0 + i) * a.v.ts);
-        o0 = fmaf(w, unpack1_16<BF16>((uint16_t)v), o0);
-        o1 = fmaf(w, unpack1_16<BF16>((uint16_t)(v >> 16)), o1);
-      }
-    }
-    const float sum = wave_sum(l), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    o0 *= inv, o1 *= inv;
-    if (a.scales) {                                                  // D is 128
-      uint32_t top = row16_umax(umax32(abs_bits(o0), abs_bits(o1)));
-      top = umax32(top, __shfl_xor(top, 16, 64));
-      top = umax32(top, __shfl_xor(top, 32, 64));
-      const uint32_t byte = f8_scale_byte(top);
-      const float unit = byte == 255u ? 1.0f : f8_inv_scale(byte);
-      const uint32_t w = byte == 255u ? 0x7F7Fu : f8_pack4(o0, o1, 0.0f, 0.0f, unit);
-      *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + (token * a.Hq + head) * 128 + 2 * lane) = (uint16_t)w;
-      const int SC = (int)f8_scale_cols((int64_t)a.Hq * 128);
-      if (lane == 0) a.scales[token * SC + head] = (uint8_t)byte;
-      if (head == a.Hq - 1 && head + 1 + lane < SC) a.scales[token * SC + head + 1 + lane] = 0;
-    } else if (2 * lane < a.D) {
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + ((token * a.Hq + head) * a.D + 2 * lane) * 2) =
-          pack2_16<BF16>(o0, o1);
-    }
+__device__ __forceinline__ void store_pair(const AttnArgs& a, int64_t token, int head, float o0, float o1) {
+  const int lane = threadIdx.x & 63;
+  if (a.scales) {                                                    // D is 128
+    uint32_t top = row16_umax(umax32(abs_bits(o0), abs_bits(o1)));
+    top = umax32(top, __shfl_xor(top, 16, 64));
+    top = umax32(top, __shfl_xor(top, 32, 64));
+    const uint32_t byte = f8_scale_byte(top);
+    const float unit = byte == 255u ? 1.0f : f8_inv_scale(byte);
+    const uint32_t w = byte == 255u ? 0x7F7Fu : f8_pack4(o0, o1, 0.0f, 0.0f, unit);
+    *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + (token * a.Hq + head) * 128 + 2 * lane) = (uint16_t)w;
+    const int SC = (int)f8_scale_cols((int64_t)a.Hq * 128);
+    if (lane == 0) a.scales[token * SC + head] = (uint8_t)byte;
+    if (head == a.Hq - 1 && head + 1 + lane < SC) a.scales[token * SC + head + 1 + lane] = 0;
+  } else if (2 * lane < a.D) {
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + ((token * a.Hq + head) * a.D + 2 * lane) * 2) =
+        pack2_16<BF16>(o0, o1);
   }
 }
 
+// A row again, by the definition: a value that is not finite has reached a row that does not see it (0 times it
+// is not 0), or such values are seen.  64 keys at a time: a lane has a key's score, then values 2 l and
+// 2 l + 1 of the sum.  Slow (ten vector instructions a key), and small: it needs none of the tiles' registers.
+template <bool BF16>
+__device__ void exact_row(const AttnArgs& a, const Span& s, int hk, int G, int row) {
+  const int lane = threadIdx.x & 63;
+  const uint8_t* const kp = a.k.p + s.k0 * a.k.ts + hk * a.k.hs;
+  const uint8_t* const vp = a.v.p + s.k0 * a.v.ts + hk * a.v.hs + 4 * lane;
+  const int head = hk * G + row % G, n = a.causal ? min(row / G + s.nk - s.nq + 1, s.nk) : s.nk;
+  const int64_t token = s.q0 + row / G;
+  const uint8_t* const qp = a.q.p + token * a.q.ts + head * a.q.hs;
+  float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+  for (int k0 = 0; k0 < n; k0 += 64) {
+    const bool there = k0 + lane < n;
+    float x = 0.0f;
+    for (int c = 0; c < a.D / 8; ++c) {
+      v4u kw = {0, 0, 0, 0};
+      if (there) kw = *reinterpret_cast<const v4u*>(kp + (int64_t)(k0 + lane) * a.k.ts + 16 * c);
+      float k[8], q[8];
+      unpack8_16<BF16>(kw, k);
+      unpack8_16<BF16>(*reinterpret_cast<const v4u*>(qp + 16 * c), q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x = fmaf(k[e], q[e], x);
+    }
+    x = there ? x * a.c : -INFINITY;
+    float to = fmaxf(m, x);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) to = fmaxf(to, __shfl_xor(to, off, 64));
+    const float base = to == -INFINITY ? 0.0f : to, f = __builtin_amdgcn_exp2f(m - base);
+    const float p = there ? __builtin_amdgcn_exp2f(x - base) : 0.0f;
+    m = to;
+    l = fmaf(l, f, p);
+    o0 *= f, o1 *= f;
+    for (int i = 0; i < min(64, n - k0); ++i) {
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), i));
+      uint32_t v = 0;
+      if (2 * lane < a.D) v = *reinterpret_cast<const uint32_t*>(vp + (int64_t)(k0 + i) * a.v.ts);
+      o0 = fmaf(w, unpack1_16<BF16>((uint16_t)v), o0);
+      o1 = fmaf(w, unpack1_16<BF16>((uint16_t)(v >> 16)), o1);
+    }
+  }
+  const float sum = wave_sum(l), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  store_pair<BF16>(a, token, head, o0 * inv, o1 * inv);
+}
+
+// Keys of part z of a sequence's nk, in whole tiles.
+__device__ __forceinline__ int part_begin(int nk, int parts, int z) {
+  const int tiles = (nk + KT - 1) / KT, per = (tiles + parts - 1) / parts;
+  return (int)min((int64_t)nk, (int64_t)z * per * KT);
+}
+
 // Two workgroups on a compute unit, three or four for narrow heads (64: 4096 tokens, 32 / 8 heads, causal 100 and 92 us).
-template <bool BF16, int KS, int DT, int NW>
+// PARTS: the keys are split, blockIdx.y says which part is the workgroup's, and what it finds goes to the workspace,
+// unnormalized: values [part][token][head][32 DT], then maxima and sums of weights [part][token][head][2].
+template <bool BF16, int KS, int DT, int NW, bool PARTS>
 __global__ __launch_bounds__(64 * NW, KS <= 2 ? 4 : KS <= 4 ? 3 : 2) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
   using P = Prompt<BF16, KS, DT, NW>;
   constexpr int QT = P::QT;
@@ -453,7 +467,26 @@ __global__ __launch_bounds__(64 * NW, KS <= 2 ? 4 : KS <= 4 ? 3 : 2) void attn_p
   }
   v16f acc[DT];
   float l;
-  P::pass(a, s, hk, G, lds, q, acc, l);
+  float m;
+  const int kb = PARTS ? part_begin(s.nk, a.parts, blockIdx.y) : 0;
+  P::pass(a, s, hk, G, kb, PARTS ? part_begin(s.nk, a.parts, blockIdx.y + 1) : s.nk, lds, q, acc, l, m);
+  if constexpr (PARTS) {
+    const float sum = half_sum(l);
+    const int row = w0 + (lane & 31);
+    if (row >= rows) return;
+    const int64_t R = a.T * a.Hq, at = blockIdx.y * R + (s.q0 + row / G) * a.Hq + hk * G + row % G;
+    if (half == 0) {
+      float* const ml = a.part + a.parts * R * 32 * DT + 2 * at;
+      ml[0] = m, ml[1] = sum;
+    }
+    float* const o = a.part + at * 32 * DT + 4 * half;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<v4f*>(o + 32 * i + 2 * e) = v4f{acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]};
+    return;
+  }
   lds_barrier();                                                     // the tiles have been read: outputs go there
   float zero = 0.0f;
 #pragma unroll
@@ -461,21 +494,99 @@ __global__ __launch_bounds__(64 * NW, KS <= 2 ? 4 : KS <= 4 ? 3 : 2) void attn_p
 #pragma unroll
     for (int e = 0; e < 16; ++e) zero = fmaf(acc[i][e], 0.0f, zero);
   if (__builtin_expect(__any(!(zero == 0.0f)), 0)) {
-    exact_rows<BF16>(a, s, hk, G, w0);
+    for (int row = w0; row < min(w0 + 32, rows); ++row) exact_row<BF16>(a, s, hk, G, row);
     return;
   }
   const float sum = half_sum(l), inv = sum == 0.0f ? 0.0f : 1.0f / sum;        // a query that sees nothing: zeros
   store_rows<BF16, DT, P::OPITCH>(a, acc, inv, s.q0, hk, G, w0, rows, lds + 32 * P::OPITCH * wid);
 }
 
+// Joins the parts of a row, one wavefront each: lane l has part l's maximum and sum, then values 2 l and 2 l + 1.
+template <bool BF16, int DT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t R = a.T * a.Hq, at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (at >= R) return;
+  const int head = (int)(at % a.Hq), G = a.Hq / a.Hkv, hk = head / G;
+  const int32_t token = (int32_t)(at / a.Hq);
+  // the token's sequence: the first that ends behind it
+  Span s = {0, 0, (int32_t)a.T, (int32_t)a.Tk, 0};
+  if (a.cu_q) {
+    const int32_t T = (int32_t)a.T, Tk = (int32_t)a.Tk;
+    int n = 0;
+    for (int i0 = 0; i0 < a.B; i0 += 64) {
+      const int c = __popcll(__ballot(i0 + lane < a.B && a.cu_q[i0 + lane + 1] <= token));
+      n += c;
+      if (c < 64) break;
+    }
+    const int i = __builtin_amdgcn_readfirstlane(n);
+    if (i >= a.B) return;
+    const int32_t q0 = min(max(a.cu_q[i], 0), T), q1 = min(max(a.cu_q[i + 1], q0), T);
+    const int32_t k0 = min(max(a.cu_k[i], 0), Tk), k1 = min(max(a.cu_k[i + 1], k0), Tk);
+    if (token < q0 || token >= q1) return;
+    s = {q0, k0, q1 - q0, k1 - k0, 0};
+  }
+  float m = -INFINITY, l = 0.0f;
+  if (lane < a.parts) {
+    const float* const ml = a.part + a.parts * R * 32 * DT + 2 * (lane * R + at);
+    m = ml[0], l = ml[1];
+  }
+  float top = m;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+  const float sum = wave_sum(lane < a.parts ? f * l : 0.0f);
+  float o0 = 0.0f, o1 = 0.0f;
+  if (2 * lane < 32 * DT) {
+    const float* const o = a.part + at * 32 * DT + 2 * lane;
+#pragma unroll 4
+    for (int z = 0; z < a.parts; ++z) {
+      const float2 v = *reinterpret_cast<const float2*>(o + z * R * 32 * DT);
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), z));
+      o0 = w == 0.0f ? o0 : fmaf(w, v.x, o0);
+      o1 = w == 0.0f ? o1 : fmaf(w, v.y, o1);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  o0 *= inv, o1 *= inv;
+  if (__builtin_expect(__any(!(fabsf(o0) < INFINITY && fabsf(o1) < INFINITY)), 0))
+    exact_row<BF16>(a, s, hk, G, (token - (int32_t)s.q0) * G + head % G);
+  else
+    store_pair<BF16>(a, token, head, o0, o1);
+}
+
+constexpr int NW = 4, QT = 32 * NW;
+
+int64_t slots_of(int64_t T, int64_t B, bool packed, int G) { return packed ? T * G / QT + B : (T * G + QT - 1) / QT; }
+
+// Parts that the keys are split into where there are few rows: as many as give each compute unit a workgroup (or, of very
+// many tiles, two), of four tiles at least, if they save more tiles' time (0.9 us) than the joining costs, which is a
+// launch and the parts' bytes.  Causal, 32 / 8 heads of 128 in bf16, whole and split (us): 16 queries of 1024 keys 22 and 14,
+// of 4096 65 and 16; 256 of 2048 38 and 24; 700 of 16384 247 and 216, of 1024 24 and (not done) 30.
+int parts_of(int64_t T, int64_t Tk, int64_t B, bool packed, int Hq, int Hkv) {
+  const int64_t groups = slots_of(T, B, packed, Hq / Hkv) * Hkv, tiles = (Tk + KT - 1) / KT, cus = device_cu_count();
+  int64_t parts = cus / groups;
+  if (parts < 2 && tiles >= 128) parts = 2 * cus / groups;
+  parts = parts < tiles / 4 ? parts : tiles / 4;
+  parts = parts < 64 ? parts : 64;
+  if (parts < 2) return 1;
+  return tiles - (tiles + parts - 1) / parts >= 6 + T * Hq * parts / 8192 ? (int)parts : 1;
+}
+
 template <bool BF16, int KS, int DT>
 hipError_t go(const AttnArgs& a, hipStream_t s) {
-  constexpr int NW = 4, QT = 32 * NW;
-  const int64_t rows = a.T * (a.Hq / a.Hkv);
-  const int64_t slots = a.cu_q ? rows / QT + a.B : (rows + QT - 1) / QT;
+  const int64_t slots = slots_of(a.T, a.B, a.cu_q != nullptr, a.Hq / a.Hkv);
   const int64_t grid = a.Hkv % 8 && 8 % a.Hkv == 0 ? (slots + 8 / a.Hkv - 1) / (8 / a.Hkv) * 8 : slots * a.Hkv;
-  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a,
-                     (int32_t)slots);
+  if (a.parts == 1) {
+    hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, false>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a,
+                       (int32_t)slots);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, true>), dim3((unsigned)grid, (unsigned)a.parts), dim3(64 * NW), 0, s,
+                     a, (int32_t)slots);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_join_kernel<BF16, DT>), dim3((unsigned)((a.T * a.Hq + 3) / 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -490,7 +601,14 @@ hipError_t by_width(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attention(bool bf16, const AttnArgs& a, hipStream_t s) {
+size_t attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, bool packed, int Hq, int Hkv, int D) {
+  const int parts = parts_of(T, Tk, B, packed, Hq, Hkv);
+  return parts == 1 ? 0 : (size_t)parts * T * Hq * ((D + 31) / 32 * 32 + 2) * sizeof(float);
+}
+
+hipError_t launch_attention(bool bf16, const AttnArgs& args, hipStream_t s) {
+  AttnArgs a = args;
+  a.parts = parts_of(a.T, a.Tk, a.B, a.cu_q != nullptr, a.Hq, a.Hkv);
   return bf16 ? by_width<true>(a, s) : by_width<false>(a, s);
 }
 

@@ -65,7 +65,11 @@ struct AttnArgs {
   float c;                             // scale log2 e
   void* out;                           // [T][Hq][D], or codes [T][Hq * 128]
   uint8_t* scales;                     // with codes
+  float* part;                         // workspace
+  int32_t parts;                       // set by the launch
 };
+// 0: none needed
+size_t attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, bool packed, int Hq, int Hkv, int D);
 hipError_t launch_attention(bool bf16, const AttnArgs& a, hipStream_t s);
 
 // Pages of keys and values: head h's row r of a page at ((page * Hkv + h) * page_rows + r) * row bytes;

@@ -47,6 +47,12 @@ kq_status check_cache(const void* kc, const void* vc, const uint8_t* ks, const u
   return KQ_OK;
 }
 
+kq_status check_sizes(int64_t B, int64_t T, int64_t Tk, int32_t Hq) {
+  if (T < 1 || Tk < 1 || B < 1) return KQ_ERR_SHAPE;
+  if (T > (1LL << 30) || Tk > (1LL << 30) || T > (1LL << 29) / Hq || B > (1LL << 22) / Hq) return KQ_ERR_UNSUPPORTED;
+  return KQ_OK;
+}
+
 AttnRows rows_of(const void* p, int64_t token, int64_t head) {
   return {static_cast<const uint8_t*>(p), 2 * token, 2 * head};
 }
@@ -57,23 +63,34 @@ constexpr float LOG2E = 1.4426950408889634f;
 
 extern "C" {
 
+size_t kq_attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, int32_t packed, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (check_heads(KQ_DT_F16, Hq, Hkv, D, true) != KQ_OK || check_sizes(B, T, Tk, Hq) != KQ_OK) return 0;
+  return attention_workspace_bytes(B, T, Tk, packed != 0, Hq, Hkv, D);
+}
+
 kq_status kq_attention(int32_t dtype, const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token,
                        int64_t k_head, const void* V, int64_t v_token, int64_t v_head, const int32_t* cu_q,
                        const int32_t* cu_k, int64_t B, int64_t T, int64_t Tk, int32_t Hq, int32_t Hkv, int32_t D,
-                       int32_t causal, float scale, void* O, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+                       int32_t causal, float scale, void* O, uint8_t* codes, uint8_t* scales, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
   if (!Q || !K || !V || !cu_q != !cu_k) return KQ_ERR_NULL;
   kq_status st = check_heads(dtype, Hq, Hkv, D, true);
   if (st == KQ_OK) st = check_output(O, codes, scales, D);
   if (st != KQ_OK) return st;
-  if (T < 1 || Tk < 1 || B < 1 || (!cu_q && B != 1)) return KQ_ERR_SHAPE;
-  if (T > (1LL << 30) || Tk > (1LL << 30) || T > (1LL << 29) / Hq || B > (1LL << 22) / Hq) return KQ_ERR_UNSUPPORTED;
+  st = check_sizes(B, T, Tk, Hq);
+  if (st != KQ_OK) return st;
+  if (!cu_q && B != 1) return KQ_ERR_SHAPE;
   st = check_rows(Q, q_token, q_head, D, 1LL << 40);
   if (st == KQ_OK) st = check_rows(K, k_token, k_head, D, 1LL << 40);
   if (st == KQ_OK) st = check_rows(V, v_token, v_head, D, 1LL << 40);
   if (st != KQ_OK) return st;
   if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return KQ_ERR_ALIGN;
   if (!std::isfinite(scale) || !(scale > 0.0f) || !std::isfinite(scale * LOG2E)) return KQ_ERR_VALUE;
+  const size_t need = attention_workspace_bytes(B, T, Tk, cu_q != nullptr, Hq, Hkv, D);
+  if (need && (!workspace || workspace_bytes < need)) return KQ_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 256)) return KQ_ERR_ALIGN;
   AttnArgs a;
+  a.part = static_cast<float*>(workspace);
   a.q = rows_of(Q, q_token, q_head);
   a.k = rows_of(K, k_token, k_head);
   a.v = rows_of(V, v_token, v_head);
