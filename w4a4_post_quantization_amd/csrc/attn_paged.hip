@@ -172,6 +172,12 @@ __device__ __forceinline__ void store_row(const float* o, const PagedArgs& a, in
 // Floats of a partial result: 16 heads' sums, then their maxima and their sums of weights.
 template <int DP> constexpr int PART = 16 * DP + 32;
 
+// Wavefronts of a workgroup and workgroups on a compute unit, which together fill its LDS with rings.  (Four wavefronts and
+// half as many workgroups wait longer at a piece's end: 37 sequences of 50 to 4000 in 16 bits 70 and 64 us, 160 of 200 to
+// 8000 in 8 bits 261 and 250; one wavefront each leaves more to join, two of 131072 in 8 bits 112 and 107.)
+constexpr int NW = 2;
+constexpr int resident(bool wide, int DP) { return wide && DP == 128 ? 2 : wide || DP == 128 ? 4 : 8; }
+
 // A row of rows that has no page.
 constexpr uint32_t NOWHERE = 0xFFFFFFFFu;
 
@@ -472,39 +478,69 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
   }
 }
 
-// Joins what the runs left of units they share: each run that begins inside a unit (the first of those in it) is a
-// workgroup's, for 16 / ROWS of the unit's heads; ROWS rows of 16 threads take the unit's runs in turn for each head, four at
-// a time.  Further workgroups write zeros for the sequences without keys, 64 each.
+// Joins what the runs left of units they share; ROWS rows of 16 threads take a unit's runs in turn for each head, four at a
+// time.  ROWS = 4 (many units): each run that begins inside a unit (the first of those in it) is a workgroup's,
+// for four of the unit's heads, and further workgroups write zeros for the sequences without keys, 64 each.
+// ROWS = 16 (many runs of each unit): a workgroup for each unit and head.
 template <bool BF16, int DP, int ROWS>
 __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int groups) {
   constexpr int HEADS = 16 / ROWS, AT = 4;
   __shared__ float so[16][DP + 2];
   const Pages& c = a.c;
-  const int k = threadIdx.x >> 4, i = threadIdx.x & 15;
+  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16, HH = c.Hkv * HC;
+  const int k = threadIdx.x >> 4, i = threadIdx.x & 15, lane = threadIdx.x & 63;
   float sum[8], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-  if (blockIdx.x >= (uint32_t)((W - 1) * groups)) {
-    const int b0 = 64 * (blockIdx.x - (W - 1) * groups), b = b0 + (threadIdx.x & 63);
-    uint64_t none = __ballot(b < c.B && c.lengths[b] <= 0);
-    for (; none; none &= none - 1)
-      for (int h = k; h < a.Hq; h += 16) store_row<BF16>(sum, a, b0 + __builtin_ctzll(none), h, i);
-    return;
+  const int hd = blockIdx.x % groups * HEADS + k / ROWS;
+  int64_t N, x0, begin;                                      // all blocks; the unit's first; its first run's first
+  int b, unit, nb, w0;                                       // w0: the unit's first run
+  if constexpr (ROWS == 4) {
+    if (blockIdx.x >= (uint32_t)((W - 1) * groups)) {
+      const int b0 = 64 * (blockIdx.x - (W - 1) * groups);
+      uint64_t none = __ballot(b0 + lane < c.B && c.lengths[b0 + lane] <= 0);
+      for (; none; none &= none - 1)
+        for (int h = k; h < a.Hq; h += 16) store_row<BF16>(sum, a, b0 + __builtin_ctzll(none), h, i);
+      return;
+    }
+    const int w = blockIdx.x / groups + 1;
+    const Run* const runs = reinterpret_cast<const Run*>(a.part + (int64_t)2 * W * PART<DP>);
+    N = runs[0].N;
+    const Run u = runs[w];
+    W = (int)min((int64_t)W, N);
+    if (w >= W || u.j0 == 0) return;
+    x0 = run_start(w, N, W) - u.j0;
+    w0 = w - 1;
+    begin = run_start(w0, N, W);
+    if (begin > x0) return;                                  // the run before began inside it, too
+    b = u.b, unit = u.unit, nb = u.nb;
+  } else {
+    const int at = blockIdx.x / groups;
+    b = at / HH, unit = at % HH;
+    int before = 0, all = 0, own = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 64) {
+      const int n = b0 + lane < c.B ? blocks_in<NW>(held(c, c.lengths[b0 + lane])) : 0;
+      all += n;
+      before += b0 + lane < b ? n : 0;
+      own += b0 + lane == b ? n : 0;
+    }
+    N = (int64_t)__builtin_amdgcn_readlane(wave_scan(all), 63) * HH;
+    nb = __builtin_amdgcn_readlane(wave_scan(own), 63);
+    if (nb == 0) {                                           // no keys: zeros
+      if (k == 0 && hd < min(16, G - 16 * (unit % HC))) store_row<BF16>(sum, a, b, unit / HC * G + 16 * (unit % HC) + hd, i);
+      return;
+    }
+    W = (int)min((int64_t)W, N);
+    x0 = (int64_t)__builtin_amdgcn_readlane(wave_scan(before), 63) * HH + (int64_t)unit * nb;
+    w0 = (int)(((x0 + 1) * W - 1) / N);
+    begin = run_start(w0, N, W);
+    if (run_start(w0 + 1, N, W) >= x0 + nb) return;          // one run has it all
   }
-  const int w = blockIdx.x / groups + 1, hd = blockIdx.x % groups * HEADS + k / ROWS;
-  const Run* const runs = reinterpret_cast<const Run*>(a.part + (int64_t)2 * W * PART<DP>);
-  const int64_t N = runs[0].N;
-  const Run u = runs[w];
-  W = (int)min((int64_t)W, N);
-  if (w >= W || u.j0 == 0) return;
-  const int64_t x0 = run_start(w, N, W) - u.j0;              // the unit's first block
-  const int64_t before = run_start(w - 1, N, W);
-  if (before > x0) return;                                   // the run before began inside it, too
-  const int G = a.Hq / c.Hkv, HC = (G + 15) / 16, h0 = 16 * (u.unit % HC);
+  const int h0 = 16 * (unit % HC);
   // the last run with a block of the unit: ((x + 1) W - 1) / N for its last block x
-  const int last = (int)(((x0 + u.nb) * W - 1) / N);
+  const int last = (int)(((x0 + nb) * W - 1) / N);
   if (hd < min(16, G - h0)) {
-    for (int v0 = w - 1 + k % ROWS; v0 <= last; v0 += ROWS * AT) {
+    for (int v0 = w0 + k % ROWS; v0 <= last; v0 += ROWS * AT) {
       float mv[AT], lv[AT];
       v4f ov[AT][2];
 #pragma unroll
@@ -513,7 +549,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int
         mv[t] = -INFINITY, lv[t] = 0.0f;
         ov[t][0] = ov[t][1] = v4f{0.f, 0.f, 0.f, 0.f};
         if (v <= last) {
-          const float* const part = a.part + (int64_t)(2 * v + (v == w - 1 && before < x0 ? 1 : 0)) * PART<DP>;
+          const float* const part = a.part + (int64_t)(2 * v + (v == w0 && begin < x0 ? 1 : 0)) * PART<DP>;
           mv[t] = part[16 * DP + hd], lv[t] = part[16 * DP + 16 + hd];
           if (8 * i < DP) {
             ov[t][0] = *reinterpret_cast<const v4f*>(part + DP * hd + 8 * i);
@@ -562,14 +598,14 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] *= inv;
-  store_row<BF16>(sum, a, u.b, u.unit / HC * G + h0 + hd, i);
+  store_row<BF16>(sum, a, b, unit / HC * G + h0 + hd, i);
 }
 
 template <bool BF16, int DP, int ROWS>
-hipError_t join(const PagedArgs& a, int W, int heads, hipStream_t s) {
+hipError_t join(const PagedArgs& a, int W, int64_t units, int heads, hipStream_t s) {
   const int groups = (heads + 16 / ROWS - 1) / (16 / ROWS);
-  hipLaunchKernelGGL((paged_join_kernel<BF16, DP, ROWS>), dim3((unsigned)((W - 1) * groups + (a.c.B + 63) / 64)), dim3(256), 0, s,
-                     a, W, groups);
+  const int64_t grid = ROWS == 4 ? (int64_t)(W - 1) * groups + (a.c.B + 63) / 64 : units * groups;
+  hipLaunchKernelGGL((paged_join_kernel<BF16, DP, ROWS>), dim3((unsigned)grid), dim3(256), 0, s, a, W, groups);
   return hipGetLastError();
 }
 
@@ -631,12 +667,6 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   }
 }
 
-// Wavefronts of a workgroup and workgroups on a compute unit, which together fill its LDS with rings.  (Four wavefronts and
-// half as many workgroups wait longer at a piece's end: 37 sequences of 50 to 4000 in 16 bits 70 and 64 us, 160 of 200 to
-// 8000 in 8 bits 261 and 250; one wavefront each leaves more to join, two of 131072 in 8 bits 112 and 107.)
-constexpr int NW = 2;
-constexpr int resident(bool wide, int DP) { return wide && DP == 128 ? 2 : wide || DP == 128 ? 4 : 8; }
-
 // A unit is one workgroup's, and nothing is joined (so no workspace is needed), where tables hold up to 640 keys, or up to 2048 and there is a unit
 // for every compute unit: 32 / 8 heads of 128, whole and dealt (us): one sequence of 500 9.4 and 9.6, 1000 14 and 9.9; 8 of
 // 1000 16.3 and 15.7; 64 of 0 to 2000 in 8 bits 38 and 44; 300 of 100 in 16 bits 43 and 46; 160 of 200 to 8000 in 8 bits 281 and
@@ -671,7 +701,7 @@ hipError_t go(const PagedArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   const int heads = G < 16 ? G : 16;
   // many runs of each unit: 16 at once for a head; else as few workgroups as there can be (1023 joins 10 and 5 us)
-  return W > 16 * units ? join<BF16, DP, 16>(a, W, heads, s) : join<BF16, DP, 4>(a, W, heads, s);
+  return W > 16 * units ? join<BF16, DP, 16>(a, W, units, heads, s) : join<BF16, DP, 4>(a, W, units, heads, s);
 }
 
 }  // namespace
