@@ -106,6 +106,44 @@ def test_nan_that_is_seen(kq):
     check(kq.paged_attention(Q, *c.args()), o, tau, "bf16")
 
 
+@pytest.mark.parametrize("dtype,cache", [("fp16", "fp16"), ("bf16", "bf16"), ("fp16", "fp8")])
+def test_many_small_weights(kq, dtype, cache):
+    """One key far above 30000 others, whose values alone count: weights near 2^-23 of the largest keep their
+    precision."""
+    n = 30000
+    c = Cache([n], 1, 64, 16, dtype, cache, 80)
+    q = torch.zeros((1, 1, 64), dtype=DT[dtype], device="cuda")
+    q[0, 0, 0] = 1.0
+    k = torch.zeros((n, 64), device="cuda")
+    k[:, 0] = torch.linspace(-0.5, 0.5, n, device="cuda")
+    k[4321, 0] = 16.0
+    v = 1.0 + 0.5 * torch.rand((n, 64), device="cuda")
+    v[4321] = 0.0
+    c.lengths[:] = n
+    kq.cache_append(k.to(DT[dtype])[:, None], v.to(DT[dtype])[:, None], *c.args(), cu=on_gpu(np.array([0, n], np.int32)), **c.scales())
+    if cache == "fp8":
+        from tests.attn_util import widened
+        c.k64, c.v64 = (widened(raw(a).reshape(a.shape), raw(s).reshape(s.shape)) for a, s in ((c.k, c.ks), (c.v, c.vs)))
+    else:
+        c.k64, c.v64 = dbl(c.k), dbl(c.v)
+    o, tau = _expect(q, c, dtype, cache, 1.0)
+    assert 0.001 < o.min() < o.max() < 0.02
+    check(kq.paged_attention(q, *c.args(), **c.scales(), scale=1.0), o, tau, dtype)
+    if cache != "fp8":
+        K, V = (torch.from_numpy(t).to(DT[dtype]).cuda() for t in (c.k64, c.v64))
+        rows = [t[torch.from_numpy(c.table[0]).long().cuda()].transpose(1, 2).reshape(-1, 1, 64)[:n].contiguous() for t in (K, V)]
+        check(kq.attention(q, *rows, scale=1.0), o, tau, dtype)
+
+
+def test_scale_byte_that_is_nan(kq):
+    """Byte 255 makes NaN what uses it, whatever the codes."""
+    c = Cache([40, 40, 40], 1, 64, 16, "bf16", "fp8", 81)
+    c.ks[c.table[0, 1], 0, 3] = 255
+    c.vs[c.table[1, 2], 0, 1] = 255
+    y = dbl(kq.paged_attention(heads((3, 2, 64), "bf16", 82), *c.args(), **c.scales()))
+    assert np.isnan(y[:2]).all() and np.isfinite(y[2]).all()
+
+
 def test_queries_views(kq):
     c = Cache([70, 30, 200], 2, 128, 16, "bf16", "bf16", 14)
     qkv = heads((3, 8, 128), "bf16", 15)
@@ -326,6 +364,30 @@ def test_two_streams(kq):
         torch.cuda.synchronize()
         for (a, b), r, pr in zip(out, ref, pref):
             assert np.array_equal(raw(a), r) and np.array_equal(raw(b), pr)
+
+
+def test_memory_of_a_given_stream(kq):
+    """Outputs and workspaces that calls make on a given stream are memory of that stream."""
+    c = Cache([3000, 50], 2, 128, 16, "bf16", "bf16", 85)
+    args, Q = c.args(), heads((2, 4, 128), "bf16", 86)
+    K, V = heads((3000, 2, 128), "bf16", 87), heads((3000, 2, 128), "bf16", 88)
+    calls = [lambda s: kq.paged_attention(Q, *args, stream=s), lambda s: kq.paged_attention(Q, *args, fp8=True, stream=s),
+             lambda s: kq.attention(Q, K, V, stream=s), lambda s: kq.attention(K, K, V, fp8=True, stream=s)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        expect = call(None)
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        before = {s["address"] for s in torch.cuda.memory_snapshot()}
+        out = call(side)
+        assert all(s["stream"] == side.cuda_stream for s in torch.cuda.memory_snapshot() if s["address"] not in before)
+        torch.cuda.synchronize()
+        for a, b in zip(expect if isinstance(expect, tuple) else (expect,), out if isinstance(out, tuple) else (out,)):
+            assert np.array_equal(raw(a), raw(b))
+        del out
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert kq.cache_append(K[:2], V[:2], *args, stream=side)[0] is c.k
+    torch.cuda.synchronize()
 
 
 def test_refusals(kq):

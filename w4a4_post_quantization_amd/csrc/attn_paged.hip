@@ -118,9 +118,9 @@ __device__ __forceinline__ void lds_load16_at(uint32_t lds, const void* p) {
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
 }
 
-// 2^(byte - 127)
+// 2^(byte - 127); 255 is NaN
 __device__ __forceinline__ float e8m0_value(uint32_t byte) {
-  return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
 }
 
 // Eight E4M3 codes as 16-bit values (exact).
@@ -195,6 +195,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
   constexpr int KS = DP / 32, DT = DP / 16;
   constexpr int RING = 2 * SLOT;
   constexpr bool PB = BF16 || !WIDE;                         // the weights' 16-bit type
+  constexpr float LIFT = PB ? 0.0f : 6.0f;
   static_assert(PART<DP> * 4 <= SLOT, "a slot takes a wavefront's results");
   __shared__ __align__(1024) uint8_t lds[NW * RING];
   const Pages& c = a.c;
@@ -384,7 +385,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][e] *= f;
       }
-      const float base = m == -INFINITY ? 0.0f : m;
+      const float base = (m == -INFINITY ? 0.0f : m) - LIFT;
       float pr[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -392,8 +393,8 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
         l += pr[e];
         if constexpr (!WIDE) pr[e] *= vscale[e];
       }
-      // a weight is hi + lo, each of 16 bits: relative error 2^-16 (bf16), 2^-22 (fp16, at most 2^8; below
-      // 2^-14 an absolute one of 2^-25)
+      // a weight is hi + lo, each of 16 bits: relative error 2^-16 (bf16), 2^-22 (fp16; or 2^-31 of the largest, as
+      // they are held 2^LIFT larger, to 2^14 at most)
       v4u hi, lo;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
