@@ -842,10 +842,12 @@ def _rows3(t, name, dtype, shape, index):
     raise ValueError(f"{name} is on {t.device}, the first tensor on GPU {index}")
 
 
-def _heads3(t, name):
-    if not isinstance(t, _torch().Tensor) or t.dim() != 3:
-        raise ValueError(f"{name} must be a 3-D torch.Tensor [tokens, heads, D]")
-    return t.shape
+def _heads3(torch, t, name):
+    if isinstance(t, torch.Tensor):
+        shape = t.shape
+        if len(shape) == 3:
+            return shape
+    raise ValueError(f"{name} must be a 3-D torch.Tensor [tokens, heads, D]")
 
 
 def _ints(torch, t, name, shape, index):
@@ -905,8 +907,8 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     if stream is not None:
         return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales, workspace)
     torch = _torch()
-    shape = T, Hq, D = _heads3(Q, "Q")
-    Tk, Hkv, _ = _heads3(K, "K")
+    shape = T, Hq, D = _heads3(torch, Q, "Q")
+    Tk, Hkv, _ = _heads3(torch, K, "K")
     dtype, index = Q.dtype, Q.get_device()
     dt = _dtype16(torch, dtype, "Q")
     q = _rows3(Q, "Q", dtype, shape, index)
@@ -938,10 +940,10 @@ def _vector(t, name):
 
 
 def _cache(torch, kcache, vcache, kscales, vscales, table, lengths, dtype, B, Hkv, D, index):
-    """Addresses and sizes of a paged cache: (k, v, ks, vs), pages, page, table, width, lengths."""
+    """Addresses and sizes of a paged cache: k, v, ks, vs, pages, page, table, width, lengths."""
     if not isinstance(kcache, torch.Tensor) or kcache.dim() != 4:
         raise ValueError("kcache must be a 4-D torch.Tensor [pages, heads, page, D]")
-    pages, _, page, _ = kcache.shape
+    pages, _, page, _ = kshape = kcache.shape
     shape = (pages, Hkv, page, D)
     ks = vs = None
     if (kscales is None) != (vscales is None):
@@ -950,10 +952,18 @@ def _cache(torch, kcache, vcache, kscales, vscales, table, lengths, dtype, B, Hk
         dtype = torch.float8_e4m3fn
         ks = _same(kscales, "kscales", torch.uint8, shape[:3], index)
         vs = _same(vscales, "vscales", torch.uint8, shape[:3], index)
-    k, v = _same(kcache, "kcache", dtype, shape, index), _same(vcache, "vcache", dtype, shape, index)
-    width = _matrix(table, "table")[1]
-    return (k, v, ks, vs, pages, page, _same(table, "table", torch.int32, (B, width), index), width,
-            _same(lengths, "lengths", torch.int32, (B,), index))
+    width, i32 = _matrix(table, "table")[1], torch.int32
+    try:
+        # one test of all four; below, what is wrong
+        if (kcache.dtype is dtype and vcache.dtype is dtype and table.dtype is i32 and lengths.dtype is i32
+                and kshape == shape and vcache.shape == shape and table.shape[0] == B and lengths.shape == (B,)
+                and kcache.get_device() == vcache.get_device() == table.get_device() == lengths.get_device() == index >= 0
+                and kcache.is_contiguous() and vcache.is_contiguous() and table.is_contiguous() and lengths.is_contiguous()):
+            return (kcache.data_ptr(), vcache.data_ptr(), ks, vs, pages, page, table.data_ptr(), width, lengths.data_ptr())
+    except AttributeError:
+        pass
+    return (_same(kcache, "kcache", dtype, shape, index), _same(vcache, "vcache", dtype, shape, index), ks, vs, pages, page,
+            _same(table, "table", i32, (B, width), index), width, _same(lengths, "lengths", i32, (B,), index))
 
 
 def cache_append(K, V, kcache, vcache, table, lengths, cu=None, kscales=None, vscales=None, stream=None):
@@ -967,7 +977,7 @@ def cache_append(K, V, kcache, vcache, table, lengths, cu=None, kscales=None, vs
     if stream is not None:
         return _on_fp8(stream, K, cache_append, V, kcache, vcache, table, lengths, cu, kscales, vscales)
     torch = _torch()
-    shape = T, Hkv, D = _heads3(K, "K")
+    shape = T, Hkv, D = _heads3(torch, K, "K")
     dtype, index = K.dtype, K.get_device()
     dt = _dtype16(torch, dtype, "K")
     k, v = _rows3(K, "K", dtype, shape, index), _rows3(V, "V", dtype, shape, index)
@@ -994,7 +1004,7 @@ def paged_attention(Q, kcache, vcache, table, lengths, kscales=None, vscales=Non
         return _on_fp8(stream, Q, paged_attention, kcache, vcache, table, lengths, kscales, vscales, scale, fp8, O, codes,
                        scales, workspace)
     torch = _torch()
-    shape = B, Hq, D = _heads3(Q, "Q")
+    shape = B, Hq, D = _heads3(torch, Q, "Q")
     dtype, index = Q.dtype, Q.get_device()
     dt = _dtype16(torch, dtype, "Q")
     q = _rows3(Q, "Q", dtype, shape, index)

