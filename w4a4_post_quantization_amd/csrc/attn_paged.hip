@@ -1,13 +1,13 @@
 // Attention of one new token a sequence over pages of cached keys and values, and the pages' filling.
 //
-// The cache's bytes bound it.  The batch's keys are cut into blocks of 128 (a key head's blocks after one
+// The cache's bytes bound it.  The batch's keys are cut into blocks of 64 (a key head's blocks after one
 // another, then the next head's, then the next sequence's) and the blocks are dealt to a fixed number of
 // workgroups in equal runs, whatever the lengths: a run may end inside a head's keys and begin inside
 // another's.  The part of a run in one head is a piece.  Pieces that are whole heads go out at once; of a head
 // that several runs share, each leaves its unnormalized sum, maximum and sum of weights in the
 // workspace (a run has two such at most), and a second kernel joins them in a fixed order.
 //
-// Within a run, each of four wavefronts takes 32 keys of a block, through a ring of two slots of its own in
+// Within a run, each of two wavefronts takes 32 keys of a block, through a ring of two slots of its own in
 // LDS: the next block's loads (the next piece's first ones, too) are in flight while the present one is
 // multiplied, and the loop has no barrier.  As for prompts everything is transposed:
 // S^T = K Q^T with the key head's queries as 16 columns, O^T += V^T P^T in the order of keys in which the
@@ -121,9 +121,25 @@ __device__ __forceinline__ void lds_load16_at(uint32_t lds, const void* p) {
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
 }
 
-// 2^(byte - 127); 255 is NaN
+// 2^(byte - 127); 0 stands for 2^-127, which is no normal float, and 255 for NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+
+// The scales of sixteen bytes.  Where none is 0 or 255 a shift and a mask do (the tests of each byte cost a call of one
+// short sequence 0.3 us).
+__device__ __forceinline__ void e8m0_values(const uint32_t (&w)[4], float (&f)[16]) {
+  float lo = INFINITY, hi = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int at = 8 * (i & 3);
+    f[i] = __uint_as_float((at < 24 ? w[i >> 2] << (23 - at) : w[i >> 2] >> 1) & 0x7F800000u);
+    lo = fminf(lo, f[i]), hi = fmaxf(hi, f[i]);
+  }
+  if (__builtin_expect(__any(!(lo > 0.0f && hi < INFINITY)), 0)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = e8m0_value((w[i >> 2] >> (8 * (i & 3))) & 255u);
+  }
 }
 
 // Eight E4M3 codes as 16-bit values (exact).
@@ -353,18 +369,13 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
             t[s] = mfma16<BF16>(widen8<BF16>(k16[2], k16[3]), q[2 * i + 1], t[s]);
           }
       }
-      float vscale[8];
+      float scale[16];                                       // of the lane's eight keys, then of its values
+      float* const vscale = scale + 8;
       if constexpr (!WIDE) {
+        const uint32_t* const bytes = reinterpret_cast<const uint32_t*>(sk + 64 * PITCH + 4 * g);
+        e8m0_values({bytes[0], bytes[4], bytes[8], bytes[12]}, scale);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t kb = *reinterpret_cast<const uint32_t*>(sk + 64 * PITCH + 16 * s + 4 * g);
-          const uint32_t vb = *reinterpret_cast<const uint32_t*>(sk + 64 * PITCH + 32 + 16 * s + 4 * g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            t[s][e] *= e8m0_value((kb >> (8 * e)) & 255u);
-            vscale[4 * s + e] = e8m0_value((vb >> (8 * e)) & 255u);
-          }
-        }
+        for (int e = 0; e < 8; ++e) t[e / 4][e & 3] *= scale[e];
       }
       if (n[0] + n[1] < 32) {
 #pragma unroll
