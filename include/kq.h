@@ -437,7 +437,7 @@ kq_status kq_attention(int32_t dtype, const void* Q, int64_t q_token, int64_t q_
 /* Writes new tokens' keys and values: lengths already count them.  Sequence s's new tokens are rows cu[s] ..
  * cu[s + 1] - 1 of K and V (int32 [B + 1], ascending; NULL: one token each, T = B), the last of them at
  * position lengths[s] - 1.  K, V: as kq_attention, head strides to 2^40.  Tokens whose position is
- * outside the table, and rows outside all sequences, are not written.  T <= 2^30. */
+ * outside the table, and rows outside all sequences, are not written.  T <= 2^25. */
 kq_status kq_cache_append(int32_t dtype, const void* K, int64_t k_token, int64_t k_head, const void* V, int64_t v_token,
                           int64_t v_head, const int32_t* cu, int64_t B, int64_t T, int32_t Hkv, int32_t D,
                           const int32_t* table, int64_t width, const int32_t* lengths, void* kcache, void* vcache,

@@ -180,7 +180,7 @@ def test_append_refusals(lib):
     _heads_refusals(call)
     _cache_refusals(call)
     assert call(T=0) == SHAPE and call(cu=None) == SHAPE and call(B=0) == SHAPE
-    assert call(T=(1 << 30) + 1) == UNSUPPORTED
+    assert call(T=(1 << 25) + 1) == UNSUPPORTED
     assert call(st=(120, 128)) == SHAPE and call(vst=(260, 128)) == SHAPE
 
 

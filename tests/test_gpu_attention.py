@@ -202,10 +202,11 @@ def test_entries_that_make_no_sense(kq, cq, ck):
     assert (room[:300] == 5).all() and (room[600:] == 5).all() and torch.isfinite(room).all()
 
 
-def test_many_sequences(kq):
-    """More sequences than a wavefront has lanes, some empty."""
+@pytest.mark.parametrize("B,most", [(201, 9), (5000, 3)])
+def test_many_sequences(kq, B, most):
+    """More sequences than a wavefront has lanes, and than its square, some empty."""
     rng = np.random.default_rng(50)
-    cu = cumulative(rng.integers(0, 9, size=201))
+    cu = cumulative(rng.integers(0, most, size=B))
     T = int(cu[-1])
     Q, K, V = heads((T, 2, 64), "fp16", 51), heads((T, 1, 64), "fp16", 52), heads((T, 1, 64), "fp16", 53)
     check(kq.attention(Q, K, V, on_gpu(cu)), *_expect(Q, K, V, cu, cu, True, "fp16"), "fp16")

@@ -233,9 +233,10 @@ def test_append_drops_what_has_no_place(kq):
         assert np.array_equal(raw(g).reshape(-1), np.ascontiguousarray(e).view(np.uint8).reshape(-1))
 
 
-def test_append_many_sequences(kq):
+@pytest.mark.parametrize("B", [150, 4500])
+def test_append_many_sequences(kq, B):
     rng = np.random.default_rng(25)
-    new = [int(n) for n in rng.integers(0, 4, size=150)]
+    new = [int(n) for n in rng.integers(0, 4, size=B)]
     c = Cache([n + 5 for n in new], 1, 64, 16, "bf16", "bf16", 26)
     K, V = heads((sum(new), 1, 64), "bf16", 27), heads((sum(new), 1, 64), "bf16", 28)
     expect = _append_expect(c, K, V, cumulative(new), "bf16", "bf16")

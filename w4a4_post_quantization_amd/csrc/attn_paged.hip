@@ -635,15 +635,8 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a) {
   if (t >= a.T) return;
   int64_t b = t, behind = 1;                                 // tokens of the sequence from this one on
   if (a.cu) {
-    int n = 0;
-    for (int i0 = 0; i0 < c.B; i0 += 64) {
-      const int i = i0 + lane;
-      const int k = __popcll(__ballot(i < c.B && a.cu[i + 1] <= t));
-      n += k;
-      if (k < 64) break;
-    }
-    b = __builtin_amdgcn_readfirstlane(n);
-    if (b >= c.B || t < a.cu[b]) return;
+    b = last_before(c.B, [&](int i) { return a.cu[i] <= t; });
+    if (t < a.cu[b] || t >= a.cu[b + 1]) return;
     behind = a.cu[b + 1] - t;
   }
   const int64_t at = (int64_t)c.lengths[b] - behind;

@@ -41,8 +41,9 @@ struct Span {
 };
 
 // Sequence i's rows begin at slot G cu_q[i] / QT + i of the grid, which leaves each at least as many
-// slots as it has tiles without anyone having summed the tiles: a slot finds its sequence by counting
-// the starts up to itself, 64 at a time.  Entries are held to 0 .. T and to their order.
+// slots as it has tiles without anyone having summed the tiles: a slot finds its sequence by the
+// starts up to itself, looking at 64 at a time (4000 sequences of 9 tokens, 8 / 2 heads of 64: 61 us;
+// looking at all of them took 151).  Entries are held to 0 .. T and to their order.
 template <int QT>
 __device__ bool find_span(const AttnArgs& a, int G, int32_t slot, Span& s) {
   if (!a.cu_q) {
@@ -51,25 +52,21 @@ __device__ bool find_span(const AttnArgs& a, int G, int32_t slot, Span& s) {
   }
   const int lane = threadIdx.x & 63;
   const int32_t T = (int32_t)a.T, Tk = (int32_t)a.Tk;
-  // lane i: sequence i0 + i's four entries, so that the search's loads are the only ones
-  int32_t q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-  int i = 0;
-  for (int i0 = 0; i0 < a.B; i0 += 64) {
-    const int at = min(i0 + lane, a.B - 1);
-    const int32_t lq0 = a.cu_q[at], lq1 = a.cu_q[at + 1], lk0 = a.cu_k[at], lk1 = a.cu_k[at + 1];
-    const bool before = i0 + lane < a.B && min(max(lq0, 0), T) * G / QT + i0 + lane <= slot;
-    const int c = __popcll(__ballot(before));
-    if (c > 0) {
-      i = i0 + c - 1;
-      q0 = __builtin_amdgcn_readlane(lq0, c - 1), q1 = __builtin_amdgcn_readlane(lq1, c - 1);
-      k0 = __builtin_amdgcn_readlane(lk0, c - 1), k1 = __builtin_amdgcn_readlane(lk1, c - 1);
-    }
-    if (c < 64) break;
-  }
+  auto start = [&](int32_t q, int i) { return min(max(q, 0), T) * G / QT + i; };
+  int lo = 0, len = a.B;
+  narrow(lo, len, [&](int i) { return start(a.cu_q[i], i) <= slot; });
+  // lane l: candidate lo + l's four entries, so that up to 64 sequences take one load
+  const int at = lo + min(lane, len - 1);
+  const int32_t lq0 = a.cu_q[at], lq1 = a.cu_q[at + 1], lk0 = a.cu_k[at], lk1 = a.cu_k[at + 1];
+  const int found = __popcll(__ballot(lane < len && start(lq0, at) <= slot));  // as an int: it may be 0, less 1
+  const int l = found > 0 ? found - 1 : 0, i = lo + l;
+  int32_t q0 = __builtin_amdgcn_readlane(lq0, l), q1 = __builtin_amdgcn_readlane(lq1, l);
+  int32_t k0 = __builtin_amdgcn_readlane(lk0, l), k1 = __builtin_amdgcn_readlane(lk1, l);
   q0 = min(max(q0, 0), T), q1 = min(max(q1, q0), T);
   k0 = min(max(k0, 0), Tk), k1 = min(max(k1, k0), Tk);
-  s = {q0, k0, q1 - q0, k1 - k0, (slot - (q0 * G / QT + i)) * QT};
-  return s.first >= 0 && s.first < s.nq * G;                 // entries out of order lead to no slot below 0
+  const int tile = slot - (q0 * G / QT + i);                 // below 0 for no sequence, and by entries out of order
+  s = {q0, k0, q1 - q0, k1 - k0, tile * QT};
+  return tile >= 0 && s.first < s.nq * G;
 }
 
 // acc + both halves of a packed pair (their products by 1 are exact).
@@ -513,18 +510,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (at >= R) return;
   const int head = (int)(at % a.Hq), G = a.Hq / a.Hkv, hk = head / G;
   const int32_t token = (int32_t)(at / a.Hq);
-  // the token's sequence: the first that ends behind it
+  // the token's sequence: the last that begins up to it
   Span s = {0, 0, (int32_t)a.T, (int32_t)a.Tk, 0};
   if (a.cu_q) {
     const int32_t T = (int32_t)a.T, Tk = (int32_t)a.Tk;
-    int n = 0;
-    for (int i0 = 0; i0 < a.B; i0 += 64) {
-      const int c = __popcll(__ballot(i0 + lane < a.B && a.cu_q[i0 + lane + 1] <= token));
-      n += c;
-      if (c < 64) break;
-    }
-    const int i = __builtin_amdgcn_readfirstlane(n);
-    if (i >= a.B) return;
+    const int i = last_before(a.B, [&](int i) { return a.cu_q[i] <= token; });
     const int32_t q0 = min(max(a.cu_q[i], 0), T), q1 = min(max(a.cu_q[i + 1], q0), T);
     const int32_t k0 = min(max(a.cu_k[i], 0), Tk), k1 = min(max(a.cu_k[i + 1], k0), Tk);
     if (token < q0 || token >= q1) return;

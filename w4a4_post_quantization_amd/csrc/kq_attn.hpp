@@ -51,6 +51,29 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Narrows [lo, lo + len) to at most 64 candidates for the last i with before(i), which holds up to some i and for none
+// behind it: 64 samples at a time.  (Whatever `before` says, the candidates stay within the given range.)
+template <class F>
+__device__ __forceinline__ void narrow(int& lo, int& len, F before) {
+  const int lane = threadIdx.x & 63;
+  while (len > 64) {
+    const int step = (len + 63) / 64;
+    const int c = __popcll(__ballot(lane * step < len && before(lo + lane * step)));
+    const int skip = c > 1 ? (c - 1) * step : 0;
+    lo += skip;
+    len = min(step, len - skip);
+  }
+}
+
+// The last i of [0, n) with before(i) (0 where it holds for none), the same in every lane.
+template <class F>
+__device__ __forceinline__ int last_before(int n, F before) {
+  int lo = 0, len = n;
+  narrow(lo, len, before);
+  const int lane = threadIdx.x & 63, c = __popcll(__ballot(lane < len && before(lo + min(lane, len - 1))));
+  return __builtin_amdgcn_readfirstlane(lo + (c > 0 ? c - 1 : 0));
+}
+
 // Rows of heads: element (token, head, d) at p[token * ts + head * hs + d].
 struct AttnRows {
   const uint8_t* p;

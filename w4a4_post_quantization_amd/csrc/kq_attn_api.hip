@@ -118,7 +118,7 @@ kq_status kq_cache_append(int32_t dtype, const void* K, int64_t k_token, int64_t
   if (st == KQ_OK) st = check_cache(kcache, vcache, kscales, vscales, pages, page, table, width, lengths, B);
   if (st != KQ_OK) return st;
   if (T < 1 || (!cu && T != B)) return KQ_ERR_SHAPE;
-  if (T > (1LL << 30)) return KQ_ERR_UNSUPPORTED;
+  if (T > (1LL << 25)) return KQ_ERR_UNSUPPORTED;            // a launch is at most 2^32 threads
   st = check_rows(K, k_token, k_head, D, 1LL << 40);
   if (st == KQ_OK) st = check_rows(V, v_token, v_head, D, 1LL << 40);
   if (st != KQ_OK) return st;
