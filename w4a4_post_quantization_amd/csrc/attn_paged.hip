@@ -188,6 +188,56 @@ __device__ __forceinline__ void store_row(const float* o, const PagedArgs& a, in
   }
 }
 
+// A row's sixteen lanes' eight values each: a cached row's values d = 8 i .. + 7 in float32 (not scaled).
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void cached_8(const uint8_t* row, int i, float* x) {
+  if constexpr (WIDE) {
+    unpack8_16<BF16>(*reinterpret_cast<const v4u*>(row + 16 * i), x);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * i);
+    unpack8_16<true>(widen8<true>(w.x, w.y), x);
+  }
+}
+
+// One head's sum over the keys [begin, end) of sequence b again, by the definition, one weight and one product a key.  For
+// sums that are not finite: with a weight as the sum of two 16-bit numbers, of which the second may be negative or zero, a
+// value that is infinite comes out as NaN.  Sixteen lanes a head, values d = 8 i .. + 7 in sum; the maximum in m, the sum of
+// weights (2^lift larger, as the pieces' are) in l.  Slow, some 70 instructions a key, and small.
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void keys_again(const PagedArgs& a, int b, int head, int begin, int end, float lift, int i, float& m,
+                                           float& l, float* sum) {
+  const Pages& c = a.c;
+  const int RB = WIDE ? 2 * c.D : c.D, hk = head / (a.Hq / c.Hkv);
+  const bool there = 8 * i < c.D;
+  float q[8], x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = x[e] = sum[e] = 0.0f;
+  if (there) unpack8_16<BF16>(*reinterpret_cast<const v4u*>(a.q + b * a.qs + head * a.qh + 16 * i), q);
+  m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+  for (int key = begin; key < end; ++key) {
+    const int page = c.table[(int64_t)b * c.width + key / c.page];
+    if (page < 0 || page >= c.pages) continue;
+    const int64_t row = ((int64_t)page * c.Hkv + hk) * c.page + key % c.page;
+    if (there) cached_8<BF16, WIDE>(c.k + row * RB, i, x);
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(x[e], q[e], s);
+    s = row16_sum(s);
+    if constexpr (!WIDE) s *= e8m0_value(c.ks[row]);
+    s *= a.scale;
+    const float to = fmaxf(m, s), base = to == -INFINITY ? 0.0f : to;
+    const float f = __builtin_amdgcn_exp2f(m - base);
+    float w = __builtin_amdgcn_exp2f(s - base + lift);
+    m = to;
+    l = fmaf(l, f, w);
+    if constexpr (!WIDE) w *= e8m0_value(c.vs[row]);
+    if (there) cached_8<BF16, WIDE>(c.v + row * RB, i, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, x[e], sum[e] * f);
+  }
+}
+
 // Floats of a partial result: 16 heads' sums, then their maxima and their sums of weights.
 template <int DP> constexpr int PART = 16 * DP + 32;
 
@@ -467,11 +517,17 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
           for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, o[u][DP * hd + 8 * i + e], sum[e]);
         }
       }
+      const int head = p.unit / HC * G + 16 * (p.unit % HC) + hd;
+      float zero = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) zero = fmaf(sum[e], 0.0f, zero);
+      if (__builtin_expect(__any(!(zero == 0.0f)), 0))
+        keys_again<BF16, WIDE>(a, p.b, head, BLK * p.j0, (int)min((int64_t)p.len, (int64_t)BLK * p.j1), LIFT, i, top, total, sum);
       if (WHOLE || (p.j0 == 0 && p.j1 == p.nb)) {
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] *= inv;
-        store_row<BF16>(sum, a, p.b, p.unit / HC * G + 16 * (p.unit % HC) + hd, i);
+        store_row<BF16>(sum, a, p.b, head, i);
       } else {
         float* const part = a.part + (int64_t)(2 * w + (first_piece ? 0 : 1)) * PART<DP>;
         if (8 * i < DP) {
