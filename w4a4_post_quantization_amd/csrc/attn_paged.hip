@@ -39,15 +39,16 @@ __device__ __forceinline__ int32_t scalar_at(const int32_t* p, int64_t i) {
 }
 __device__ __forceinline__ int length_of(const Pages& c, int b) { return held(c, scalar_at(c.lengths, b)); }
 
-// Sums over the lanes up to each one.
-__device__ __forceinline__ int wave_scan(int v) {
+// Sums over the lanes up to each one.  Of blocks: B width page <= 2^37 and B <= 2^20, so all sequences together have up to
+// 2^31 + 2^20, which 32 bits hold without a sign.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   const int lane = threadIdx.x & 63;
   // within rows of 16 by shifts, then the rows' totals
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);      // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  const int t0 = __builtin_amdgcn_readlane(v, 15), t1 = __builtin_amdgcn_readlane(v, 31), t2 = __builtin_amdgcn_readlane(v, 47);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);      // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);
+  const uint32_t t0 = __builtin_amdgcn_readlane(v, 15), t1 = __builtin_amdgcn_readlane(v, 31), t2 = __builtin_amdgcn_readlane(v, 47);
   return v + (lane >= 16 ? t0 : 0) + (lane >= 32 ? t1 : 0) + (lane >= 48 ? t2 : 0);
 }
 
@@ -72,36 +73,37 @@ __device__ int64_t find_run(const Pages& c, int HH, int w, int& W, int64_t& N, P
   const int lane = threadIdx.x & 63;
   auto length = [&](int b) { return b < c.B ? held(c, c.lengths[b]) : 0; };
   // up to 64 sequences: the scan that the search needs has the sum, too
-  const int len0 = length(lane), n0 = blocks_in<NW>(len0), upto0 = wave_scan(n0);
-  int all = __builtin_amdgcn_readlane(upto0, 63);
+  const int len0 = length(lane);
+  const uint32_t upto0 = wave_scan(blocks_in<NW>(len0));
+  uint32_t all = __builtin_amdgcn_readlane(upto0, 63);
   if (c.B > 64) {
-    int more = 0;
+    uint32_t more = 0;
     for (int b = 64; b < c.B; b += 64) more += blocks_in<NW>(length(b + lane));
-    all += __builtin_amdgcn_readlane(wave_scan(more), 63);
+    all += (uint32_t)__builtin_amdgcn_readlane(wave_scan(more), 63);
   }
   N = (int64_t)all * HH;
   W = (int)min((int64_t)W, N);
   if (w >= W) return 0;
   const int64_t x = run_start(w, N, W);
-  const int y = (int)(x / HH);                               // the block, counting one unit of each sequence
-  int base = 0;
+  const uint32_t y = (uint32_t)(x / HH);                     // the block, counting one unit of each sequence
+  uint32_t base = 0;
   for (int b0 = 0; b0 < c.B; b0 += 64) {
     const int len = b0 == 0 ? len0 : length(b0 + lane);
-    const int upto = b0 == 0 ? upto0 : wave_scan(blocks_in<NW>(len));
+    const uint32_t upto = b0 == 0 ? upto0 : wave_scan(blocks_in<NW>(len));
     const uint64_t hit = __ballot(y < base + upto);
     if (hit) {
       const int i = __builtin_ctzll(hit);
       p.b = b0 + i;
       p.len = __builtin_amdgcn_readlane(len, i);
       p.nb = blocks_in<NW>(p.len);
-      const int64_t in = x - (int64_t)(base + __builtin_amdgcn_readlane(upto, i) - p.nb) * HH;
+      const int64_t in = x - (int64_t)(base + (uint32_t)__builtin_amdgcn_readlane(upto, i) - (uint32_t)p.nb) * HH;
       p.unit = (int)(in / p.nb);
       p.j0 = (int)(in % p.nb);
       const int64_t blocks = run_start(w + 1, N, W) - x;
       p.j1 = (int)min((int64_t)p.nb, p.j0 + blocks);
       return blocks;
     }
-    base += __builtin_amdgcn_readlane(upto, 63);
+    base += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
   }
   return 0;
 }
@@ -588,21 +590,21 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int
   } else {
     const int at = blockIdx.x / groups;
     b = at / HH, unit = at % HH;
-    int before = 0, all = 0, own = 0;
+    uint32_t before = 0, all = 0, own = 0;
     for (int b0 = 0; b0 < c.B; b0 += 64) {
-      const int n = b0 + lane < c.B ? blocks_in<NW>(held(c, c.lengths[b0 + lane])) : 0;
+      const uint32_t n = b0 + lane < c.B ? blocks_in<NW>(held(c, c.lengths[b0 + lane])) : 0;
       all += n;
       before += b0 + lane < b ? n : 0;
       own += b0 + lane == b ? n : 0;
     }
-    N = (int64_t)__builtin_amdgcn_readlane(wave_scan(all), 63) * HH;
+    N = (int64_t)(uint32_t)__builtin_amdgcn_readlane(wave_scan(all), 63) * HH;
     nb = __builtin_amdgcn_readlane(wave_scan(own), 63);
     if (nb == 0) {                                           // no keys: zeros
       if (k == 0 && hd < min(16, G - 16 * (unit % HC))) store_row<BF16>(sum, a, b, unit / HC * G + 16 * (unit % HC) + hd, i);
       return;
     }
     W = (int)min((int64_t)W, N);
-    x0 = (int64_t)__builtin_amdgcn_readlane(wave_scan(before), 63) * HH + (int64_t)unit * nb;
+    x0 = (int64_t)(uint32_t)__builtin_amdgcn_readlane(wave_scan(before), 63) * HH + (int64_t)unit * nb;
     w0 = (int)(((x0 + 1) * W - 1) / N);
     begin = run_start(w0, N, W);
     if (run_start(w0 + 1, N, W) >= x0 + nb) return;          // one run has it all
