@@ -530,6 +530,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
   const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
   const float sum = wave_sum(lane < a.parts ? f * l : 0.0f);
+  // Parts that begin behind the last key that the row sees are left out, whatever those keys' values have made of their
+  // sums.  The others count even if their weights vanish (or are none) beside another part's, so that what is not finite
+  // among them is looked at again below.
+  const int32_t row = (token - (int32_t)s.q0) * G + head % G;
+  const int32_t sees = a.causal ? min(row / G + s.nk - s.nq + 1, s.nk) : s.nk;
+  const uint64_t unseen = __ballot(lane < a.parts && part_begin(s.nk, a.parts, lane) >= sees);
   float o0 = 0.0f, o1 = 0.0f;
   if (2 * lane < 32 * DT) {
     const float* const o = a.part + at * 32 * DT + 2 * lane;
@@ -537,14 +543,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     for (int z = 0; z < a.parts; ++z) {
       const float2 v = *reinterpret_cast<const float2*>(o + z * R * 32 * DT);
       const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), z));
-      o0 = w == 0.0f ? o0 : fmaf(w, v.x, o0);
-      o1 = w == 0.0f ? o1 : fmaf(w, v.y, o1);
+      const bool skip = unseen >> z & 1;
+      o0 = skip ? o0 : fmaf(w, v.x, o0);
+      o1 = skip ? o1 : fmaf(w, v.y, o1);
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   o0 *= inv, o1 *= inv;
   if (__builtin_expect(__any(!(fabsf(o0) < INFINITY && fabsf(o1) < INFINITY)), 0))
-    exact_row<BF16>(a, s, hk, G, (token - (int32_t)s.q0) * G + head % G);
+    exact_row<BF16>(a, s, hk, G, row);
   else
     store_pair<BF16>(a, token, head, o0, o1);
 }
