@@ -526,9 +526,9 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
       if (__builtin_expect(__any(!(zero == 0.0f)), 0))
         keys_again<BF16, WIDE>(a, p.b, head, BLK * p.j0, (int)min((int64_t)p.len, (int64_t)BLK * p.j1), LIFT, i, top, total, sum);
       if (WHOLE || (p.j0 == 0 && p.j1 == p.nb)) {
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        const float inv = 1.0f / total;                      // no weight: zeros, whatever the values
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] *= inv;
+        for (int e = 0; e < 8; ++e) sum[e] = total == 0.0f ? 0.0f : sum[e] * inv;
         store_row<BF16>(sum, a, p.b, head, i);
       } else {
         float* const part = a.part + (int64_t)(2 * w + (first_piece ? 0 : 1)) * PART<DP>;
@@ -668,9 +668,9 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int W, int
       for (int e = 0; e < 8; ++e) sum[e] = fmaf(f, so[k + r][8 * i + e], sum[e]);
     }
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const float inv = 1.0f / total;                            // no weight: zeros, whatever the values
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] *= inv;
+  for (int e = 0; e < 8; ++e) sum[e] = total == 0.0f ? 0.0f : sum[e] * inv;
   store_row<BF16>(sum, a, b, unit / HC * G + h0 + hd, i);
 }
 

@@ -415,8 +415,10 @@ __device__ void exact_row(const AttnArgs& a, const Span& s, int hk, int G, int r
       o1 = fmaf(w, unpack1_16<BF16>((uint16_t)(v >> 16)), o1);
     }
   }
-  const float sum = wave_sum(l), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  store_pair<BF16>(a, token, head, o0 * inv, o1 * inv);
+  // no weight at all (no key, or no score above minus infinity): zeros, whatever the values
+  const float sum = wave_sum(l), inv = 1.0f / sum;
+  const bool none = sum == 0.0f;
+  store_pair<BF16>(a, token, head, none ? 0.0f : o0 * inv, none ? 0.0f : o1 * inv);
 }
 
 // Keys of part z of a sequence's nk, in whole tiles.
