@@ -413,7 +413,8 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
  * and to their order.
  * Q, K, V: element (token, head, d) at token * token stride + head * head stride + d, strides in elements,
  * multiples of 8; token strides D to 2^21, head strides 0 to 2^40.  Views of one projection's output
- * [T][(Hq + 2 Hkv) D] are the usual case.  T, Tk <= 2^30, T Hq <= 2^29, B Hq <= 2^22.  scale finite, above 0.
+ * [T][(Hq + 2 Hkv) D] are the usual case.  1 <= T, Tk <= 2^30 (a sequence may have no
+ * queries or no keys; a call may not), T Hq <= 2^29, 1 <= B, B Hq <= 2^22.  scale finite, above 0.
  * workspace: at least kq_attention_workspace_bytes bytes (packed: whether cu is given), 256-byte aligned (0: none needed; few
  * queries of many keys are split over the keys, and it holds the parts.  It depends on the device's compute units:
  * ask on the device that runs the call).  Calls that share a workspace must not overlap, replays of captured
@@ -437,7 +438,7 @@ kq_status kq_attention(int32_t dtype, const void* Q, int64_t q_token, int64_t q_
 /* Writes new tokens' keys and values: lengths already count them.  Sequence s's new tokens are rows cu[s] ..
  * cu[s + 1] - 1 of K and V (int32 [B + 1], ascending; NULL: one token each, T = B), the last of them at
  * position lengths[s] - 1.  K, V: as kq_attention, head strides to 2^40.  Tokens whose position is
- * outside the table, and rows outside all sequences, are not written.  T <= 2^25. */
+ * outside the table, and rows outside all sequences, are not written.  1 <= T <= 2^25. */
 kq_status kq_cache_append(int32_t dtype, const void* K, int64_t k_token, int64_t k_head, const void* V, int64_t v_token,
                           int64_t v_head, const int32_t* cu, int64_t B, int64_t T, int32_t Hkv, int32_t D,
                           const int32_t* table, int64_t width, const int32_t* lengths, void* kcache, void* vcache,

@@ -845,8 +845,10 @@ def _rows3(t, name, dtype, shape, index):
 def _heads3(torch, t, name):
     if isinstance(t, torch.Tensor):
         shape = t.shape
-        if len(shape) == 3:
+        if len(shape) == 3 and 0 not in shape:
             return shape
+        if len(shape) == 3:
+            raise ValueError(f"{name} must hold at least one token, head and value (got shape {tuple(shape)})")
     raise ValueError(f"{name} must be a 3-D torch.Tensor [tokens, heads, D]")
 
 
@@ -900,7 +902,8 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     of a row next to each other), so views of a projection's output serve.  cu_q, cu_k (int32 [B + 1]): where each
     sequence's queries and keys begin and the last one's end; cu_k defaults to cu_q, and without either all is
     one sequence.  causal: query i of Lq sees the keys j <= i + Lk - Lq of Lk.  scale (above 0) defaults to
-    D ** -0.5.  A query that sees no key gets zeros; rows outside all sequences are left as they were.  Returns O
+    D ** -0.5.  A query that sees no key gets zeros; rows outside all sequences are left as they were.  T and Tk are 1 at
+    least (a sequence may be empty, or have no keys; a call may not).  Returns O
     [T][Hq][D] in the inputs' dtype, or with fp8 (D 128) codes [T][Hq * 128] and scales as quantize_fp8 gives them,
     which fp8_linear takes.  workspace: a uint8 device tensor of attention_workspace_bytes bytes (256-byte aligned; few
     queries of many keys need one); by default one is taken from torch's allocator."""
