@@ -395,10 +395,12 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
  *   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j - max),  over the keys j that the query sees;
  *
  * a query that sees no key (or none with a score above minus infinity) gets zeros, and what is at keys that
- * it does not see (NaN and infinities included) does not reach it.  Scores, maxima and sums are float32; the weights are rounded to the
- * 16-bit type for the product with the values (in an 8-bit cache: to bf16, for fp16 outputs to the sum of
- * two bf16 numbers).  They are divided by their sum at the end, so values beyond 10^30 may overflow.  The
- * order of additions is fixed for one device: equal inputs of equal shape give equal bits.
+ * it does not see (NaN and infinities included) does not reach it.  Scores, maxima and sums are float32.  For the
+ * product with the values kq_attention rounds a weight to the 16-bit type (relative error 2^-8 bf16, 2^-11 fp16);
+ * kq_paged_attention multiplies it as the sum of two 16-bit numbers, of the cache's type or, for 8-bit rows, bf16
+ * (2^-16 bf16, 2^-22 fp16).  What a weight loses besides is below 2^-31 of the largest (fp16) or 2^-125; one that
+ * vanishes makes NaN of an infinite value.  Sums are divided by the weights' sum at the end, so values beyond 10^30
+ * may overflow.  The order of additions is fixed for one device: equal inputs of equal shape give equal bits.
  *
  * Outputs: O [rows][Hq][D] in the 16-bit type, or, where codes and scales are given instead (O NULL; D = 128
  * only), E4M3 codes [rows][Hq 128] with one E8M0 byte for each head, [rows][kq_fp8_scale_cols(Hq 128)],

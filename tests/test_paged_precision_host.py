@@ -1,0 +1,34 @@
+"""The paged attention's tolerance, without a GPU: it takes weights of two 16-bit numbers and refuses weights of one."""
+
+import numpy as np
+import pytest
+
+from oracle import fp8
+from tests import paged_pairs as pairs
+from tests.attn_util import check
+
+
+@pytest.mark.parametrize("dtype,cache", pairs.KINDS)
+@pytest.mark.parametrize("n,D", [(8, 128), (30, 64), (17, 128)])
+def test_one_number_is_not_enough(dtype, cache, n, D):
+    k, v = pairs.rows(n, 1, D, dtype, cache, n)
+    K, V = (pairs.cached(t, cache)[:, 0] for t in (k, v))
+    q = pairs.rounded(np.random.default_rng(1).normal(size=(4, D)), dtype).double().numpy()
+    o, tau = pairs.expect(q, K, V, D ** -0.5, dtype, cache)
+    two, one = (pairs.multiplied(q, K, V, D ** -0.5, dtype, cache, m) for m in (2, 1))
+    check(pairs.rounded(two, dtype), o, tau, dtype)
+    with pytest.raises(AssertionError, match="of the bound"):
+        check(pairs.rounded(one, dtype), o, tau, dtype)
+
+
+@pytest.mark.parametrize("dtype,cache", [kind for kind in pairs.KINDS if kind[1] != "fp16"])
+def test_codes_of_one_number(dtype, cache):
+    """(One fp16 number is within what codes allow: 30 weights' errors of 2^-12 add up to 4e-5 here, and the bound of
+    float32 scores alone is 1e-4.)"""
+    k, v = pairs.rows(30, 1, 128, dtype, cache, 5)
+    K, V = (pairs.cached(t, cache)[:, 0] for t in (k, v))
+    q = pairs.rounded(np.random.default_rng(2).normal(size=(16, 128)), dtype).double().numpy()
+    o, tau = pairs.expect(q, K, V, 128 ** -0.5, dtype, cache)
+    for m, good in ((2, True), (1, False)):
+        codes, scales = fp8.quantize(pairs.multiplied(q, K, V, 128 ** -0.5, dtype, cache, m))
+        assert (not fp8.check_codes(codes, scales, o, tau)) == good
