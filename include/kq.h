@@ -335,8 +335,9 @@ kq_status kq_w4a4_linear_t(int32_t fmt,
  * current device must be the one that the stream and the pointers belong to. */
 enum { KQ_DT_F16 = 0, KQ_DT_BF16 = 1 };
 enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1, KQ_ACT_GELU_TANH = 2 };
-/* Or'ed into the dtype of kq_fp8_linear or the act of kq_fp8_gated_linear: every product of two codes
- * exact and added in float32, as calls of up to 16 tokens always do, and a gated call's activation by
+/* Or'ed into the dtype of kq_attention: see there.  Or'ed into the dtype of kq_fp8_linear or the act of
+ * kq_fp8_gated_linear: every product of two codes exact and added in float32, as calls of up to 16 tokens
+ * always do, and a gated call's activation by
  * the library's exponential and a rounded quotient.  Without it, calls of more tokens use the 8-bit matrix
  * instructions, which cut off (towards zero) each of eight consecutive products at 2^(E - 13), E the largest
  * of the eight's sums of two exponents (a subnormal code's exponent is that of the smallest normal one).
@@ -396,9 +397,11 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
  *
  * a query that sees no key (or none with a score above minus infinity) gets zeros, and what is at keys that
  * it does not see (NaN and infinities included) does not reach it.  Scores, maxima and sums are float32.  For the
- * product with the values kq_attention rounds a weight to the 16-bit type (relative error 2^-8 bf16, 2^-11 fp16);
- * kq_paged_attention multiplies it as the sum of two 16-bit numbers, of the cache's type or, for 8-bit rows, bf16
- * (2^-16 bf16, 2^-22 fp16).  What a weight loses besides is below 2^-31 of the largest (fp16) or 2^-125; one that
+ * product with the values kq_attention rounds a weight to the 16-bit type (relative error 2^-8 bf16, 2^-11 fp16), which
+ * moves 16-bit outputs by less than their own rounding, and codes by 0.2 to 1% of the norm (E4M3 itself 2.7%).
+ * kq_paged_attention, and kq_attention with KQ_FP8_PRECISE or'ed into its dtype, multiply it as the sum of two 16-bit
+ * numbers, of the cache's type or, for 8-bit rows, bf16 (2^-16 bf16, 2^-22 fp16; codes 0.03%); prompts take up to 1.4
+ * times as long so.  What a weight loses besides is below 2^-31 of the largest (fp16) or 2^-125; one that
  * vanishes makes NaN of an infinite value.  Sums are divided by the weights' sum at the end, so values beyond 10^30
  * may overflow.  The order of additions is fixed for one device: equal inputs of equal shape give equal bits.
  *

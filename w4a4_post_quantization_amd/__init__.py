@@ -896,7 +896,7 @@ def _workspace(torch, workspace, index, need, *sizes):
 
 
 def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False, O=None, codes=None, scales=None,
-              workspace=None, stream=None):
+              workspace=None, stream=None, precise=False):
     """Attention of packed sequences.  Q [T][Hq][D], K and V [Tk][Hkv][D], fp16 or bf16, Hq a multiple of Hkv (head h
     reads key head h Hkv // Hq), D a multiple of 8 up to 128; any strides that are multiples of 8 (the values
     of a row next to each other), so views of a projection's output serve.  cu_q, cu_k (int32 [B + 1]): where each
@@ -906,9 +906,12 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     least (a sequence may be empty, or have no keys; a call may not).  Returns O
     [T][Hq][D] in the inputs' dtype, or with fp8 (D 128) codes [T][Hq * 128] and scales as quantize_fp8 gives them,
     which fp8_linear takes.  workspace: a uint8 device tensor of attention_workspace_bytes bytes (256-byte aligned; few
-    queries of many keys need one); by default one is taken from torch's allocator."""
+    queries of many keys need one); by default one is taken from torch's allocator.  precise: the softmax's weights
+    multiply the values as two 16-bit numbers each, as paged_attention's always do, not rounded to one (KQ_FP8_PRECISE
+    in kq.h, with what it gives and costs)."""
     if stream is not None:
-        return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales, workspace)
+        return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales, workspace,
+                       precise=precise)
     torch = _torch()
     shape = T, Hq, D = _heads3(torch, Q, "Q")
     Tk, Hkv, _ = _heads3(torch, K, "K")
@@ -931,7 +934,7 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     wk = nb = None
     if workspace is not None or Tk > 704:                    # no fewer keys are split: spared a library call
         wk, nb, workspace = _workspace(torch, workspace, index, attention_workspace_bytes, B, T, Tk, cq is not None, Hq, Hkv, D)
-    _call(torch, "kq_attention", index, (dt, *q, *k, *v, cq, ck, B, T, Tk, Hq, Hkv, D, 1 if causal else 0,
+    _call(torch, "kq_attention", index, (dt | _PRECISE if precise else dt, *q, *k, *v, cq, ck, B, T, Tk, Hq, Hkv, D, 1 if causal else 0,
                                          D ** -0.5 if scale is None else scale, o, c, s, wk, nb or 0))
     return out
 

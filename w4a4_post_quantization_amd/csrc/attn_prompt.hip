@@ -13,6 +13,12 @@
 // float32 sums or 16-bit weights), which spares most rescalings of the 16 DT accumulators.  fp16 weights are held
 // 2^6 larger, to 2^14 at most, so that what falls under fp16's smallest step is 2^-31 of the largest.
 //
+// The weights are rounded to the 16-bit type for the second product, which keeps it one matrix instruction; 16-bit outputs
+// show little of it (relative error against 64 bits 1.76e-3 bf16, 2.20e-4 fp16; of float32 throughout 1.66e-3 and
+// 2.08e-4), codes fall to the other side of a rounding border here and there (0.6 to 1% of the norm bf16, 0.2% fp16; E4M3
+// itself 2.7%).  PRECISE multiplies a weight as the sum of two 16-bit numbers: 1.66e-3 and 2.08e-4, codes 0.03%; 8192 tokens
+// of 32 / 8 heads of 128 take 693 us and not 495, two images of 4096 with 16 heads of 72 287 and not 204.
+//
 // A step multiplies the next tile's keys while the present tile's exponentials are taken, and the present
 // tile's values while the next maximum is, so that the matrix cores and the vector units have work of
 // the same wavefront side by side.
@@ -83,7 +89,8 @@ __device__ __forceinline__ float add_pair(uint32_t w, float acc) {
 // Scores of masked keys.
 constexpr float HIDDEN = -INFINITY;
 
-template <bool BF16, int KS, int DT, int NW>
+// PRECISE: a weight is multiplied as the sum of two 16-bit numbers, else rounded to one.
+template <bool BF16, int KS, int DT, int NW, bool PRECISE>
 struct Prompt {
   static constexpr int QT = 32 * NW;
   static constexpr float LIFT = BF16 ? 0.0f : 6.0f;
@@ -143,7 +150,7 @@ struct Prompt {
 
     float base = 0.0f;                                               // m scaled: weights are exp2(x c - base)
     v16f x[2][2];                                                    // scores of a tile, in x[t % 2]
-    v4u p[4];                                                        // weights of a tile
+    v4u p[4], pl[4];                                                 // weights of a tile; what their rounding left
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -161,19 +168,25 @@ struct Prompt {
       const v2u lo = lds_tr16(at), hi = lds_tr16(at + 8 * PITCH);
       return v4u{lo[0], lo[1], hi[0], hi[1]};
     };
-    // weights 2 n and 2 n + 1 of the lane's 32; their sum is that of the rounded ones
+    // weights 2 n and 2 n + 1 of the lane's 32; their sum is that of the numbers they are multiplied as (precise: to 2^-16)
     auto weight_pair = [&](const v16f (&y)[2], int n) {
       const int h = n >> 3, e = 2 * (n & 7);
       const float p0 = __builtin_amdgcn_exp2f(fmaf(y[h][e], a.c, -base));
       const float p1 = __builtin_amdgcn_exp2f(fmaf(y[h][e + 1], a.c, -base));
       const uint32_t w = pack2_16<BF16>(p0, p1);
-      l = add_pair<BF16>(w, l);
       p[n >> 2][n & 3] = w;
+      if constexpr (PRECISE) {
+        l += p0 + p1;
+        pl[n >> 2][n & 3] = pack2_16<BF16>(p0 - unpack1_16<BF16>((uint16_t)w), p1 - unpack1_16<BF16>((uint16_t)(w >> 16)));
+      } else {
+        l = add_pair<BF16>(w, l);
+      }
     };
     // The compiler's own order reads each fragment just before its product; these loops keep AHEAD fragments in
     // flight and put a share of the vector work behind each product.  (Heads of 128, 8192 tokens: 512, 497 and 502 us with 2,
-    // 3 and 4; heads of 72 206, 207 and 205; heads of 64 leave registers for a third workgroup with 3.)
-    constexpr int AHEAD = KS == 5 || KS == 6 ? 4 : 3, NK = 2 * KS, NV = 4 * DT;
+    // 3 and 4; heads of 72 206, 207 and 205; heads of 64 leave registers for a third workgroup with 3; PRECISE leaves heads of
+    // 128 registers for 2.)
+    constexpr int AHEAD = KS == 5 || KS == 6 ? 4 : PRECISE && KS == 8 ? 2 : 3, NK = 2 * KS, NV = 4 * DT;
     auto scores = [&](v16f (&y)[2], int slot, auto beside) {
       v4u f[NK];
       v16f z;
@@ -198,6 +211,7 @@ struct Prompt {
       for (int n = 0; n < NV; ++n) {
         if (n + AHEAD < NV) f[n + AHEAD] = value_frag(slot, n + AHEAD);
         acc[n % DT] = mfma32<BF16>(f[n], p[n / DT], acc[n % DT]);
+        if constexpr (PRECISE) acc[n % DT] = mfma32<BF16>(f[n], pl[n / DT], acc[n % DT]);
 #pragma unroll
         for (int i = 16 * n / NV; i < 16 * (n + 1) / NV; ++i) beside(i);
         __builtin_amdgcn_sched_barrier(0);
@@ -245,6 +259,7 @@ struct Prompt {
       step(t, S0);
       scores(x[S1], S1, [&](int n) { weight_pair(x[S0], n); });
       asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]));       // here, not behind the branch
+      if constexpr (PRECISE) asm volatile("" : "+v"(pl[0]), "+v"(pl[1]), "+v"(pl[2]), "+v"(pl[3]));
       hide(x[S1], KT * (t + 1));
       top = HIDDEN;
       values(S0, [&](int n) { compare(x[S1], n); });
@@ -376,7 +391,9 @@ __device__ __forceinline__ void store_pair(const AttnArgs& a, int64_t token, int
 
 // A row again, by the definition: a value that is not finite has reached a row that does not see it (0 times it
 // is not 0), or such values are seen.  64 keys at a time: a lane has a key's score, then values 2 l and
-// 2 l + 1 of the sum.  Slow (ten vector instructions a key), and small: it needs none of the tiles' registers.
+// 2 l + 1 of the sum.  Slow (16 us for 64 keys of a row, 32 rows in turn: of 8192 tokens, 32 / 8 heads of 128, an infinite
+// value at the last key takes the call from 0.5 to 67 ms, at the first 111), and small: it needs none of the tiles'
+// registers.
 template <bool BF16>
 __device__ void exact_row(const AttnArgs& a, const Span& s, int hk, int G, int row) {
   const int lane = threadIdx.x & 63;
@@ -427,12 +444,13 @@ __device__ __forceinline__ int part_begin(int nk, int parts, int z) {
   return (int)min((int64_t)nk, (int64_t)z * per * KT);
 }
 
-// Two workgroups on a compute unit, three or four for narrow heads (64: 4096 tokens, 32 / 8 heads, causal 100 and 92 us).
+// Two workgroups on a compute unit, three or four for narrow heads (64: 4096 tokens, 32 / 8 heads, causal 100 and 92 us); one
+// less where PRECISE's second numbers take the registers.
 // PARTS: the keys are split, blockIdx.y says which part is the workgroup's, and what it finds goes to the workspace,
 // unnormalized: values [part][token][head][32 DT], then maxima and sums of weights [part][token][head][2].
-template <bool BF16, int KS, int DT, int NW, bool PARTS>
-__global__ __launch_bounds__(64 * NW, KS <= 2 ? 4 : KS <= 4 ? 3 : 2) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
-  using P = Prompt<BF16, KS, DT, NW>;
+template <bool BF16, int KS, int DT, int NW, bool PARTS, bool PRECISE>
+__global__ __launch_bounds__(64 * NW, KS <= 2 ? 4 - PRECISE : KS <= 4 ? 3 - PRECISE : 2) void attn_prompt_kernel(AttnArgs a, int32_t slots) {
+  using P = Prompt<BF16, KS, DT, NW, PRECISE>;
   constexpr int QT = P::QT;
   constexpr int LDS = 4 * P::TILE > 32 * NW * P::OPITCH ? 4 * P::TILE : 32 * NW * P::OPITCH;
   __shared__ __align__(1024) uint8_t lds[LDS];
@@ -576,16 +594,16 @@ int parts_of(int64_t T, int64_t Tk, int64_t B, bool packed, int Hq, int Hkv) {
   return tiles - (tiles + parts - 1) / parts >= 6 + T * Hq * parts / 8192 ? (int)parts : 1;
 }
 
-template <bool BF16, int KS, int DT>
+template <bool BF16, int KS, int DT, bool PRECISE>
 hipError_t go(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = slots_of(a.T, a.B, a.cu_q != nullptr, a.Hq / a.Hkv);
   const int64_t grid = a.Hkv % 8 && 8 % a.Hkv == 0 ? (slots + 8 / a.Hkv - 1) / (8 / a.Hkv) * 8 : slots * a.Hkv;
   if (a.parts == 1) {
-    hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, false>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a,
+    hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, false, PRECISE>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a,
                        (int32_t)slots);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, true>), dim3((unsigned)grid, (unsigned)a.parts), dim3(64 * NW), 0, s,
+  hipLaunchKernelGGL((attn_prompt_kernel<BF16, KS, DT, NW, true, PRECISE>), dim3((unsigned)grid, (unsigned)a.parts), dim3(64 * NW), 0, s,
                      a, (int32_t)slots);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -593,13 +611,13 @@ hipError_t go(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF16>
+template <bool BF16, bool PRECISE>
 hipError_t by_width(const AttnArgs& a, hipStream_t s) {
-  if (a.D <= 32) return go<BF16, 2, 1>(a, s);
-  if (a.D <= 64) return go<BF16, 4, 2>(a, s);
-  if (a.D <= 80) return go<BF16, 5, 3>(a, s);
-  if (a.D <= 96) return go<BF16, 6, 3>(a, s);
-  return go<BF16, 8, 4>(a, s);
+  if (a.D <= 32) return go<BF16, 2, 1, PRECISE>(a, s);
+  if (a.D <= 64) return go<BF16, 4, 2, PRECISE>(a, s);
+  if (a.D <= 80) return go<BF16, 5, 3, PRECISE>(a, s);
+  if (a.D <= 96) return go<BF16, 6, 3, PRECISE>(a, s);
+  return go<BF16, 8, 4, PRECISE>(a, s);
 }
 
 }  // namespace
@@ -609,10 +627,11 @@ size_t attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, bool packed, 
   return parts == 1 ? 0 : (size_t)parts * T * Hq * ((D + 31) / 32 * 32 + 2) * sizeof(float);
 }
 
-hipError_t launch_attention(bool bf16, const AttnArgs& args, hipStream_t s) {
+hipError_t launch_attention(bool bf16, bool precise, const AttnArgs& args, hipStream_t s) {
   AttnArgs a = args;
   a.parts = parts_of(a.T, a.Tk, a.B, a.cu_q != nullptr, a.Hq, a.Hkv);
-  return bf16 ? by_width<true>(a, s) : by_width<false>(a, s);
+  if (precise) return bf16 ? by_width<true, true>(a, s) : by_width<false, true>(a, s);
+  return bf16 ? by_width<true, false>(a, s) : by_width<false, false>(a, s);
 }
 
 }  // namespace kq

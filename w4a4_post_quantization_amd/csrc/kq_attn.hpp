@@ -93,7 +93,8 @@ struct AttnArgs {
 };
 // 0: none needed
 size_t attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, bool packed, int Hq, int Hkv, int D);
-hipError_t launch_attention(bool bf16, const AttnArgs& a, hipStream_t s);
+// precise: weights as the sum of two 16-bit numbers
+hipError_t launch_attention(bool bf16, bool precise, const AttnArgs& a, hipStream_t s);
 
 // Pages of keys and values: head h's row r of a page at ((page * Hkv + h) * page_rows + r) * row bytes;
 // scales (8-bit rows only) one byte a row, in the same order.

@@ -73,6 +73,8 @@ kq_status kq_attention(int32_t dtype, const void* Q, int64_t q_token, int64_t q_
                        const int32_t* cu_k, int64_t B, int64_t T, int64_t Tk, int32_t Hq, int32_t Hkv, int32_t D,
                        int32_t causal, float scale, void* O, uint8_t* codes, uint8_t* scales, void* workspace,
                        size_t workspace_bytes, hipStream_t stream) {
+  const bool precise = (dtype & KQ_FP8_PRECISE) != 0;
+  dtype &= ~KQ_FP8_PRECISE;
   if (!Q || !K || !V || !cu_q != !cu_k) return KQ_ERR_NULL;
   kq_status st = check_heads(dtype, Hq, Hkv, D, true);
   if (st == KQ_OK) st = check_output(O, codes, scales, D);
@@ -106,7 +108,7 @@ kq_status kq_attention(int32_t dtype, const void* Q, int64_t q_token, int64_t q_
   a.c = scale * LOG2E;
   a.out = O ? O : codes;
   a.scales = scales;
-  return hip_status(launch_attention(dtype == KQ_DT_BF16, a, stream));
+  return hip_status(launch_attention(dtype == KQ_DT_BF16, precise, a, stream));
 }
 
 kq_status kq_cache_append(int32_t dtype, const void* K, int64_t k_token, int64_t k_head, const void* V, int64_t v_token,
