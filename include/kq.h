@@ -420,8 +420,8 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
  * multiples of 8; token strides D to 2^21, head strides 0 to 2^40.  Views of one projection's output
  * [T][(Hq + 2 Hkv) D] are the usual case.  1 <= T, Tk <= 2^30 (a sequence may have no
  * queries or no keys; a call may not), T Hq <= 2^29, 1 <= B, B Hq <= 2^22.  scale finite, above 0.
- * workspace: at least kq_attention_workspace_bytes bytes (packed: whether cu is given), 256-byte aligned (0: none needed; few
- * queries of many keys are split over the keys, and it holds the parts.  It depends on the device's compute units:
+ * workspace: at least kq_attention_workspace_bytes bytes (packed: whether cu is given), 256-byte aligned (0: none needed, as
+ * for Tk <= 704 whatever else; few queries of more keys are split over the keys, and it holds the parts.  It depends on the device's compute units:
  * ask on the device that runs the call).  Calls that share a workspace must not overlap, replays of captured
  * graphs that hold it included. */
 size_t kq_attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, int32_t packed, int32_t Hq, int32_t Hkv, int32_t D);

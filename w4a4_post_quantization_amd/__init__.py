@@ -932,7 +932,7 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
         raise ValueError("cu_k is given without cu_q")
     out, o, c, s = _attn_out(torch, T, Hq, D, dtype, fp8, O, codes, scales, index)
     wk = nb = None
-    if workspace is not None or Tk > 704:                    # no fewer keys are split: spared a library call
+    if workspace is not None or Tk > 704:                    # else none is needed (kq.h): spared a library call
         wk, nb, workspace = _workspace(torch, workspace, index, attention_workspace_bytes, B, T, Tk, cq is not None, Hq, Hkv, D)
     _call(torch, "kq_attention", index, (dt | _PRECISE if precise else dt, *q, *k, *v, cq, ck, B, T, Tk, Hq, Hkv, D, 1 if causal else 0,
                                          D ** -0.5 if scale is None else scale, o, c, s, wk, nb or 0))

@@ -584,7 +584,10 @@ int64_t slots_of(int64_t T, int64_t B, bool packed, int G) { return packed ? T *
 // many tiles, two), of four tiles at least, if they save more tiles' time (0.9 us) than the joining costs, which is a
 // launch and the parts' bytes.  Causal, 32 / 8 heads of 128 in bf16, whole and split (us): 16 queries of 1024 keys 22 and 14,
 // of 4096 65 and 16; 256 of 2048 38 and 24; 700 of 16384 247 and 216, of 1024 24 and (not done) 30.
+// Up to 704 keys (11 tiles, of which two parts save five) are never split: kq.h says so, and callers spare themselves the
+// question.
 int parts_of(int64_t T, int64_t Tk, int64_t B, bool packed, int Hq, int Hkv) {
+  if (Tk <= 704) return 1;
   const int64_t groups = slots_of(T, B, packed, Hq / Hkv) * Hkv, tiles = (Tk + KT - 1) / KT, cus = device_cu_count();
   int64_t parts = cus / groups;
   if (parts < 2 && tiles >= 128) parts = 2 * cus / groups;
