@@ -9,7 +9,7 @@ DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
 HALF = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}             # half a step, relative
 # A prompt's weight is rounded to the 16-bit type of the second product; fp16 ones are held at 2^6 of the largest or more,
 # so what falls below fp16's smallest step of 2^-24 is at most 2^-31 of the largest weight.  The paged cache's weights are
-# two 16-bit numbers each, beside an 8-bit cache of bf16 (2^-8 of 2^-8); paged_pairs.WEIGHT has what that allows.
+# sums of such numbers and allow less: paged_pairs.WEIGHT.
 WEIGHT = {("fp16", "fp16"): (2.0 ** -11, 2.0 ** -31), ("bf16", "bf16"): (2.0 ** -8, 0.0),
           ("fp16", "fp8"): (2.0 ** -16, 0.0), ("bf16", "fp8"): (2.0 ** -8, 0.0)}
 

@@ -1,5 +1,5 @@
-"""GPU parity of attention with precise weights (two 16-bit numbers each) against the float64 oracle, at the tolerance of the
-paged attention's weights (tests/paged_pairs.py, whose test without a GPU shows that one number does not meet it)."""
+"""GPU parity of attention with precise weights (several 16-bit numbers each) against the float64 oracle, at the tolerance of
+the paged attention's weights (tests/paged_pairs.py, whose test without a GPU shows that one number less does not meet it)."""
 
 import numpy as np
 import pytest
@@ -44,6 +44,17 @@ def test_values_that_nearly_cancel(kq, n, D, dtype):
         check(kq.attention(Q, K, V, causal=causal, precise=True), o, tau, dtype)
     if n == 8:                                              # and the other form is another
         assert not np.array_equal(raw(kq.attention(Q, K, V, precise=True)), raw(kq.attention(Q, K, V)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_number_of_a_weight(kq, dtype):
+    q, k, v = pairs.triples(64, dtype, 3)
+    cq, ck = on_gpu(cumulative([1] * 64)), on_gpu(cumulative([3] * 64))
+    O = kq.attention(q[:, None].cuda().contiguous(), k.reshape(192, 1, 32).cuda(), v.reshape(192, 1, 32).cuda(), cq, ck, scale=1.0,
+                     precise=True)
+    for b in range(64):
+        o, tau = pairs.expect_triple(*(t[b].double().numpy() for t in (q, k, v)))
+        check(O[b, 0], o, tau, dtype, f"sequence {b}")
 
 
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])

@@ -1,4 +1,4 @@
-"""GPU parity of the paged attention at the precision of its weights, two 16-bit numbers each: on values that nearly cancel
+"""GPU parity of the paged attention at the precision of its weights, several 16-bit numbers each: on values that nearly cancel
 (tolerances, and what they tell apart: tests/paged_pairs.py, tests/test_paged_precision_host.py), and in general."""
 
 import numpy as np
@@ -11,10 +11,10 @@ from tests.attn_util import Cache, check, check_codes, cumulative, dbl, heads, o
 pytestmark = pytest.mark.gpu
 
 
-def _filled(kq, lengths, Hkv, D, dtype, cache, width, seed):
-    """A cache whose sequences hold pairs that nearly cancel."""
+def _filled(kq, lengths, Hkv, D, dtype, cache, width, seed, new=None):
+    """A cache whose sequences hold pairs that nearly cancel, or `new`."""
     c = Cache(lengths, Hkv, D, 16, dtype, cache, seed, width=width)
-    new = [pairs.rows(n, Hkv, D, dtype, cache, seed + i) for i, n in enumerate(lengths)]
+    new = new or [pairs.rows(n, Hkv, D, dtype, cache, seed + i) for i, n in enumerate(lengths)]
     K, V = (on_gpu(np.concatenate([t[i].float().numpy() for t in new])).to(new[0][0].dtype) for i in (0, 1))
     kq.cache_append(K, V, *c.args(), cu=on_gpu(cumulative(lengths)), **c.scales())
     if cache == "fp8":
@@ -56,3 +56,14 @@ def test_one_token(kq, Hq, Hkv, D, page, dtype, cache, width):
     check(kq.paged_attention(Q, *c.args(), **c.scales()), o, tau, dtype)
     if D == 128:
         check_codes(*kq.paged_attention(Q, *c.args(), **c.scales(), fp8=True), o, tau)
+
+
+@pytest.mark.parametrize("dtype,cache", pairs.KINDS)
+@pytest.mark.parametrize("width", [None, 100])
+def test_every_number_of_a_weight(kq, dtype, cache, width):
+    q, k, v = pairs.triples(64, dtype, 3)
+    c = _filled(kq, [3] * 64, 1, 32, dtype, cache, width, 5, [(k[b][:, None], v[b][:, None]) for b in range(64)])
+    O = kq.paged_attention(q[:, None].cuda().contiguous(), *c.args(), **c.scales(), scale=1.0)
+    for b in range(64):
+        o, tau = pairs.expect_triple(q[b].double().numpy(), *(pairs.cached(t[b], cache) for t in (k, v)))
+        check(O[b, 0], o, tau, dtype, f"sequence {b}")

@@ -1,4 +1,4 @@
-"""The paged attention's tolerance, without a GPU: it takes weights of two 16-bit numbers and refuses weights of one."""
+"""The paged attention's tolerances, without a GPU: they take the weights' 16-bit numbers and refuse one number less."""
 
 import numpy as np
 import pytest
@@ -15,8 +15,8 @@ def test_one_number_is_not_enough(dtype, cache, n, D):
     K, V = (pairs.cached(t, cache)[:, 0] for t in (k, v))
     q = pairs.rounded(np.random.default_rng(1).normal(size=(4, D)), dtype).double().numpy()
     o, tau = pairs.expect(q, K, V, D ** -0.5, dtype, cache)
-    two, one = (pairs.multiplied(q, K, V, D ** -0.5, dtype, cache, m) for m in (2, 1))
-    check(pairs.rounded(two, dtype), o, tau, dtype)
+    all_, one = (pairs.multiplied(q, K, V, D ** -0.5, dtype, cache, m) for m in (pairs.NUMBERS[cache], 1))
+    check(pairs.rounded(all_, dtype), o, tau, dtype)
     with pytest.raises(AssertionError, match="of the bound"):
         check(pairs.rounded(one, dtype), o, tau, dtype)
 
@@ -29,6 +29,23 @@ def test_codes_of_one_number(dtype, cache):
     K, V = (pairs.cached(t, cache)[:, 0] for t in (k, v))
     q = pairs.rounded(np.random.default_rng(2).normal(size=(16, 128)), dtype).double().numpy()
     o, tau = pairs.expect(q, K, V, 128 ** -0.5, dtype, cache)
-    for m, good in ((2, True), (1, False)):
+    for m, good in ((pairs.NUMBERS[cache], True), (1, False)):
         codes, scales = fp8.quantize(pairs.multiplied(q, K, V, 128 ** -0.5, dtype, cache, m))
         assert (not fp8.check_codes(codes, scales, o, tau)) == good
+
+
+@pytest.mark.parametrize("dtype,cache", pairs.KINDS)
+def test_one_number_less(dtype, cache):
+    q, k, v = pairs.triples(64, dtype, 3)
+    far = 0
+    for b in range(64):
+        K, V = (pairs.cached(t[b], cache) for t in (k, v))
+        qb = q[b].double().numpy()
+        o, tau = pairs.expect_triple(qb, K, V)
+        y = [pairs.multiplied(qb[None], K, V, 1.0, dtype, cache, pairs.NUMBERS[cache] - m)[0] for m in (0, 1)]
+        check(pairs.rounded(y[0], dtype), o, tau, dtype)
+        try:
+            check(pairs.rounded(y[1], dtype), o, tau, dtype)
+        except AssertionError:
+            far += 1
+    assert far > 8, far

@@ -907,8 +907,8 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     [T][Hq][D] in the inputs' dtype, or with fp8 (D 128) codes [T][Hq * 128] and scales as quantize_fp8 gives them,
     which fp8_linear takes.  workspace: a uint8 device tensor of attention_workspace_bytes bytes (256-byte aligned; few
     queries of many keys need one); by default one is taken from torch's allocator.  precise: the softmax's weights
-    multiply the values as two 16-bit numbers each, as paged_attention's always do, not rounded to one (KQ_FP8_PRECISE
-    in kq.h, with what it gives and costs)."""
+    multiply the values as sums of 16-bit numbers, as paged_attention's always do, with float32's precision, not rounded to
+    one (KQ_FP8_PRECISE in kq.h; what that gives and costs stands beside the formulas there)."""
     if stream is not None:
         return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales, workspace,
                        precise=precise)

@@ -12,8 +12,9 @@
 // multiplied, and the loop has no barrier.  As for prompts everything is transposed:
 // S^T = K Q^T with the key head's queries as 16 columns, O^T += V^T P^T in the order of keys in which the
 // scores came out, V^T by transposing reads.  8-bit rows are widened exactly; their scales go to the scores
-// (keys) and to the weights (values).  The weights are multiplied as the sum of two 16-bit numbers, which
-// costs eight products where there is time for them.
+// (keys) and to the weights (values).  The weights are multiplied as sums of 16-bit numbers, three of bf16 or
+// two of fp16, as exactly as float32 holds them; there is time for the products (one number less: 0 to 0.4 us less a call,
+// but codes further from 64 bits than float32's own, 1 to 2e-4 of the norm and 0.2 to 1e-4).
 //
 // Measured with 32 / 8 heads of 128: 160 sequences of 200 to 8000 in 8 bits (1.28 GB) 239 us, 5.4 TB/s (a copy reaches 5.1);
 // two of 131072 in 8 bits 100 us, 5.3 TB/s; 37 of 50 to 4000 in 16 bits from HBM 56 us, 4.7 TB/s; joins 4 to 7 us.
@@ -202,8 +203,8 @@ __device__ __forceinline__ void cached_8(const uint8_t* row, int i, float* x) {
 }
 
 // One head's sum over the keys [begin, end) of sequence b again, by the definition, one weight and one product a key.  For
-// sums that are not finite: with a weight as the sum of two 16-bit numbers, of which the second may be negative or zero, a
-// value that is infinite comes out as NaN.  Sixteen lanes a head, values d = 8 i .. + 7 in sum; the maximum in m, the sum of
+// sums that are not finite: with a weight as a sum of 16-bit numbers, of which all but the first may be negative or zero,
+// a value that is infinite comes out as NaN.  Sixteen lanes a head, values d = 8 i .. + 7 in sum; the maximum in m, the sum of
 // weights (2^lift larger, as the pieces' are) in l.  Slow, some 70 instructions a key (one infinite value takes a call of 513
 // tokens, 32 / 8 heads of 128, from 12 to 276 us, of 37 sequences of 50 to 4000 from 54 to 847), and small.
 template <bool BF16, bool WIDE>
@@ -267,6 +268,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
   constexpr int KS = DP / 32, DT = DP / 16;
   constexpr int RING = 2 * SLOT;
   constexpr bool PB = BF16 || !WIDE;                         // the weights' 16-bit type
+  constexpr int PARTS = PB ? 3 : 2;                          // of a weight
   constexpr float LIFT = PB ? 0.0f : 6.0f;
   static_assert(PART<DP> * 4 <= SLOT, "a slot takes a wavefront's results");
   __shared__ __align__(1024) uint8_t lds[NW * RING];
@@ -460,14 +462,17 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
         l += pr[e];
         if constexpr (!WIDE) pr[e] *= vscale[e];
       }
-      // a weight is hi + lo, each of 16 bits: relative error 2^-16 (bf16), 2^-22 (fp16; or 2^-31 of the largest, as
-      // they are held 2^LIFT larger, to 2^14 at most)
-      v4u hi, lo;
+      // a weight is a sum of 16-bit numbers: relative error 2^-24 (three of bf16), 2^-22 (two of fp16; or 2^-31 of the
+      // largest, as they are held 2^LIFT larger, to 2^14 at most)
+      v4u wn[PARTS];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        hi[e] = pack2_16<PB>(pr[2 * e], pr[2 * e + 1]);
-        const uint32_t h = hi[e];
-        lo[e] = pack2_16<PB>(pr[2 * e] - unpack1_16<PB>((uint16_t)h), pr[2 * e + 1] - unpack1_16<PB>((uint16_t)(h >> 16)));
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u) {
+          const uint32_t w = pack2_16<PB>(pr[2 * e], pr[2 * e + 1]);
+          wn[u][e] = w;
+          pr[2 * e] -= unpack1_16<PB>((uint16_t)w), pr[2 * e + 1] -= unpack1_16<PB>((uint16_t)(w >> 16));
+        }
       }
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
@@ -482,7 +487,8 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
           const v2u w8 = lds_tr8(sv + PITCH * row + 16 * (i ^ swizzle_v(row)) + 8 * (r & 1));
           v = widen8<true>(w8[0], w8[1]);
         }
-        acc[i] = mfma16<PB>(v, lo, mfma16<PB>(v, hi, acc[i]));
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u) acc[i] = mfma16<PB>(v, wn[u], acc[i]);
       }
       slot ^= 1;
       n[0] = n2[0], n[1] = n2[1];

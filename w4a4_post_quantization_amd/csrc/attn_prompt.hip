@@ -16,8 +16,10 @@
 // The weights are rounded to the 16-bit type for the second product, which keeps it one matrix instruction; 16-bit outputs
 // show little of it (relative error against 64 bits 1.76e-3 bf16, 2.20e-4 fp16; of float32 throughout 1.66e-3 and
 // 2.08e-4), codes fall to the other side of a rounding border here and there (0.6 to 1% of the norm bf16, 0.2% fp16; E4M3
-// itself 2.7%).  PRECISE multiplies a weight as the sum of two 16-bit numbers: 1.66e-3 and 2.08e-4, codes 0.03%; 8192 tokens
-// of 32 / 8 heads of 128 take 693 us and not 495, two images of 4096 with 16 heads of 72 287 and not 204.
+// itself 2.7%).  PRECISE multiplies a weight as a sum of 16-bit numbers, two of fp16 or three of bf16, as exactly as float32
+// holds it: 1.66e-3 and 2.08e-4, codes 0.015 to 0.026% (float32 throughout: 0.017 and 0.023).  8192 tokens of 32 / 8 heads of
+// 128 in bf16 take 938 us so and not 510 (with two numbers 693, codes 0.027%, which is measurably more than float32's), two
+// images of 4096 with 16 heads of 72 in fp16 300 and not 210, 37 tokens 9.6 and not 8.6.
 //
 // A step multiplies the next tile's keys while the present tile's exponentials are taken, and the present
 // tile's values while the next maximum is, so that the matrix cores and the vector units have work of
@@ -89,11 +91,12 @@ __device__ __forceinline__ float add_pair(uint32_t w, float acc) {
 // Scores of masked keys.
 constexpr float HIDDEN = -INFINITY;
 
-// PRECISE: a weight is multiplied as the sum of two 16-bit numbers, else rounded to one.
+// PRECISE: a weight is multiplied as the sum of several 16-bit numbers, else rounded to one.
 template <bool BF16, int KS, int DT, int NW, bool PRECISE>
 struct Prompt {
   static constexpr int QT = 32 * NW;
   static constexpr float LIFT = BF16 ? 0.0f : 6.0f;
+  static constexpr int PARTS = BF16 ? 3 : 2;                         // of a precise weight: 24 or 22 bits
   static constexpr int PITCH = KS <= 4 ? 128 : 256;                  // bytes of a key's row in LDS
   static constexpr int TILE = KT * PITCH;
   static constexpr int LOADS = TILE / (1024 * NW);                   // of a wavefront, a matrix and tile
@@ -150,7 +153,7 @@ struct Prompt {
 
     float base = 0.0f;                                               // m scaled: weights are exp2(x c - base)
     v16f x[2][2];                                                    // scores of a tile, in x[t % 2]
-    v4u p[4], pl[4];                                                 // weights of a tile; what their rounding left
+    v4u p[4];                                                        // weights of a tile (PRECISE: they replace its scores)
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -168,24 +171,37 @@ struct Prompt {
       const v2u lo = lds_tr16(at), hi = lds_tr16(at + 8 * PITCH);
       return v4u{lo[0], lo[1], hi[0], hi[1]};
     };
-    // weights 2 n and 2 n + 1 of the lane's 32; their sum is that of the numbers they are multiplied as (precise: to 2^-16)
-    auto weight_pair = [&](const v16f (&y)[2], int n) {
+    // weights 2 n and 2 n + 1 of the lane's 32; their sum is that of the rounded ones
+    auto weight_pair = [&](v16f (&y)[2], int n) {
       const int h = n >> 3, e = 2 * (n & 7);
       const float p0 = __builtin_amdgcn_exp2f(fmaf(y[h][e], a.c, -base));
       const float p1 = __builtin_amdgcn_exp2f(fmaf(y[h][e + 1], a.c, -base));
-      const uint32_t w = pack2_16<BF16>(p0, p1);
-      p[n >> 2][n & 3] = w;
       if constexpr (PRECISE) {
         l += p0 + p1;
-        pl[n >> 2][n & 3] = pack2_16<BF16>(p0 - unpack1_16<BF16>((uint16_t)w), p1 - unpack1_16<BF16>((uint16_t)(w >> 16)));
+        y[h][e] = p0, y[h][e + 1] = p1;
       } else {
+        const uint32_t w = pack2_16<BF16>(p0, p1);
         l = add_pair<BF16>(w, l);
+        p[n >> 2][n & 3] = w;
+      }
+    };
+    // the weights of contraction step k as sums of PARTS 16-bit numbers, the largest first
+    auto split = [&](const v16f (&y)[2], int k, v4u (&w)[PARTS]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float p0 = y[k >> 1][8 * (k & 1) + 2 * i], p1 = y[k >> 1][8 * (k & 1) + 2 * i + 1];
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u) {
+          const uint32_t r = pack2_16<BF16>(p0, p1);
+          w[u][i] = r;
+          p0 -= unpack1_16<BF16>((uint16_t)r), p1 -= unpack1_16<BF16>((uint16_t)(r >> 16));
+        }
       }
     };
     // The compiler's own order reads each fragment just before its product; these loops keep AHEAD fragments in
     // flight and put a share of the vector work behind each product.  (Heads of 128, 8192 tokens: 512, 497 and 502 us with 2,
-    // 3 and 4; heads of 72 206, 207 and 205; heads of 64 leave registers for a third workgroup with 3; PRECISE leaves heads of
-    // 128 registers for 2.)
+    // 3 and 4; heads of 72 206, 207 and 205; heads of 64 leave registers for a third workgroup with 3; PRECISE spills less with
+    // 2 for heads of 128.)
     constexpr int AHEAD = KS == 5 || KS == 6 ? 4 : PRECISE && KS == 8 ? 2 : 3, NK = 2 * KS, NV = 4 * DT;
     auto scores = [&](v16f (&y)[2], int slot, auto beside) {
       v4u f[NK];
@@ -203,15 +219,20 @@ struct Prompt {
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    auto values = [&](int slot, auto beside) {
-      v4u f[NV];
+    auto values = [&](const v16f (&y)[2], int slot, auto beside) {
+      v4u f[NV], w[PARTS];
 #pragma unroll
       for (int n = 0; n < AHEAD; ++n) f[n] = value_frag(slot, n);
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         if (n + AHEAD < NV) f[n + AHEAD] = value_frag(slot, n + AHEAD);
-        acc[n % DT] = mfma32<BF16>(f[n], p[n / DT], acc[n % DT]);
-        if constexpr (PRECISE) acc[n % DT] = mfma32<BF16>(f[n], pl[n / DT], acc[n % DT]);
+        if constexpr (PRECISE) {
+          if (n % DT == 0) split(y, n / DT, w);
+#pragma unroll
+          for (int u = 0; u < PARTS; ++u) acc[n % DT] = mfma32<BF16>(f[n], w[u], acc[n % DT]);
+        } else {
+          acc[n % DT] = mfma32<BF16>(f[n], p[n / DT], acc[n % DT]);
+        }
 #pragma unroll
         for (int i = 16 * n / NV; i < 16 * (n + 1) / NV; ++i) beside(i);
         __builtin_amdgcn_sched_barrier(0);
@@ -258,11 +279,11 @@ struct Prompt {
       constexpr int S0 = decltype(S)::value, S1 = S0 ^ 1;
       step(t, S0);
       scores(x[S1], S1, [&](int n) { weight_pair(x[S0], n); });
-      asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]));       // here, not behind the branch
-      if constexpr (PRECISE) asm volatile("" : "+v"(pl[0]), "+v"(pl[1]), "+v"(pl[2]), "+v"(pl[3]));
+      if constexpr (PRECISE) asm volatile("" : "+v"(x[S0][0]), "+v"(x[S0][1]));         // here, not behind the branch
+      else asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]));
       hide(x[S1], KT * (t + 1));
       top = HIDDEN;
-      values(S0, [&](int n) { compare(x[S1], n); });
+      values(x[S0], S0, [&](int n) { compare(x[S1], n); });
       raise();
     };
     auto last = [&](int t, auto S) {
@@ -270,7 +291,7 @@ struct Prompt {
       step(t, S0);
 #pragma unroll
       for (int n = 0; n < 16; ++n) weight_pair(x[S0], n);
-      values(S0, [](int) {});
+      values(x[S0], S0, [](int) {});
     };
     const std::integral_constant<int, 0> even;
     const std::integral_constant<int, 1> odd;
@@ -444,8 +465,9 @@ __device__ __forceinline__ int part_begin(int nk, int parts, int z) {
   return (int)min((int64_t)nk, (int64_t)z * per * KT);
 }
 
-// Two workgroups on a compute unit, three or four for narrow heads (64: 4096 tokens, 32 / 8 heads, causal 100 and 92 us); one
-// less where PRECISE's second numbers take the registers.
+// Two workgroups on a compute unit, three or four for narrow heads (64: 4096 tokens, 32 / 8 heads, causal 100 and 92 us).  PRECISE
+// keeps a tile's weights in float32, which takes one away from narrow heads; heads of 128 keep two and spill 11 to 14
+// registers (one without spilling: 1072 us and not 938).
 // PARTS: the keys are split, blockIdx.y says which part is the workgroup's, and what it finds goes to the workspace,
 // unnormalized: values [part][token][head][32 DT], then maxima and sums of weights [part][token][head][2].
 template <bool BF16, int KS, int DT, int NW, bool PARTS, bool PRECISE>

@@ -93,7 +93,7 @@ struct AttnArgs {
 };
 // 0: none needed
 size_t attention_workspace_bytes(int64_t B, int64_t T, int64_t Tk, bool packed, int Hq, int Hkv, int D);
-// precise: weights as the sum of two 16-bit numbers
+// precise: weights as sums of 16-bit numbers, with float32's precision
 hipError_t launch_attention(bool bf16, bool precise, const AttnArgs& a, hipStream_t s);
 
 // Pages of keys and values: head h's row r of a page at ((page * Hkv + h) * page_rows + r) * row bytes;
