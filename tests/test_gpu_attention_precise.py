@@ -97,3 +97,18 @@ def test_captured_and_given_stream(kq):
         side = kq.attention(Q, K, V, cu, precise=True, stream=torch.cuda.Stream())
         torch.cuda.synchronize()
         assert np.array_equal(raw(O), raw(ref)) and np.array_equal(raw(side), raw(ref))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,Tk", [(150, 150), (6, 2000)])
+def test_default(kq, dtype, T, Tk):
+    """Codes are precise unless the caller says otherwise, 16-bit outputs only if it does."""
+    Q, (K, V) = heads((T, 4, 128), dtype, 60), (t.cuda() for t in pairs.rows(Tk, 2, 128, dtype, dtype, 61))
+    o, tau = _expect(Q, K, V, [0, T], [0, Tk], True, dtype)
+    codes, scales = kq.attention(Q, K, V, fp8=True)
+    check_codes(codes, scales, o, tau)
+    for a, b in zip((codes, scales), kq.attention(Q, K, V, fp8=True, precise=True)):
+        assert np.array_equal(raw(a), raw(b))
+    assert not np.array_equal(raw(codes), raw(kq.attention(Q, K, V, fp8=True, precise=False)[0]))
+    assert np.array_equal(raw(kq.attention(Q, K, V)), raw(kq.attention(Q, K, V, precise=False)))
+    assert not np.array_equal(raw(kq.attention(Q, K, V)), raw(kq.attention(Q, K, V, precise=True)))

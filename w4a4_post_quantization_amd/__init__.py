@@ -896,7 +896,7 @@ def _workspace(torch, workspace, index, need, *sizes):
 
 
 def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False, O=None, codes=None, scales=None,
-              workspace=None, stream=None, precise=False):
+              workspace=None, stream=None, precise=None):
     """Attention of packed sequences.  Q [T][Hq][D], K and V [Tk][Hkv][D], fp16 or bf16, Hq a multiple of Hkv (head h
     reads key head h Hkv // Hq), D a multiple of 8 up to 128; any strides that are multiples of 8 (the values
     of a row next to each other), so views of a projection's output serve.  cu_q, cu_k (int32 [B + 1]): where each
@@ -907,12 +907,15 @@ def attention(Q, K, V, cu_q=None, cu_k=None, causal=True, scale=None, fp8=False,
     [T][Hq][D] in the inputs' dtype, or with fp8 (D 128) codes [T][Hq * 128] and scales as quantize_fp8 gives them,
     which fp8_linear takes.  workspace: a uint8 device tensor of attention_workspace_bytes bytes (256-byte aligned; few
     queries of many keys need one); by default one is taken from torch's allocator.  precise: the softmax's weights
-    multiply the values as sums of 16-bit numbers, as paged_attention's always do, with float32's precision, not rounded to
-    one (KQ_FP8_PRECISE in kq.h; what that gives and costs stands beside the formulas there)."""
+    multiply the values as sums of 16-bit numbers, as paged_attention's always do, with float32's precision; False: rounded
+    to one, which 16-bit outputs hide and codes show, and which takes 0.5 to 0.9 of the time (KQ_FP8_PRECISE in kq.h).
+    Default: precise with fp8, else not."""
     if stream is not None:
         return _on_fp8(stream, Q, attention, K, V, cu_q, cu_k, causal, scale, fp8, O, codes, scales, workspace,
                        precise=precise)
     torch = _torch()
+    if precise is None:
+        precise = fp8
     shape = T, Hq, D = _heads3(torch, Q, "Q")
     Tk, Hkv, _ = _heads3(torch, K, "K")
     dtype, index = Q.dtype, Q.get_device()
