@@ -401,7 +401,7 @@ kq_status kq_fp8_gated_linear(int32_t act, const uint8_t* xcodes, const uint8_t*
  * moves 16-bit outputs by less than their own rounding, and codes by 0.2 to 1% of the norm (E4M3 itself 2.7%).
  * kq_paged_attention, and kq_attention with KQ_FP8_PRECISE or'ed into its dtype, multiply it as a sum of 16-bit
  * numbers: two of fp16 (2^-22) for fp16 keys and values, else three of bf16 (2^-24); codes are then as near 64 bits as
- * with float32 throughout (0.02% of the norm).  Prompts take 1.2 to 1.9 times as long so.  What a weight loses besides is below 2^-31 of the largest (fp16) or 2^-125; one that
+ * with float32 throughout (0.02% of the norm).  Prompts take 1.1 to 1.9 times as long so.  What a weight loses besides is below 2^-31 of the largest (fp16) or 2^-125; one that
  * vanishes makes NaN of an infinite value.  Sums are divided by the weights' sum at the end, so values beyond 10^30
  * may overflow.  The order of additions is fixed for one device: equal inputs of equal shape give equal bits.
  *

@@ -16,8 +16,8 @@
 // two of fp16, as exactly as float32 holds them; there is time for the products (one number less: 0 to 0.4 us less a call,
 // but codes further from 64 bits than float32's own, 1 to 2e-4 of the norm and 0.2 to 1e-4).
 //
-// Measured with 32 / 8 heads of 128: 160 sequences of 200 to 8000 in 8 bits (1.28 GB) 239 us, 5.4 TB/s (a copy reaches 5.1);
-// two of 131072 in 8 bits 100 us, 5.3 TB/s; 37 of 50 to 4000 in 16 bits from HBM 56 us, 4.7 TB/s; joins 4 to 7 us.
+// Measured with 32 / 8 heads of 128: 160 sequences of 200 to 8000 in 8 bits (1.28 GB) 241 us, 5.3 TB/s (a copy reaches 5.1);
+// two of 131072 in 8 bits 103 us, 5.2 TB/s; 37 of 50 to 4000 in 16 bits from HBM 56 us, 4.7 TB/s; joins 4 to 7 us.
 #include "kq_attn.hpp"
 #include "kq_launch.hpp"
 

@@ -24,8 +24,8 @@
 // A step multiplies the next tile's keys while the present tile's exponentials are taken, and the present
 // tile's values while the next maximum is, so that the matrix cores and the vector units have work of
 // the same wavefront side by side.
-// Long prompts are bound by the chip's power: 8192 tokens, 32 / 8 heads of 128, causal, bf16 take 498 to 529 us (1.04 to
-// 1.10 PFLOP/s; a library product of 8192^3 1.41) with the matrix cores 63% busy at 1.54 GHz, so what is left
+// Long prompts are bound by the chip's power: 8192 tokens, 32 / 8 heads of 128, causal, bf16 take 495 to 546 us (1.01 to
+// 1.11 PFLOP/s; a library product of 8192^3 1.41) with the matrix cores 63% busy at 1.54 GHz, so what is left
 // out counts more than what is hidden: of that time exponentials have 5%, the fragments' LDS reads 11%, the tiles' loads
 // 6 to 8%, barriers 1%.  Short ones are bound by latency: 37 tokens 8.4 us, of which a launch and three loads in turn.
 #include "kq_attn.hpp"
