@@ -268,7 +268,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
   constexpr int KS = DP / 32, DT = DP / 16;
   constexpr int RING = 2 * SLOT;
   constexpr bool PB = BF16 || !WIDE;                         // the weights' 16-bit type
-  constexpr int PARTS = PB ? 3 : 2;                          // of a weight
+  constexpr int NUMBERS = PB ? 3 : 2;                          // of a weight
   constexpr float LIFT = PB ? 0.0f : 6.0f;
   static_assert(PART<DP> * 4 <= SLOT, "a slot takes a wavefront's results");
   __shared__ __align__(1024) uint8_t lds[NW * RING];
@@ -464,11 +464,11 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
       }
       // a weight is a sum of 16-bit numbers: relative error 2^-24 (three of bf16), 2^-22 (two of fp16; or 2^-31 of the
       // largest, as they are held 2^LIFT larger, to 2^14 at most)
-      v4u wn[PARTS];
+      v4u wn[NUMBERS];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
 #pragma unroll
-        for (int u = 0; u < PARTS; ++u) {
+        for (int u = 0; u < NUMBERS; ++u) {
           const uint32_t w = pack2_16<PB>(pr[2 * e], pr[2 * e + 1]);
           wn[u][e] = w;
           pr[2 * e] -= unpack1_16<PB>((uint16_t)w), pr[2 * e + 1] -= unpack1_16<PB>((uint16_t)(w >> 16));
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(64 * NW, RES) void paged_kernel(PagedArgs a, int W)
           v = widen8<true>(w8[0], w8[1]);
         }
 #pragma unroll
-        for (int u = 0; u < PARTS; ++u) acc[i] = mfma16<PB>(v, wn[u], acc[i]);
+        for (int u = 0; u < NUMBERS; ++u) acc[i] = mfma16<PB>(v, wn[u], acc[i]);
       }
       slot ^= 1;
       n[0] = n2[0], n[1] = n2[1];

@@ -96,7 +96,7 @@ template <bool BF16, int KS, int DT, int NW, bool PRECISE>
 struct Prompt {
   static constexpr int QT = 32 * NW;
   static constexpr float LIFT = BF16 ? 0.0f : 6.0f;
-  static constexpr int PARTS = BF16 ? 3 : 2;                         // of a precise weight: 24 or 22 bits
+  static constexpr int NUMBERS = BF16 ? 3 : 2;                         // of a precise weight: 24 or 22 bits
   static constexpr int PITCH = KS <= 4 ? 128 : 256;                  // bytes of a key's row in LDS
   static constexpr int TILE = KT * PITCH;
   static constexpr int LOADS = TILE / (1024 * NW);                   // of a wavefront, a matrix and tile
@@ -185,13 +185,13 @@ struct Prompt {
         p[n >> 2][n & 3] = w;
       }
     };
-    // the weights of contraction step k as sums of PARTS 16-bit numbers, the largest first
-    auto split = [&](const v16f (&y)[2], int k, v4u (&w)[PARTS]) {
+    // the weights of contraction step k as sums of NUMBERS 16-bit numbers, the largest first
+    auto split = [&](const v16f (&y)[2], int k, v4u (&w)[NUMBERS]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float p0 = y[k >> 1][8 * (k & 1) + 2 * i], p1 = y[k >> 1][8 * (k & 1) + 2 * i + 1];
 #pragma unroll
-        for (int u = 0; u < PARTS; ++u) {
+        for (int u = 0; u < NUMBERS; ++u) {
           const uint32_t r = pack2_16<BF16>(p0, p1);
           w[u][i] = r;
           p0 -= unpack1_16<BF16>((uint16_t)r), p1 -= unpack1_16<BF16>((uint16_t)(r >> 16));
@@ -220,7 +220,7 @@ struct Prompt {
       }
     };
     auto values = [&](const v16f (&y)[2], int slot, auto beside) {
-      v4u f[NV], w[PARTS];
+      v4u f[NV], w[NUMBERS];
 #pragma unroll
       for (int n = 0; n < AHEAD; ++n) f[n] = value_frag(slot, n);
 #pragma unroll
@@ -229,7 +229,7 @@ struct Prompt {
         if constexpr (PRECISE) {
           if (n % DT == 0) split(y, n / DT, w);
 #pragma unroll
-          for (int u = 0; u < PARTS; ++u) acc[n % DT] = mfma32<BF16>(f[n], w[u], acc[n % DT]);
+          for (int u = 0; u < NUMBERS; ++u) acc[n % DT] = mfma32<BF16>(f[n], w[u], acc[n % DT]);
         } else {
           acc[n % DT] = mfma32<BF16>(f[n], p[n / DT], acc[n % DT]);
         }
